@@ -377,6 +377,101 @@ size_t muon_adamw_workspace_bytes(int32_t n);
 int muon_adamw_step(const muon_vec* params, const muon_vec* grads, muon_adamw_state* st,
                     const muon_adamw_hparams* hp, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 4-bit operators for training and serving with the weights that the step
+ * keeps: quantisation to microscaled 4-bit blocks (the OCP MXFP4 element and
+ * scale encodings), reading back, products, and dropout.
+ *
+ * Number format.  Blocks of 32 consecutive elements along a row (the
+ * contraction index of the products; the last block of a row may be shorter)
+ * share a scale 2^e, e the smallest integer >= -127 for which no element of
+ * the block exceeds 6 * 2^e in magnitude.  An element is a sign and one of
+ * {0, 0.5, 1, 1.5, 2, 3, 4, 6} times the scale.  Rounding is to nearest, ties
+ * to the even code, or stochastic: up where 256 times the fraction of the step
+ * exceeds the element's random byte plus 1/2, so with the probability of the
+ * fraction in steps of 1/256.  No element saturates, so stochastic rounding
+ * has no bias beyond that step.  A block that holds an infinity or a NaN reads
+ * back as NaN and makes the sums it enters NaN.  Zeros keep their sign.
+ *
+ * Random numbers are those of Philox 4x32 with ten rounds, keyed by a 64-bit
+ * seed, so a mask or a rounding is a function of the seed and the element's
+ * place and is never stored.  Counter words: the group of consecutive elements
+ * in its row, the row, what the numbers are for, the matrix's place in the
+ * list.  Dropout ("DROP") takes 16 bits an element, eight elements a group;
+ * rounding takes 8 bits an element, 16 elements of the output's row a group
+ * ("SR40" for the matrix, "SR41" for its transpose; tags as big-endian bytes).
+ * Words serve elements from the first word's low bits upwards.
+ * A seed is given by value or, where the *_dev pointer is not NULL, by the
+ * device address of one (8-byte aligned), read when the kernel runs: a
+ * replayed graph repeats its numbers unless that memory changes.
+ *
+ * All matrices of one call may have different shapes, zero rows or columns
+ * included, and share one element type.  The matrices here need only the
+ * alignment of their elements (16-byte aligned rows are faster).  Nothing a
+ * call writes may overlap anything else that it reads or writes
+ * (MUON_E_ALIAS); column slices of one buffer do not overlap.  Calls keep no
+ * state, use no workspace and may run under stream capture, from several host
+ * threads at once. */
+
+/* A rows x cols matrix in 4 bits.  The buffers are the caller's, 16-byte
+ * aligned, of muon_mx_codes_bytes and muon_mx_scales_bytes bytes (NULL allowed
+ * when rows or cols is 0).  Their layout is the order in which the matrix
+ * instructions read them (csrc/muon_mx.h); it is not row-major.
+ * rows <= 2^30, cols <= 2^24. */
+typedef struct {
+  void*   codes;
+  void*   scales;
+  int64_t rows;
+  int64_t cols;
+} muon_mx;
+
+/* Options of the 4-bit operators; muon_mx_default_options() zeroes them, and
+ * a NULL pointer stands for the defaults. */
+typedef struct {
+  int32_t  stochastic;       /* quantise: 1 rounds stochastically (seed)         */
+  int32_t  accumulate;       /* matmul: out += product (fp32 sum)                */
+  float    dropout;          /* in [0,1), taken in steps of 2^-16; see below     */
+  int32_t  _pad;
+  uint64_t seed;
+  uint64_t dropout_seed;
+  const uint64_t* seed_dev;
+  const uint64_t* dropout_seed_dev;
+} muon_mx_options;
+
+void muon_mx_default_options(muon_mx_options* opt);
+
+/* Bytes of the two buffers of a 4-bit matrix; 0 for an invalid shape (and for
+ * an empty matrix). */
+size_t muon_mx_codes_bytes(int64_t rows, int64_t cols);
+size_t muon_mx_scales_bytes(int64_t rows, int64_t cols);
+
+/* out[i] = in[i] in 4 bits, out_t[i] = its transpose in 4 bits (blocks along
+ * the rows of in[i], for products that contract over them); one of the arrays
+ * may be NULL.  Both come from one read of in[i].  With opt->dropout the
+ * values that muon_dropout would store are quantised (its mask for the place i
+ * in the list). */
+int muon_mx_quantize(const muon_mat* in, const muon_mx* out, const muon_mx* out_t, int32_t n,
+                     const muon_mx_options* opt, void* stream);
+
+/* out[i] = the values that in[i] stands for (exact, but for bf16 or fp32
+ * overflow of a block at the top of the fp32 range). */
+int muon_mx_dequantize(const muon_mx* in, const muon_mat* out, int32_t n, void* stream);
+
+/* out[i] = a[i] b[i]^T (M x K times N x K), fp32 accumulation, rounded once to
+ * out's type; K = 0 gives zeros.  With opt->accumulate the product is added to
+ * out in fp32 first.  With opt->dropout the product's elements are dropped or
+ * scaled as muon_dropout does (the gradient of a dropped-out input), before
+ * any accumulation. */
+int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int32_t n,
+                   const muon_mx_options* opt, void* stream);
+
+/* out = in with each element kept with probability 1 - p and multiplied by
+ * 1 / (1 - p), or set to zero (p taken in steps of 2^-16; p that rounds to 1
+ * is refused).  The same call on a gradient is the backward pass.  out may be
+ * in itself. */
+int muon_dropout(const muon_mat* in, const muon_mat* out, float p, uint64_t seed,
+                 const uint64_t* seed_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -3,7 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_uint8, c_void_p
+from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_uint8, c_uint64, c_void_p
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 # MUON_LIB_PATH selects another build of the same library (the host-sanitised
@@ -59,6 +59,16 @@ class AdamWState(ctypes.Structure):
     _fields_ = [("n", c_int32), ("_pad", c_int32), ("m", POINTER(c_void_p)),
                 ("v", POINTER(c_void_p)), ("workspace", c_void_p),
                 ("workspace_bytes", c_size_t), ("step", c_int64)]
+
+
+class MuonMX(ctypes.Structure):
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("rows", c_int64), ("cols", c_int64)]
+
+
+class MXOptions(ctypes.Structure):
+    _fields_ = [("stochastic", c_int32), ("accumulate", c_int32), ("dropout", c_float),
+                ("_pad", c_int32), ("seed", c_uint64), ("dropout_seed", c_uint64),
+                ("seed_dev", c_void_p), ("dropout_seed_dev", c_void_p)]
 
 
 class MuonError(RuntimeError):
@@ -119,6 +129,22 @@ def load() -> ctypes.CDLL:
     lib.muon_adamw_step.argtypes = [P(MuonVec), P(MuonVec), P(AdamWState), P(AdamWHparams),
                                     c_void_p]
     lib.muon_adamw_step.restype = c_int32
+    lib.muon_mx_default_options.argtypes = [P(MXOptions)]
+    lib.muon_mx_default_options.restype = None
+    lib.muon_mx_codes_bytes.argtypes = [c_int64, c_int64]
+    lib.muon_mx_codes_bytes.restype = c_size_t
+    lib.muon_mx_scales_bytes.argtypes = [c_int64, c_int64]
+    lib.muon_mx_scales_bytes.restype = c_size_t
+    lib.muon_mx_quantize.argtypes = [P(MuonMat), P(MuonMX), P(MuonMX), c_int32, P(MXOptions),
+                                     c_void_p]
+    lib.muon_mx_quantize.restype = c_int32
+    lib.muon_mx_dequantize.argtypes = [P(MuonMX), P(MuonMat), c_int32, c_void_p]
+    lib.muon_mx_dequantize.restype = c_int32
+    lib.muon_mx_matmul.argtypes = [P(MuonMX), P(MuonMX), P(MuonMat), c_int32, P(MXOptions),
+                                   c_void_p]
+    lib.muon_mx_matmul.restype = c_int32
+    lib.muon_dropout.argtypes = [P(MuonMat), P(MuonMat), c_float, c_uint64, c_void_p, c_void_p]
+    lib.muon_dropout.restype = c_int32
     _LIB = lib
     return lib
 

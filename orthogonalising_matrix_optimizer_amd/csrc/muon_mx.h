@@ -1,0 +1,126 @@
+// Shared host/device definitions of the 4-bit (MXFP4) operators and dropout.
+//
+// Storage of a rows x cols matrix (blocks of 32 along the columns, the
+// contraction index of every product):
+//   codes : tiles of 16 rows x 128 columns, 1 KiB each, tile (r / 16, k / 128)
+//           at ((r / 16) * K + k / 128) * 1024 for K = ceil(cols / 128).  Inside
+//           a tile the 16 bytes of the block (r % 16, (k % 128) / 32) are at
+//           16 * (16 * ((k % 128) / 32) + r % 16): 16 consecutive bytes per lane
+//           in the order in which a wave feeds v_mfma_scale_f32_16x16x128_f8f6f4,
+//           so a tile is one contiguous load and one conflict-free LDS read.
+//   scales: one byte per block; a dword holds the four row tiles of 64 rows:
+//           byte ((r / 64) * K + k / 128) * 256 + 4 * (16 * ((k % 128) / 32)
+//           + r % 16) + (r % 64) / 16, so one dword per lane serves four MFMA
+//           operands, which pick their byte by an immediate.
+// Blocks past the last column have zero codes and an ordinary scale; rows past
+// the last row of a tile are never stored from any product, and may hold anything.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace muon {
+
+constexpr int kMxBlock = 32;       // elements that share a scale
+constexpr int kMxTileR = 16;       // rows of a code tile
+constexpr int kMxTileK = 128;      // columns of a code tile
+constexpr int kMxTileBytes = 1024;
+constexpr int kMxScaleRows = 64;   // rows of a scale tile (256 bytes)
+constexpr int kMxScaleBytes = 256;
+constexpr uint32_t kMxNan = 255;   // scale byte of a block that is NaN
+
+// third counter word of the generator: what the numbers are for
+constexpr uint32_t kTagDropout = 0x44524F50u, kTagRound = 0x53523430u, kTagRoundT = 0x53523431u;
+
+// Descriptors travel as kernel arguments (under the 4 KiB limit), so the calls
+// need no device table, no workspace for one and no staging memory.
+constexpr int kMxMaxList = 40;
+
+// A seed given by value, or by the device address of one (then read by the
+// kernel: a replayed graph can be given new numbers).
+struct MxSeed {
+  uint64_t value;
+  const uint64_t* dev;   // or null
+};
+
+struct MxQuantMat {
+  const void* in;        // rows x cols, row pitch ld elements
+  uint8_t* codes;        // the matrix in 4 bits, or null
+  uint8_t* scales;
+  uint8_t* codes_t;      // its transpose in 4 bits, or null
+  uint8_t* scales_t;
+  int64_t ld;
+  int32_t rows, cols;
+  int32_t vec;           // rows allow 16-byte access
+  int32_t index;         // place in the caller's list (fourth counter word)
+};
+struct MxQuantArgs {
+  MxQuantMat m[kMxMaxList];
+  uint32_t base[kMxMaxList];   // first block of each matrix
+  int32_t n;
+  uint32_t drop;               // dropout threshold in steps of 2^-16, 0: none
+  float drop_scale;
+  MxSeed seed;                 // stochastic rounding
+  MxSeed drop_seed;
+};
+
+struct MxDequantMat {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  void* out;
+  int64_t ld;
+  int32_t rows, cols;
+  int32_t vec;
+  int32_t _pad;
+};
+struct MxDequantArgs {
+  MxDequantMat m[kMxMaxList];
+  uint32_t base[kMxMaxList];
+  int32_t n;
+  int32_t _pad;
+};
+
+// out (M x N) = a (M x K) * b (N x K)^T
+struct MxProduct {
+  const uint8_t* ac;
+  const uint8_t* as;
+  const uint8_t* bc;
+  const uint8_t* bs;
+  void* out;
+  int64_t ld;
+  int32_t M, N;
+  int32_t kt;              // code tiles along the contraction
+  int32_t index;           // place in the caller's list
+};
+struct MxGemmArgs {
+  MxProduct p[kMxMaxList];
+  uint32_t base[kMxMaxList];
+  int32_t n;
+  int32_t accumulate;      // out += product
+  uint32_t drop;
+  float drop_scale;
+  MxSeed drop_seed;
+};
+
+struct MxDropArgs {
+  const void* in;
+  void* out;
+  int64_t ldi, ldo;
+  int32_t rows, cols;
+  int32_t vec;             // both rows allow 16-byte access
+  uint32_t drop;
+  float scale;
+  int32_t _pad;
+  MxSeed seed;
+};
+
+hipError_t launch_mx_quantize(const MxQuantArgs& a, int dt, bool rows, bool cols, bool stochastic,
+                              int64_t blocks, hipStream_t s);
+hipError_t launch_mx_dequantize(const MxDequantArgs& a, int dt, int64_t blocks, hipStream_t s);
+hipError_t launch_mx_gemm(const MxGemmArgs& a, int odt, int tile, int64_t blocks, hipStream_t s);
+hipError_t launch_dropout(const MxDropArgs& a, int dt, int64_t blocks, hipStream_t s);
+
+// Work of one block of each kernel (the host sizes the grids with these).
+constexpr int kMxQuantTile = 128;              // quantise, dequantise: square tile edge
+constexpr int kDropItems = 1024;               // dropout: groups of 8 elements per block
+
+}  // namespace muon
