@@ -410,8 +410,8 @@ int muon_adamw_step(const muon_vec* params, const muon_vec* grads, muon_adamw_st
  * alignment of their elements (16-byte aligned rows are faster).  Nothing a
  * call writes may overlap anything else that it reads or writes
  * (MUON_E_ALIAS); column slices of one buffer do not overlap.  Calls keep no
- * state, use no workspace and may run under stream capture, from several host
- * threads at once. */
+ * state and may run under stream capture and from several host threads at
+ * once; only muon_mx_matmul takes a workspace. */
 
 /* A rows x cols matrix in 4 bits.  The buffers are the caller's, 16-byte
  * aligned, of muon_mx_codes_bytes and muon_mx_scales_bytes bytes (NULL allowed
@@ -461,9 +461,21 @@ int muon_mx_dequantize(const muon_mx* in, const muon_mat* out, int32_t n, void* 
  * out's type; K = 0 gives zeros.  With opt->accumulate the product is added to
  * out in fp32 first.  With opt->dropout the product's elements are dropped or
  * scaled as muon_dropout does (the gradient of a dropped-out input), before
- * any accumulation. */
+ * any accumulation.  Long contractions with few output tiles are split and
+ * their fp32 partial products summed in a fixed order: the caller's workspace
+ * (16-byte aligned) holds them during the call's work on the stream, of
+ * muon_mx_matmul_workspace_bytes bytes, which is 0 for lists that are not
+ * split (workspace may then be NULL); MUON_E_WORKSPACE if it is smaller. */
+size_t muon_mx_matmul_workspace_bytes(const muon_mx* a, const muon_mx* b, int32_t n);
 int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int32_t n,
-                   const muon_mx_options* opt, void* stream);
+                   const muon_mx_options* opt, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* out = x b^T for at most MUON_MX_FEW_ROWS rows of x that are not in 4 bits yet
+ * (the layer of single tokens): x is quantised to nearest in the same launch,
+ * with the codes of muon_mx_quantize.  out has any element type. */
+#define MUON_MX_FEW_ROWS 16
+int muon_mx_matmul_rows(const muon_mat* x, const muon_mx* b, const muon_mat* out, void* stream);
 
 /* out = in with each element kept with probability 1 - p and multiplied by
  * 1 / (1 - p), or set to zero (p taken in steps of 2^-16; p that rounds to 1

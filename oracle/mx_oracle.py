@@ -114,19 +114,19 @@ def dropout(x: np.ndarray, p: float, seed: int, index: int = 0) -> np.ndarray:
 
 def storage(code, sign, byte):
     """Codes and scale bytes in the tiled storage order (muon_mx layout):
-    (codes uint8 [row tiles, k tiles, 1024], scales uint8 [row tiles of 64, k
-    tiles, 256], scales' valid mask)."""
+    (codes uint8 [k tiles, row tiles, 1024], scales uint8 [k tiles, row tiles
+    of 64, 256], scales' valid mask)."""
     rows, nb = byte.shape
     rt, kt, st = -(-rows // 16), -(-nb // 4), -(-rows // 64)
-    codes = np.zeros((rt, kt, 4, 16, 16), np.uint8)
-    scales = np.zeros((st, kt, 4, 16, 4), np.uint8)
+    codes = np.zeros((kt, rt, 4, 16, 16), np.uint8)
+    scales = np.zeros((kt, st, 4, 16, 4), np.uint8)
     valid = np.zeros(scales.shape, bool)
     nib = (code + 8 * sign).astype(np.uint8)
     nib[byte == NAN_BYTE] = 0
     packed = nib[..., 0::2] | (nib[..., 1::2] << 4)
     for r in range(rows):
         for b in range(nb):
-            codes[r // 16, b // 4, b % 4, r % 16] = packed[r, b]
-            scales[r // 64, b // 4, b % 4, r % 16, r % 64 // 16] = byte[r, b]
-            valid[r // 64, b // 4, b % 4, r % 16, r % 64 // 16] = True
-    return codes.reshape(rt, kt, 1024), scales.reshape(st, kt, 256), valid.reshape(st, kt, 256)
+            codes[b // 4, r // 16, b % 4, r % 16] = packed[r, b]
+            scales[b // 4, r // 64, b % 4, r % 16, r % 64 // 16] = byte[r, b]
+            valid[b // 4, r // 64, b % 4, r % 16, r % 64 // 16] = True
+    return codes.reshape(kt, rt, 1024), scales.reshape(kt, st, 256), valid.reshape(kt, st, 256)

@@ -23,6 +23,7 @@ PHASES = {"prepare": 0, "gram": 1, "poly": 2, "apply": 3, "finish": 4, "adamw": 
           "apply_update": 6, "ns_single": 7}
 MAX_STEPS = 16
 NOALLOC_SCRATCH_BYTES = 64 << 20
+MX_FEW_ROWS = 16
 
 
 class MuonMat(ctypes.Structure):
@@ -135,15 +136,19 @@ def load() -> ctypes.CDLL:
     lib.muon_mx_codes_bytes.restype = c_size_t
     lib.muon_mx_scales_bytes.argtypes = [c_int64, c_int64]
     lib.muon_mx_scales_bytes.restype = c_size_t
-    lib.muon_mx_quantize.argtypes = [P(MuonMat), P(MuonMX), P(MuonMX), c_int32, P(MXOptions),
-                                     c_void_p]
+    # the 4-bit operators' descriptor arrays are passed as packed bytes
+    V = c_void_p
+    lib.muon_mx_quantize.argtypes = [V, V, V, c_int32, P(MXOptions), V]
     lib.muon_mx_quantize.restype = c_int32
-    lib.muon_mx_dequantize.argtypes = [P(MuonMX), P(MuonMat), c_int32, c_void_p]
+    lib.muon_mx_dequantize.argtypes = [V, V, c_int32, V]
     lib.muon_mx_dequantize.restype = c_int32
-    lib.muon_mx_matmul.argtypes = [P(MuonMX), P(MuonMX), P(MuonMat), c_int32, P(MXOptions),
-                                   c_void_p]
+    lib.muon_mx_matmul_workspace_bytes.argtypes = [V, V, c_int32]
+    lib.muon_mx_matmul_workspace_bytes.restype = c_size_t
+    lib.muon_mx_matmul.argtypes = [V, V, V, c_int32, P(MXOptions), V, c_size_t, V]
     lib.muon_mx_matmul.restype = c_int32
-    lib.muon_dropout.argtypes = [P(MuonMat), P(MuonMat), c_float, c_uint64, c_void_p, c_void_p]
+    lib.muon_mx_matmul_rows.argtypes = [V, V, V, V]
+    lib.muon_mx_matmul_rows.restype = c_int32
+    lib.muon_dropout.argtypes = [V, V, c_float, c_uint64, V, V]
     lib.muon_dropout.restype = c_int32
     _LIB = lib
     return lib

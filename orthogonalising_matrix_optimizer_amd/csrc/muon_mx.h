@@ -3,15 +3,18 @@
 // Storage of a rows x cols matrix (blocks of 32 along the columns, the
 // contraction index of every product):
 //   codes : tiles of 16 rows x 128 columns, 1 KiB each, tile (r / 16, k / 128)
-//           at ((r / 16) * K + k / 128) * 1024 for K = ceil(cols / 128).  Inside
-//           a tile the 16 bytes of the block (r % 16, (k % 128) / 32) are at
-//           16 * (16 * ((k % 128) / 32) + r % 16): 16 consecutive bytes per lane
-//           in the order in which a wave feeds v_mfma_scale_f32_16x16x128_f8f6f4,
-//           so a tile is one contiguous load and one conflict-free LDS read.
+//           at ((k / 128) * R + r / 16) * 1024 for R = ceil(rows / 16): the
+//           tiles of a row panel and one step along the contraction are
+//           contiguous, so the panels that many blocks read at once spread
+//           over all L2 channels.  Inside a tile the 16 bytes of the block
+//           (r % 16, (k % 128) / 32) are at 16 * (16 * ((k % 128) / 32) + r % 16):
+//           16 consecutive bytes per lane in the order in which a wave feeds
+//           v_mfma_scale_f32_16x16x128_f8f6f4, so a tile is one contiguous
+//           load and one conflict-free LDS read.
 //   scales: one byte per block; a dword holds the four row tiles of 64 rows:
-//           byte ((r / 64) * K + k / 128) * 256 + 4 * (16 * ((k % 128) / 32)
-//           + r % 16) + (r % 64) / 16, so one dword per lane serves four MFMA
-//           operands, which pick their byte by an immediate.
+//           byte ((k / 128) * ceil(rows / 64) + r / 64) * 256 + 4 * (16 *
+//           ((k % 128) / 32) + r % 16) + (r % 64) / 16, so one dword per lane
+//           serves four MFMA operands, which pick their byte by an immediate.
 // Blocks past the last column have zero codes and an ordinary scale; rows past
 // the last row of a tile are never stored from any product, and may hold anything.
 #pragma once
@@ -33,7 +36,7 @@ constexpr uint32_t kTagDropout = 0x44524F50u, kTagRound = 0x53523430u, kTagRound
 
 // Descriptors travel as kernel arguments (under the 4 KiB limit), so the calls
 // need no device table, no workspace for one and no staging memory.
-constexpr int kMxMaxList = 40;
+constexpr int kMxMaxList = 36;
 
 // A seed given by value, or by the device address of one (then read by the
 // kernel: a replayed graph can be given new numbers).
@@ -79,7 +82,8 @@ struct MxDequantArgs {
   int32_t _pad;
 };
 
-// out (M x N) = a (M x K) * b (N x K)^T
+// out (M x N) = a (M x K) * b (N x K)^T, or with a split contraction the
+// partial products over `chunk` code tiles each, `stride` elements apart
 struct MxProduct {
   const uint8_t* ac;
   const uint8_t* as;
@@ -87,15 +91,42 @@ struct MxProduct {
   const uint8_t* bs;
   void* out;
   int64_t ld;
+  int64_t stride;
   int32_t M, N;
   int32_t kt;              // code tiles along the contraction
+  int32_t chunk;           // ... of one work item
+  int32_t tiles;           // output tiles; item = split * tiles + tile
   int32_t index;           // place in the caller's list
 };
 struct MxGemmArgs {
   MxProduct p[kMxMaxList];
+  uint32_t base[kMxMaxList];   // first work item of each product
+  int32_t n;
+  int32_t items;           // work items of the launch
+  int32_t accumulate;      // out += product
+  int32_t vec;             // every out allows 16-byte access
+  uint32_t drop;
+  float drop_scale;
+  MxSeed drop_seed;
+};
+
+// out (M x N) = sum over the splits of the partial products (fp32, row pitch
+// ldp, `stride` elements apart)
+struct MxReduce {
+  const float* in;
+  void* out;
+  int64_t ld;
+  int64_t stride;
+  int32_t M, N, ldp;
+  int32_t splits;
+  int32_t vec;
+  int32_t index;
+};
+struct MxReduceArgs {
+  MxReduce p[kMxMaxList];
   uint32_t base[kMxMaxList];
   int32_t n;
-  int32_t accumulate;      // out += product
+  int32_t accumulate;
   uint32_t drop;
   float drop_scale;
   MxSeed drop_seed;
@@ -113,10 +144,24 @@ struct MxDropArgs {
   MxSeed seed;
 };
 
+// out (M x N) = x (M x K, not in 4 bits) * b (N x K)^T, M <= 16
+struct MxRowsArgs {
+  const void* x;
+  const uint8_t* bc;
+  const uint8_t* bs;
+  void* out;
+  int64_t ldx, ldo;
+  int32_t M, N, K;
+  int32_t vec;             // rows of x allow 16-byte access
+};
+
 hipError_t launch_mx_quantize(const MxQuantArgs& a, int dt, bool rows, bool cols, bool stochastic,
                               int64_t blocks, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxDequantArgs& a, int dt, int64_t blocks, hipStream_t s);
-hipError_t launch_mx_gemm(const MxGemmArgs& a, int odt, int tile, int64_t blocks, hipStream_t s);
+// tile_m: rows of the output tiles (256 or 128; always 128 columns)
+hipError_t launch_mx_gemm(const MxGemmArgs& a, int odt, int tile_m, hipStream_t s);
+hipError_t launch_mx_reduce(const MxReduceArgs& a, int odt, int64_t blocks, hipStream_t s);
+hipError_t launch_mx_rows(const MxRowsArgs& a, int xdt, int odt, hipStream_t s);
 hipError_t launch_dropout(const MxDropArgs& a, int dt, int64_t blocks, hipStream_t s);
 
 // Work of one block of each kernel (the host sizes the grids with these).

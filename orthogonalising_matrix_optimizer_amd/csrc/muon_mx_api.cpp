@@ -121,6 +121,87 @@ int drop_of(float p, uint32_t* thr, float* scale) {
   return MUON_OK;
 }
 
+int64_t round_up(int64_t v, int64_t a) { return ceil_div(v, a) * a; }
+
+// How a list of products is run: the tile height, and the contraction length
+// (in code tiles) above which a product is split, 0 for none; per product the
+// workspace offset of its partial products.
+constexpr int64_t kTileN = 128;
+constexpr int64_t kMinChunk = 16;
+struct ProductPlan {
+  int tile_m = 256;
+  int64_t chunk = 0;
+  size_t bytes = 0;
+  std::vector<size_t> offset;
+};
+
+// The splits of a contraction of kt code tiles have the same length (but the last).
+int64_t even_chunk(int64_t kt, int64_t chunk) { return ceil_div(kt, ceil_div(kt, chunk)); }
+
+// Microseconds a stage (128 columns) of a work item takes with 1, 2, 3 blocks
+// on its CU, measured on MI355X: 256 x 128 tiles (two blocks a CU) and 128 x
+// 128 (three).  Of the two the cheaper is taken, e.g. K = 2560, N = 2560: M =
+// 2048 18 us with 128-high tiles and 20 with 256-high ones, 6000 29.5 and 27.5,
+// 8192 35 and 43 (640 tall tiles leave half of the CUs one short); M = 8191, N
+// = 10240: 132 and 121.
+constexpr double kStage256[3] = {0.72, 1.10, 1.10}, kStage128[3] = {0.45, 0.68, 0.88};
+
+// Time of a list whose items have `work` stages in all, the longest `longest`.
+double list_us(const double* t, int per_cu, double items, double work, double longest) {
+  if (items == 0) return 0;
+  const int n = int(std::ceil(items / 256));             // items on a CU
+  const double rounds = (n / per_cu) * t[per_cu - 1] + (n % per_cu ? t[n % per_cu - 1] : 0);
+  return std::max(work / items * rounds, longest * t[std::min(n, per_cu) - 1]);
+}
+
+ProductPlan plan_products(const muon_mx* a, const muon_mx* b, int n) {
+  ProductPlan p;
+  double i256 = 0, i128 = 0, w256 = 0, w128 = 0, longest = 0;
+  for (int i = 0; i < n; ++i) {
+    const double tn = ceil_div(b[i].rows, kTileN), kt = ceil_div(a[i].cols, kMxTileK);
+    const double n256 = ceil_div(a[i].rows, 256) * tn, n128 = ceil_div(a[i].rows, 128) * tn;
+    i256 += n256;
+    i128 += n128;
+    w256 += n256 * kt;
+    w128 += n128 * kt;
+    if (n128 > 0) longest = std::max(longest, kt);
+  }
+  const double t256 = list_us(kStage256, 2, i256, w256, longest);
+  double best = list_us(kStage128, 3, i128, w128, longest);
+  p.tile_m = t256 < best ? 256 : 128;
+  best = std::min(best, t256);
+  // Splitting adds the partial products' way to memory and back (4 TB/s) and
+  // a launch (5 us); it pays for few tiles with a long contraction and for
+  // lists with one much longer than the rest: 768 x 768 x 8192 21 us against
+  // 32, 128 x 2560 x 10240 20 against 39, twelve 768 x 768 with K of 1630 to
+  // 23201 75 against 98, but 2560 x 2560 x 16384 98 against 86.
+  for (int64_t c = kMinChunk; c < longest; c += c / 2) {
+    double items = 0, bytes = 0;
+    for (int i = 0; i < n; ++i) {
+      const int64_t kt = ceil_div(a[i].cols, kMxTileK), splits = std::max<int64_t>(1, ceil_div(kt, c));
+      items += double(splits) * ceil_div(a[i].rows, 128) * ceil_div(b[i].rows, kTileN);
+      if (splits > 1) bytes += 8.0 * splits * a[i].rows * b[i].rows;
+    }
+    const double t = list_us(kStage128, 3, items, w128, double(c)) + bytes / 4e6 + 5;
+    if (t < 0.9 * best) {
+      best = t / 0.9;
+      p.chunk = c;
+      p.tile_m = 128;
+    }
+  }
+  if (p.chunk) {
+    p.offset.assign(n, 0);
+    for (int i = 0; i < n; ++i) {
+      const int64_t kt = ceil_div(a[i].cols, kMxTileK);
+      if (kt <= p.chunk || a[i].rows == 0 || b[i].rows == 0) continue;
+      p.offset[i] = p.bytes;
+      p.bytes += size_t(ceil_div(kt, even_chunk(kt, p.chunk))) * a[i].rows * round_up(b[i].rows, 8) * 4;
+      p.bytes = round_up(p.bytes, 256);
+    }
+  }
+  return p;
+}
+
 int seed_ok(const uint64_t* dev) {
   return reinterpret_cast<uintptr_t>(dev) % 8 ? MUON_E_ALIGN : MUON_OK;
 }
@@ -269,8 +350,19 @@ int muon_mx_dequantize(const muon_mx* in, const muon_mat* out, int32_t n, void* 
   return MUON_E_HIP;
 }
 
+size_t muon_mx_matmul_workspace_bytes(const muon_mx* a, const muon_mx* b, int32_t n) try {
+  if (n <= 0 || !a || !b) return 0;
+  for (int i = 0; i < n; ++i)
+    if (!shape_ok(a[i].rows, a[i].cols) || !shape_ok(b[i].rows, b[i].cols) || a[i].cols != b[i].cols)
+      return 0;
+  return plan_products(a, b, n).bytes;
+} catch (...) {   // an allocation of the host's failed
+  return 0;
+}
+
 int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int32_t n,
-                   const muon_mx_options* opt, void* stream) try {
+                   const muon_mx_options* opt, void* workspace, size_t workspace_bytes,
+                   void* stream) try {
   if (n < 0) return MUON_E_SHAPE;
   if (n == 0) return MUON_OK;
   if (!a || !b || !out) return MUON_E_NULL;
@@ -279,13 +371,14 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
   if (opt) o = *opt;
   MxGemmArgs g;
   std::memset(&g, 0, sizeof(g));
+  MxReduceArgs red;
+  std::memset(&red, 0, sizeof(red));
   int rc;
-  if ((rc = drop_of(o.dropout, &g.drop, &g.drop_scale)) != MUON_OK) return rc;
+  if ((rc = drop_of(o.dropout, &red.drop, &red.drop_scale)) != MUON_OK) return rc;
   if ((rc = seed_ok(o.dropout_seed_dev)) != MUON_OK) return rc;
-  g.accumulate = o.accumulate != 0;
-  g.drop_seed = {o.dropout_seed, g.drop ? o.dropout_seed_dev : nullptr};
+  red.accumulate = o.accumulate != 0;
+  red.drop_seed = {o.dropout_seed, red.drop ? o.dropout_seed_dev : nullptr};
   std::vector<Span> spans;
-  const int ts = 128;
   for (int i = 0; i < n; ++i) {
     if ((rc = check_mx(a[i])) != MUON_OK || (rc = check_mx(b[i])) != MUON_OK ||
         (rc = check_dense(out[i])) != MUON_OK)
@@ -293,41 +386,124 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
     if (out[i].dtype != out[0].dtype) return MUON_E_DTYPE;
     if (a[i].cols != b[i].cols || out[i].rows != a[i].rows || out[i].cols != b[i].rows)
       return MUON_E_SHAPE;
-    if (ceil_div(a[i].rows, ts) * ceil_div(b[i].rows, ts) > kMaxBlocks) return MUON_E_SHAPE;
+    if (ceil_div(a[i].rows, 128) * ceil_div(b[i].rows, kTileN) > kMaxBlocks) return MUON_E_SHAPE;
     add_span(spans, a[i], false);
     add_span(spans, b[i], false);
     add_span(spans, out[i], true);
   }
-  if (g.drop) add_span(spans, o.dropout_seed_dev, sizeof(uint64_t), false);
+  const ProductPlan plan = plan_products(a, b, n);
+  if (plan.bytes) {
+    if (!workspace || workspace_bytes < plan.bytes) return MUON_E_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) % 16) return MUON_E_ALIGN;
+    add_span(spans, workspace, plan.bytes, true);
+  }
+  if (red.drop) add_span(spans, o.dropout_seed_dev, sizeof(uint64_t), false);
   if (conflict(spans)) return MUON_E_ALIAS;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  int64_t blocks = 0;
-  auto flush = [&]() {
-    if (g.n && launch_mx_gemm(g, out[0].dtype, ts, blocks, s) != hipSuccess) return MUON_E_HIP;
-    g.n = 0;
-    blocks = 0;
-    return MUON_OK;
-  };
-  for (int i = 0; i < n; ++i) {
-    const int64_t nb = ceil_div(a[i].rows, ts) * ceil_div(b[i].rows, ts);
-    if (nb == 0) continue;
-    if (g.n == kMxMaxList || blocks + nb > kMaxBlocks)
-      if ((rc = int(flush())) != MUON_OK) return rc;
-    MxProduct& p = g.p[g.n];
-    p.ac = static_cast<const uint8_t*>(a[i].codes);
-    p.as = static_cast<const uint8_t*>(a[i].scales);
-    p.bc = static_cast<const uint8_t*>(b[i].codes);
-    p.bs = static_cast<const uint8_t*>(b[i].scales);
-    p.out = out[i].ptr;
-    p.ld = out[i].ld;
-    p.M = int32_t(a[i].rows);
-    p.N = int32_t(b[i].rows);
-    p.kt = int32_t(ceil_div(a[i].cols, kMxTileK));
-    p.index = i;
-    g.base[g.n++] = uint32_t(blocks);
-    blocks += nb;
+
+  // products whose contraction is split write fp32 partials, the others their result
+  for (const bool split : {false, true}) {
+    int64_t items = 0, blocks = 0;
+    g.n = red.n = 0;
+    g.vec = 1;
+    g.accumulate = split ? 0 : red.accumulate;
+    g.drop = split ? 0 : red.drop;
+    g.drop_scale = red.drop_scale;
+    g.drop_seed = red.drop_seed;
+    auto flush = [&]() {
+      g.items = int32_t(items);
+      if (g.n && launch_mx_gemm(g, split ? int(kF32) : out[0].dtype, plan.tile_m, s) != hipSuccess)
+        return MUON_E_HIP;
+      if (split && g.n && launch_mx_reduce(red, out[0].dtype, blocks, s) != hipSuccess)
+        return MUON_E_HIP;
+      g.n = red.n = 0;
+      g.vec = 1;
+      items = blocks = 0;
+      return MUON_OK;
+    };
+    for (int i = 0; i < n; ++i) {
+      const int64_t M = a[i].rows, N = b[i].rows, kt = ceil_div(a[i].cols, kMxTileK);
+      const int64_t tiles = ceil_div(M, plan.tile_m) * ceil_div(N, kTileN);
+      const int64_t chunk = plan.chunk && kt > plan.chunk ? even_chunk(kt, plan.chunk) : std::max<int64_t>(kt, 1);
+      const int64_t splits = std::max<int64_t>(1, ceil_div(kt, chunk));
+      if (tiles == 0 || (splits > 1) != split) continue;
+      const int64_t nb = split ? ceil_div(M * (round_up(N, 8) / 8), 256) : 0;
+      if (g.n == kMxMaxList || items + tiles * splits > kMaxBlocks || blocks + nb > kMaxBlocks)
+        if ((rc = int(flush())) != MUON_OK) return rc;
+      MxProduct& p = g.p[g.n];
+      p.ac = static_cast<const uint8_t*>(a[i].codes);
+      p.as = static_cast<const uint8_t*>(a[i].scales);
+      p.bc = static_cast<const uint8_t*>(b[i].codes);
+      p.bs = static_cast<const uint8_t*>(b[i].scales);
+      p.M = int32_t(M);
+      p.N = int32_t(N);
+      p.kt = int32_t(kt);
+      p.chunk = int32_t(chunk);
+      p.tiles = int32_t(tiles);
+      p.index = i;
+      if (split) {
+        MxReduce& r = red.p[g.n];
+        r.ldp = int32_t(round_up(N, 8));
+        r.stride = M * r.ldp;
+        r.in = reinterpret_cast<const float*>(static_cast<char*>(workspace) + plan.offset[i]);
+        r.out = out[i].ptr;
+        r.ld = out[i].ld;
+        r.M = p.M;
+        r.N = p.N;
+        r.splits = int32_t(splits);
+        r.vec = vec_ok(out[i]);
+        r.index = i;
+        red.base[g.n] = uint32_t(blocks);
+        red.n = g.n + 1;
+        p.out = const_cast<float*>(r.in);
+        p.ld = r.ldp;
+        p.stride = r.stride;
+      } else {
+        p.out = out[i].ptr;
+        p.ld = out[i].ld;
+        p.stride = 0;
+        g.vec = g.vec && vec_ok(out[i]);
+      }
+      g.base[g.n++] = uint32_t(items);
+      items += tiles * splits;
+      blocks += nb;
+    }
+    if ((rc = int(flush())) != MUON_OK) return rc;
   }
-  return flush();
+  return MUON_OK;
+} catch (...) {   // an allocation of the host's failed
+  return MUON_E_HIP;
+}
+
+int muon_mx_matmul_rows(const muon_mat* x, const muon_mx* b, const muon_mat* out,
+                        void* stream) try {
+  if (!x || !b || !out) return MUON_E_NULL;
+  int rc;
+  if ((rc = check_dense(*x)) != MUON_OK || (rc = check_mx(*b)) != MUON_OK ||
+      (rc = check_dense(*out)) != MUON_OK)
+    return rc;
+  if (x->rows > MUON_MX_FEW_ROWS || x->cols != b->cols || out->rows != x->rows || out->cols != b->rows)
+    return MUON_E_SHAPE;
+  std::vector<Span> spans;
+  add_span(spans, *x, false);
+  add_span(spans, *b, false);
+  add_span(spans, *out, true);
+  if (conflict(spans)) return MUON_E_ALIAS;
+  if (out->rows == 0 || out->cols == 0) return MUON_OK;
+  MxRowsArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = x->ptr;
+  a.ldx = x->ld;
+  a.bc = static_cast<const uint8_t*>(b->codes);
+  a.bs = static_cast<const uint8_t*>(b->scales);
+  a.out = out->ptr;
+  a.ldo = out->ld;
+  a.M = int32_t(x->rows);
+  a.N = int32_t(b->rows);
+  a.K = int32_t(x->cols);
+  a.vec = x->cols == 0 || vec_ok(*x);
+  return launch_mx_rows(a, x->dtype, out->dtype, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? MUON_OK : MUON_E_HIP;
 } catch (...) {   // an allocation of the host's failed
   return MUON_E_HIP;
 }

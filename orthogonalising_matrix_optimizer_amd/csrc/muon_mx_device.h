@@ -1,10 +1,30 @@
-// Device helpers shared by the 4-bit operators: random numbers and the lookup
-// of a block's matrix in a grouped launch.
+// Device helpers shared by the 4-bit operators: random numbers, block scales and
+// codes, and the lookup of a block's matrix in a grouped launch.
 #pragma once
 #include "muon_mx.h"
 
 namespace muon {
 namespace {
+
+#if defined(__HIP_DEVICE_COMPILE__)
+#define GAS __attribute__((address_space(1)))
+#else
+#define GAS
+#endif
+template <class T>
+__device__ __forceinline__ GAS T* glb(T* p) { return (GAS T*)(p); }
+template <class T>
+__device__ __forceinline__ const GAS T* glb(const T* p) { return (const GAS T*)(p); }
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Scale byte of a block from the bits of its largest magnitude (fp32), and the
+// power of two itself as fp32 bits (255: the block holds an infinity or NaN).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+  if (top >= 0x7f800000u) return kMxNan;
+  const uint32_t e = (top + 0x3FFFFFu) >> 23;
+  return e > 2 ? e - 2 : 0;
+}
 
 __device__ __forceinline__ uint64_t seed_of(const MxSeed& s) { return s.dev ? *s.dev : s.value; }
 
@@ -35,6 +55,57 @@ __device__ __forceinline__ int find_in_list(const uint32_t* base, int n, uint32_
   const int lane = threadIdx.x & 63;
   const bool below = lane < n && base[lane < n ? lane : 0] <= b;
   return __builtin_amdgcn_readfirstlane(__popcll(__ballot(below))) - 1;
+}
+
+// Eight codes of a block in a dword, element i in bits 4 i, rounded to nearest
+// (ties to the even code): the conversion reads only the scale's exponent.
+__device__ __forceinline__ uint32_t encode8_near(const float* v, uint32_t byte) {
+  const float sc = __uint_as_float(byte << 23);
+  uint32_t out = 0;
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[0], v[1], sc, 0);
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[2], v[3], sc, 1);
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[4], v[5], sc, 2);
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[6], v[7], sc, 3);
+  return byte == kMxNan ? 0u : out;
+}
+
+// The same for eight bf16 elements in four dwords, which need no widening.
+__device__ __forceinline__ bf16x2_t bf16_pair(uint32_t q) { return __builtin_bit_cast(bf16x2_t, q); }
+__device__ __forceinline__ uint32_t encode8_near(u32x4_t q, uint32_t byte) {
+  const float sc = __uint_as_float(byte << 23);
+  uint32_t out = 0;
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(out, bf16_pair(q[0]), sc, 0);
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(out, bf16_pair(q[1]), sc, 1);
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(out, bf16_pair(q[2]), sc, 2);
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(out, bf16_pair(q[3]), sc, 3);
+  return byte == kMxNan ? 0u : out;
+}
+
+// Bits of the largest magnitude as fp32, of n dwords of two bf16 or one fp32.
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+template <int DT, int N>
+__device__ __forceinline__ uint32_t top_of(const uint32_t* q) {
+  if constexpr (DT == kBF16) {
+    u16x2_t m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, q[i] & 0x7fff7fffu));
+    return static_cast<uint32_t>(m[0] > m[1] ? m[0] : m[1]) << 16;
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = umax(m, q[i] & 0x7fffffffu);
+    return m;
+  }
+}
+
+// Largest of a value over a pair (four) of neighbouring lanes.
+__device__ __forceinline__ uint32_t max_pair(uint32_t v) {
+  return umax(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xF, 0xF, true)));
+}
+__device__ __forceinline__ uint32_t max_quad(uint32_t v) {
+  v = max_pair(v);
+  return umax(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4E, 0xF, 0xF, true)));
 }
 
 }  // namespace

@@ -17,26 +17,6 @@
 namespace muon {
 namespace {
 
-#if defined(__HIP_DEVICE_COMPILE__)
-#define GAS __attribute__((address_space(1)))
-#else
-#define GAS
-#endif
-template <class T>
-__device__ __forceinline__ GAS T* glb(T* p) { return (GAS T*)(p); }
-template <class T>
-__device__ __forceinline__ const GAS T* glb(const T* p) { return (const GAS T*)(p); }
-
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
-// Scale byte of a block from the bits of its largest magnitude (fp32), and the
-// power of two itself as fp32 bits (255: the block holds an infinity or NaN).
-__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
-  if (top >= 0x7f800000u) return kMxNan;
-  const uint32_t e = (top + 0x3FFFFFu) >> 23;
-  return e > 2 ? e - 2 : 0;
-}
-
 // Code of |t| <= 6 (t already divided by the scale) rounded stochastically:
 // up where 256 times the fraction of the step exceeds r + 1/2.
 __device__ __forceinline__ uint32_t code_sr(float t, uint32_t r) {
@@ -109,29 +89,17 @@ __device__ __forceinline__ void drop16(float* v, uint32_t row, uint32_t c0, uint
 // Eight codes of a block in a dword, element i in bits 4 i.
 template <bool SR>
 __device__ __forceinline__ uint32_t encode8(const float* v, uint32_t byte, const uint32_t* r8) {
-  uint32_t out = 0;
   if constexpr (SR) {
+    uint32_t out = 0;
     // 2^(127 - byte), an ordinary number: a finite block's byte is at most 253
     const float inv = __uint_as_float((254u - byte) << 23);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       out |= code_sr(v[i] * inv, (r8[i / 4] >> (8 * (i & 3))) & 255u) << (4 * i);
+    return byte == kMxNan ? 0u : out;
   } else {
-    const float sc = __uint_as_float(byte << 23);   // only the exponent is read
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[0], v[1], sc, 0);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[2], v[3], sc, 1);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[4], v[5], sc, 2);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[6], v[7], sc, 3);
+    return encode8_near(v, byte);
   }
-  return byte == kMxNan ? 0u : out;
-}
-
-template <int N>
-__device__ __forceinline__ uint32_t top_of(const float* v) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) m = umax(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  return m;
 }
 
 // One 128 x 128 tile of the input per block of four waves.  A lane reads 16
@@ -186,9 +154,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs args) {
       }
     }
     if constexpr (ROWS) {
-      uint32_t top = top_of<16>(v);
-      top = umax(top, __shfl_xor(top, 1, 64));
-      const uint32_t byte = scale_byte(top);
+      const uint32_t byte = scale_byte(max_pair(top_of<kF32, 16>(reinterpret_cast<const uint32_t*>(v))));
       Words w = {{0, 0, 0, 0}};
       if constexpr (SR) w = philox(c0 / 16, r, kTagRound, m.index, seed);
       uint2 code;
@@ -196,7 +162,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs args) {
       code.y = encode8<SR>(v + 8, byte, w.w + 2);
       const int rt = tr * (T / 16) + (t >> 7) * 4 + i;   // 16-row tile
       if (rt * 16 < m.rows) {
-        const int64_t o = (static_cast<int64_t>(rt) * kt + tc) * kMxTileBytes +
+        const int64_t o = (static_cast<int64_t>(tc) * ((m.rows + 15) / 16) + rt) * kMxTileBytes +
                           ((ch >> 1) * 16 + r16) * 16 + (ch & 1) * 8;
         *glb(reinterpret_cast<uint2*>(m.codes + o)) = code;
       }
@@ -206,7 +172,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs args) {
   if constexpr (ROWS) {
     const int sg = tr * 2 + (t >> 7);                    // 64-row scale tile
     if ((ch & 1) == 0 && sg * 64 < m.rows)
-      *glb(reinterpret_cast<uint32_t*>(m.scales + (static_cast<int64_t>(sg) * kt + tc) * kMxScaleBytes +
+      *glb(reinterpret_cast<uint32_t*>(m.scales + (static_cast<int64_t>(tc) * ((m.rows + 63) / 64) + sg) * kMxScaleBytes +
                                        ((ch >> 1) * 16 + r16) * 4)) = sdw;
   }
   if constexpr (COLS) {
@@ -225,12 +191,12 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs args) {
         v[1][j] = q.y;
       }
     }
-    const int ktt = (m.rows + T - 1) / T;                // tiles along the transpose's columns
+    const int rtt = (m.cols + 15) / 16, sgt = (m.cols + 63) / 64;   // the transpose's row and scale tiles
     uint32_t sb = 0;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int c = tc * T + 2 * cp + e;                 // row of the transpose
-      const uint32_t byte = scale_byte(top_of<32>(v[e]));
+      const uint32_t byte = scale_byte(top_of<kF32, 32>(reinterpret_cast<const uint32_t*>(v[e])));
       sb |= byte << (8 * e);
       u32x4_t code;
 #pragma unroll
@@ -242,7 +208,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs args) {
       }
       const int rt = c >> 4;
       if (rt * 16 < m.cols)
-        *glb(reinterpret_cast<u32x4_t*>(m.codes_t + (static_cast<int64_t>(rt) * ktt + tr) * kMxTileBytes +
+        *glb(reinterpret_cast<u32x4_t*>(m.codes_t + (static_cast<int64_t>(tr) * rtt + rt) * kMxTileBytes +
                                         (rb * 16 + (c & 15)) * 16)) = code;
     }
     // the four columns c, c + 16, c + 32, c + 48 of a scale dword are eight lanes apart
@@ -252,7 +218,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs args) {
       uint2 d;
       d.x = (sb & 255) | (s1 & 255) << 8 | (s2 & 255) << 16 | (s3 & 255) << 24;
       d.y = (sb >> 8) | (s1 >> 8) << 8 | (s2 >> 8) << 16 | (s3 >> 8) << 24;
-      *glb(reinterpret_cast<uint2*>(m.scales_t + (static_cast<int64_t>(c >> 6) * ktt + tr) * kMxScaleBytes +
+      *glb(reinterpret_cast<uint2*>(m.scales_t + (static_cast<int64_t>(tr) * sgt + (c >> 6)) * kMxScaleBytes +
                                     (rb * 16 + (c & 15)) * 4)) = d;
     }
   }
@@ -294,8 +260,8 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs args) {
     if (r >= m.rows) return;
     const int slot = (ch >> 2) * 16 + r16;
     const uint32_t code = *glb(reinterpret_cast<const uint32_t*>(
-        m.codes + (static_cast<int64_t>(rt) * kt + tc) * kMxTileBytes + slot * 16 + (ch & 3) * 4));
-    const uint32_t byte = *glb(m.scales + (static_cast<int64_t>(rt >> 2) * kt + tc) * kMxScaleBytes +
+        m.codes + (static_cast<int64_t>(tc) * ((m.rows + 15) / 16) + rt) * kMxTileBytes + slot * 16 + (ch & 3) * 4));
+    const uint32_t byte = *glb(m.scales + (static_cast<int64_t>(tc) * ((m.rows + 63) / 64) + (rt >> 2)) * kMxScaleBytes +
                                slot * 4 + (rt & 3));
     // 2^(byte - 127) in fp32 (2^-127 is subnormal); 255 is NaN
     const float sc = byte == kMxNan ? __uint_as_float(0x7fc00000u)

@@ -8,6 +8,7 @@
 // lane holds the bytes of four row tiles, picked by the instruction's byte
 // select.  b is the instruction's first operand, so a lane's four results are
 // consecutive columns of out.
+#include <type_traits>
 #include <utility>
 
 #include "muon_common.h"
@@ -35,45 +36,94 @@ __device__ __forceinline__ void unrolled(std::integer_sequence<int, I...>, F&& f
   (f(std::integral_constant<int, I>{}), ...);
 }
 
-// One operand of a block: the code tiles of its rows and their scales.  Row
-// tiles past the matrix's last are read as the last one again: their products
-// are never stored.
-template <int ROWS, int NW>
+// One operand of a work item: the code tiles of its rows and their scales, one
+// step of 128 columns a stage.  Row tiles past the matrix's last are read as
+// the last one again: their products are never stored.  The stage's scales are
+// one load, by wave SW (a load costs as much with few lanes as with all).
+template <int ROWS, int NW, int SW>
 struct Operand {
-  static constexpr int kTiles = ROWS / kMxTileR;          // code tiles per stage
-  static constexpr int kPer = kTiles / NW;                // ... per wave
-  static constexpr int kScaleLanes = ROWS * 4 / 16 / NW;  // lanes of a wave's scale load
+  static constexpr int kPer = ROWS / kMxTileR / NW;       // row tiles of a wave
   static constexpr int kBytes = ROWS * (kMxTileK / 2);    // codes per stage
   static constexpr int kScales = ROWS * 4;                // scales per stage
-  static_assert(kTiles % NW == 0 && kScaleLanes >= 1, "load split");
-  u32x4_t codes, scales;
-  uint32_t vcode[kPer];    // byte offset of the wave's tiles in the first stage
+  static constexpr int kScaleLanes = kScales / 16;
+  static_assert(ROWS / kMxTileR % NW == 0 && kScaleLanes <= 64 && SW < NW, "load split");
+  uint64_t codes, scales;  // the next stage's row panel
+  uint64_t kcode, kscale;  // bytes from one stage to the next
+  uint32_t vcode[kPer];    // byte offset of the wave's tiles in a panel
   uint32_t vscale;
 
   __device__ __forceinline__ void plan(const uint8_t* c, const uint8_t* s, int row0, int rows,
-                                       int kt, int wave, int lane) {
+                                       int k0, int wave, int lane) {
     const int t0 = row0 / kMxTileR, s0 = row0 / kMxScaleRows;
-    const int nt = (rows + kMxTileR - 1) / kMxTileR - t0;     // row tiles from here on
-    const int ns = (rows + kMxScaleRows - 1) / kMxScaleRows - s0;
-    codes = make_desc(c + static_cast<int64_t>(t0) * kt * kMxTileBytes, 0xffffffffu);
-    scales = make_desc(s + static_cast<int64_t>(s0) * kt * kMxScaleBytes, 0xffffffffu);
+    const int rt = (rows + kMxTileR - 1) / kMxTileR, st = (rows + kMxScaleRows - 1) / kMxScaleRows;
+    kcode = static_cast<uint64_t>(rt) * kMxTileBytes;
+    kscale = static_cast<uint64_t>(st) * kMxScaleBytes;
+    codes = reinterpret_cast<uint64_t>(c) + k0 * kcode + static_cast<uint64_t>(t0) * kMxTileBytes;
+    scales = reinterpret_cast<uint64_t>(s) + k0 * kscale + static_cast<uint64_t>(s0) * kMxScaleBytes;
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int j = wave + NW * u;
-      vcode[u] = static_cast<uint32_t>(j < nt ? j : nt - 1) * kt * kMxTileBytes;
+      vcode[u] = (j < rt - t0 ? j : rt - t0 - 1) * kMxTileBytes;
     }
-    const int b = (wave * kScaleLanes + lane) * 16;          // byte of the stage's scales
-    const int g = b / kMxScaleBytes;
-    vscale = static_cast<uint32_t>(g < ns ? g : ns - 1) * kt * kMxScaleBytes + b % kMxScaleBytes;
+    const int g = lane * 16 / kMxScaleBytes;
+    vscale = (g < st - s0 ? g : st - s0 - 1) * kMxScaleBytes + lane * 16 % kMxScaleBytes;
   }
-  __device__ __forceinline__ void load(int k, int wave, int lane, uint8_t* dst, uint8_t* sdst) const {
+  // Loads the stage and moves on; dst, sdst: LDS addresses of its codes and scales.
+  __device__ __forceinline__ void load(int wave, int lane, uint32_t dst, uint32_t sdst) {
+    const u32x4_t dc = make_desc(reinterpret_cast<const void*>(codes), kBytes);
 #pragma unroll
     for (int u = 0; u < kPer; ++u)
-      dma16(codes, lds_addr(dst) + (wave + NW * u) * kMxTileBytes, lane * 16,
-            vcode[u] + k * kMxTileBytes);
-    if (lane < kScaleLanes)
-      dma16(scales, lds_addr(sdst) + wave * kScaleLanes * 16, vscale, k * kMxScaleBytes);
+      dma16(dc, dst + (wave + NW * u) * kMxTileBytes, lane * 16, vcode[u]);
+    if (wave == SW) {
+      const u32x4_t ds = make_desc(reinterpret_cast<const void*>(scales), kScales);
+      if (lane < kScaleLanes) dma16(ds, sdst, vscale, 0);
+    }
+    codes += kcode;
+    scales += kscale;
   }
+};
+
+// Work item b of a launch: product, tile origin and contraction range.
+struct Item {
+  const MxProduct* p;
+  int m0, n0, k0, k1, split;
+};
+template <int TM, int TN>
+__device__ __forceinline__ Item item_of(const MxGemmArgs& args, uint32_t b) {
+  const int g = find_in_list(args.base, args.n, b);
+  const MxProduct& p = args.p[g];
+  const int in_product = static_cast<int>(b - args.base[g]);
+  Item it;
+  it.p = &p;
+  it.split = in_product / p.tiles;
+  const int t = in_product % p.tiles;
+  // groups of GM row tiles, column by column, so that neighbouring blocks of
+  // an XCD share both operands
+  constexpr int GM = 8;
+  const int tm_n = (p.M + TM - 1) / TM, tn_n = (p.N + TN - 1) / TN;
+  const int per_group = GM * tn_n;
+  const int grp = t / per_group, in = t % per_group;
+  const int gm = tm_n - grp * GM < GM ? tm_n - grp * GM : GM;
+  it.m0 = (grp * GM + in % gm) * TM;
+  it.n0 = in / gm * TN;
+  it.k0 = it.split * p.chunk;
+  it.k1 = it.k0 + p.chunk < p.kt ? it.k0 + p.chunk : p.kt;
+  return it;
+}
+
+// Register operands of one stage for a wave: FN row tiles of b, FM of a.
+//
+// The 16 results of an instruction that a lane group holds are four
+// consecutive rows of the first operand.  So that a lane ends up with eight
+// consecutive columns of out (16-byte stores), two operands of b share 32
+// rows: row r of the even one is row 8 (r / 4) + 4 (r / 8) + r % 4 of the 32,
+// row r of the odd one the same with the other half of the eight.  (The halves
+// swap at r = 8 so that 16 lanes still read 16 different 16-byte slots.)
+template <int FN, int FM>
+struct Frags {
+  i32x4_t n[FN], m[FM];
+  uint32_t dn[FN / 2];
+  int dm[FM / 4];
 };
 
 __device__ __forceinline__ float load_out(const uint16_t* p) {
@@ -82,134 +132,462 @@ __device__ __forceinline__ float load_out(const uint16_t* p) {
 __device__ __forceinline__ float load_out(const float* p) { return *p; }
 __device__ __forceinline__ void store_out(uint16_t* p, float v) { *p = f2bf(v); }
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
-
-// TM x TN output tile by WM x WN waves; NST stages of 128 columns in LDS.
-template <int ODT, int TM, int TN, int WM, int WN, int NST>
-__global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_gemm(MxGemmArgs args) {
-  using T = typename std::conditional<ODT == kBF16, uint16_t, float>::type;
-  constexpr int NW = WM * WN;
-  using OpN = Operand<TN, NW>;
-  using OpM = Operand<TM, NW>;
-  constexpr int kStage = OpN::kBytes + OpM::kBytes + OpN::kScales + OpM::kScales;
-  constexpr int PER = OpN::kPer + OpM::kPer + 2;      // loads per wave per stage
-  constexpr int FN = TN / WN / 16, FM = TM / WM / 16; // 16-row operands of a wave
-  static_assert(FN % 4 == 0 && FM % 4 == 0, "a wave takes whole scale dwords");
-  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-
-  const uint32_t blk = xcd_block();
-  const int g = find_in_list(args.base, args.n, blk);
-  const MxProduct& p = args.p[g];
-  const uint32_t b = blk - args.base[g];
-  // groups of GM row tiles, column by column, so that neighbouring blocks of
-  // an XCD share both operands
-  constexpr int GM = 8;
-  const int tm_n = (p.M + TM - 1) / TM, tn_n = (p.N + TN - 1) / TN;
-  const int per_group = GM * tn_n;
-  const int grp = b / per_group, in = b % per_group;
-  const int gm = tm_n - grp * GM < GM ? tm_n - grp * GM : GM;
-  const int tm = grp * GM + in % gm, tn = in / gm;
-
-  const int t = threadIdx.x, lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int wm = wave / WN, wn = wave % WN;
-  const int kt = p.kt;
-  OpN on;
-  OpM om;
-  on.plan(p.bc, p.bs, tn * TN, p.N, kt, wave, lane);
-  om.plan(p.ac, p.as, tm * TM, p.M, kt, wave, lane);
-
-  auto issue = [&](int k) {
-    uint8_t* st = smem + (k % NST) * kStage;
-    on.load(k, wave, lane, st, st + OpN::kBytes + OpM::kBytes);
-    om.load(k, wave, lane, st + OpN::kBytes, st + OpN::kBytes + OpM::kBytes + OpN::kScales);
-  };
-  f32x4_t acc[FN][FM];
+__device__ __forceinline__ void load8(const uint16_t* p, float* v) {
+  const u32x4_t q = *reinterpret_cast<const u32x4_t*>(p);
 #pragma unroll
-  for (int i = 0; i < FN; ++i)
-#pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  for (int k = 0; k < NST - 1 && k < kt; ++k) issue(k);
-  for (int k = 0; k < kt; ++k) {
-    wait_ahead<NST - 2, PER>(kt - 1 - k);
-    lds_barrier();
-    if (k + NST - 1 < kt) issue(k + NST - 1);
-    const uint8_t* st = smem + (k % NST) * kStage;
-    const uint8_t* sn = st + OpN::kBytes + OpM::kBytes;
-    const uint8_t* sm = sn + OpN::kScales;
-    i32x4_t fn[FN], fm[FM];
-    int dn[FN / 4], dm[FM / 4];
-#pragma unroll
-    for (int i = 0; i < FN / 4; ++i)
-      dn[i] = *reinterpret_cast<const int*>(sn + (wn * (FN / 4) + i) * kMxScaleBytes + lane * 4);
-#pragma unroll
-    for (int i = 0; i < FM / 4; ++i)
-      dm[i] = *reinterpret_cast<const int*>(sm + (wm * (FM / 4) + i) * kMxScaleBytes + lane * 4);
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-      fn[i] = *reinterpret_cast<const i32x4_t*>(st + (wn * FN + i) * kMxTileBytes + lane * 16);
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-      fm[i] = *reinterpret_cast<const i32x4_t*>(st + OpN::kBytes + (wm * FM + i) * kMxTileBytes + lane * 16);
-    unrolled(std::make_integer_sequence<int, FN>{}, [&](auto I) {
-      unrolled(std::make_integer_sequence<int, FM>{}, [&](auto J) {
-        constexpr int i = decltype(I)::value, j = decltype(J)::value;
-        acc[i][j] = mfma4<i & 3, j & 3>(fn[i], fm[j], acc[i][j], dn[i / 4], dm[j / 4]);
-      });
-    });
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(q[i] << 16);
+    v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
   }
+}
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = a[i];
+    v[4 + i] = b[i];
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
+  *reinterpret_cast<u32x4_t*>(p) = u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                           pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  *reinterpret_cast<f32x4_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+}
 
-  const uint64_t seed = args.drop ? seed_of(args.drop_seed) : 0;
-  T* out = static_cast<T*>(p.out);
-#pragma unroll
-  for (int j = 0; j < FM; ++j) {
-    const int r = tm * TM + (wm * FM + j) * 16 + (lane & 15);
-    if (r >= p.M) continue;
-#pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      const int c = tn * TN + (wn * FN + i) * 16 + 4 * (lane >> 4);
-      if (c >= p.N) continue;
-      T* o = out + r * p.ld + c;
-      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      if (args.drop) {
-        const Words w = philox(c / 8, r, kTagDropout, p.index, seed);
-        const uint32_t lo = c & 4 ? w.w[2] : w.w[0], hi = c & 4 ? w.w[3] : w.w[1];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t q = ((e < 2 ? lo : hi) >> (16 * (e & 1))) & 0xffffu;
-          v[e] = q >= args.drop ? v[e] * args.drop_scale : 0.f;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (c + e < p.N) store_out(o + e, args.accumulate ? load_out(o + e) + v[e] : v[e]);
+// Output written past the caches' keeping: the operand panels stay in L2.
+__device__ __forceinline__ void store8nt(uint16_t* p, const float* v) {
+  const u32x4_t q = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                     pack_bf16(v[6], v[7])};
+  __builtin_nontemporal_store(q, reinterpret_cast<u32x4_t*>(p));
+}
+__device__ __forceinline__ void store8nt(float* p, const float* v) {
+  __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_t*>(p));
+  __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4_t*>(p) + 1);
+}
+
+// Wait until a stage has landed when `ahead` (at most MAXA) later stages of PER
+// loads each, and EXTRA stores if `extra`, were issued after it.
+template <int MAXA, int PER, int EXTRA>
+__device__ __forceinline__ void wait_stage(int ahead, bool extra) {
+  if constexpr (MAXA == 0) {
+    if (extra) wait_vm<(EXTRA < 63 ? EXTRA : 63)>();
+    else wait_vm<0>();
+  } else {
+    if (ahead >= MAXA) {
+      if (extra) wait_vm<(MAXA * PER + EXTRA < 63 ? MAXA * PER + EXTRA : 63)>();
+      else wait_vm<MAXA * PER>();
+    } else {
+      wait_stage<MAXA - 1, PER, EXTRA>(ahead, extra);
     }
   }
 }
 
-template <int ODT, int TM, int TN, int WM, int WN, int NST>
-hipError_t launch_tile(const MxGemmArgs& a, int64_t blocks, hipStream_t s) {
+// TM x TN output tiles by WM x WN waves; a ring of NST stages of 128 columns
+// in LDS, loaded NST - 1 stages ahead.  A block takes work items in turn (all
+// blocks of an XCD neighbouring ones) and the stages of its items form one
+// sequence, so an item's stores run beside the next item's loads.  PER_CU
+// blocks share a CU, and one multiplies while another waits at its barrier.
+//
+// Measured on MI355X (random codes, 16384 x 2560 outputs, K = 10240): 256 x 128
+// tiles of four waves, two blocks a CU, 3.9-4.3 PF; 128 x 128, three blocks,
+// 3.5-3.8; 256 x 256 of eight waves 3.6-3.9 (with the two waves of a SIMD
+// alternating between reads and products 2.9).  The instruction alone sustains
+// 9.5 PF on zeros and 7.1 on random codes (power).  What bounds the loop: the
+// LDS loads of a stage need as long as its products (skipping parts at 16384 x
+// 4096 x 10240: all 312 us, without loads 228, without LDS reads 280, without
+// products 215, loads alone 215).
+template <int ODT, int TM, int TN, int WM, int WN, int NST, int PER_CU, bool DROP>
+__global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(MxGemmArgs args) {
+  using T = typename std::conditional<ODT == kBF16, uint16_t, float>::type;
   constexpr int NW = WM * WN;
-  constexpr int lds = NST * (Operand<TN, NW>::kBytes + Operand<TM, NW>::kBytes +
-                             Operand<TN, NW>::kScales + Operand<TM, NW>::kScales);
-  const void* f = reinterpret_cast<const void*>(&k_mx_gemm<ODT, TM, TN, WM, WN, NST>);
-  static_assert(lds <= 160 * 1024, "LDS");
-  const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  using OpN = Operand<TN, NW, 0>;
+  using OpM = Operand<TM, NW, 1>;
+  constexpr int kStage = OpN::kBytes + OpM::kBytes + OpN::kScales + OpM::kScales;
+  constexpr int PER = OpN::kPer + OpM::kPer;          // loads per wave per stage; waves 0 and 1
+                                                      // load scales too
+  constexpr int FN = TN / WN / 16, FM = TM / WM / 16; // 16-row operands of a wave
+  static_assert(FN % 4 == 0 && FM % 4 == 0, "a wave takes whole scale dwords");
+  static_assert(NST >= 2, "ring");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  const uint32_t lds = lds_addr(smem);
+
+  // items of this block: XCD x (blocks b = x mod 8) owns a contiguous range
+  const uint32_t total = args.items, grid = gridDim.x, x = blockIdx.x & 7, loc = blockIdx.x >> 3;
+  const uint32_t q = total >> 3, rem = total & 7;
+  const uint32_t first = x * q + (x < rem ? x : rem), last = first + q + (x < rem ? 1 : 0);
+  const uint32_t step = (grid + 7 - x) >> 3;
+
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  // ---- loads: run NST stages ahead of the products
+  uint32_t ld_item = first + loc;
+  int ld_k = 0, ld_k1 = 0, ld_slot = 0;
+  int issued = 0;                       // stages issued so far
+  OpN on;
+  OpM om;
+  auto ld_open = [&]() {                // plan ld_item, skipping items without stages
+    while (ld_item < last) {
+      const Item it = item_of<TM, TN>(args, ld_item);
+      ld_k = it.k0;
+      ld_k1 = it.k1;
+      if (ld_k < ld_k1) {
+        on.plan(it.p->bc, it.p->bs, it.n0, it.p->N, it.k0, wave, lane);
+        om.plan(it.p->ac, it.p->as, it.m0, it.p->M, it.k0, wave, lane);
+        return;
+      }
+      ld_item += step;
+    }
+  };
+  auto issue = [&]() {                  // the next stage of the sequence, if there is one
+    if (ld_item >= last) return;
+    const uint32_t st = lds + ld_slot * kStage;
+    on.load(wave, lane, st, st + OpN::kBytes + OpM::kBytes);
+    om.load(wave, lane, st + OpN::kBytes, st + OpN::kBytes + OpM::kBytes + OpN::kScales);
+    ld_slot = ld_slot + 1 == NST ? 0 : ld_slot + 1;
+    ++issued;
+    if (++ld_k == ld_k1) {
+      ld_item += step;
+      ld_open();
+    }
+  };
+
+  // ---- register operands
+  const int r = lane & 15, kb = lane >> 4, half = r >> 3;
+  const int even = 8 * (r >> 2) + 4 * half + (r & 3), odd = 8 * (r >> 2) + 4 * (1 - half) + (r & 3);
+  const int off_e = (even >> 4) * kMxTileBytes + kb * 256 + (even & 15) * 16;
+  const int off_o = (odd >> 4) * kMxTileBytes + kb * 256 + (odd & 15) * 16;
+  const int soff_e = (kb * 16 + (even & 15)) * 4, soff_o = (kb * 16 + (odd & 15)) * 4;
+  int rd_slot = 0;
+  auto read = [&](Frags<FN, FM>& f) {   // the stage in rd_slot
+    const uint8_t* st = smem + rd_slot * kStage;
+    const uint8_t* sn = st + OpN::kBytes + OpM::kBytes;
+    const uint8_t* sm = st + OpN::kBytes + OpM::kBytes + OpN::kScales;
+    const uint8_t* pn = st + wn * FN * kMxTileBytes;
+    const uint8_t* pm = st + OpN::kBytes + wm * FM * kMxTileBytes + lane * 16;
+#pragma unroll
+    for (int i = 0; i < FN / 4; ++i) {
+      const uint8_t* s = sn + (wn * (FN / 4) + i) * kMxScaleBytes;
+      f.dn[2 * i] = *reinterpret_cast<const uint32_t*>(s + soff_e);
+      f.dn[2 * i + 1] = *reinterpret_cast<const uint32_t*>(s + soff_o);
+    }
+#pragma unroll
+    for (int i = 0; i < FM / 4; ++i)
+      f.dm[i] = *reinterpret_cast<const int*>(sm + (wm * (FM / 4) + i) * kMxScaleBytes + lane * 4);
+    f.n[0] = *reinterpret_cast<const i32x4_t*>(pn + off_e);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) f.m[i] = *reinterpret_cast<const i32x4_t*>(pm + i * kMxTileBytes);
+#pragma unroll
+    for (int i = 1; i < FN; ++i)
+      f.n[i] = *reinterpret_cast<const i32x4_t*>(pn + (i & ~1) * kMxTileBytes + (i & 1 ? off_o : off_e));
+    rd_slot = rd_slot + 1 == NST ? 0 : rd_slot + 1;
+  };
+
+  f32x4_t acc[FN][FM];
+  auto multiply = [&](Frags<FN, FM>& f) {
+    // lanes of the upper rows use the next row tile's scale byte
+#pragma unroll
+    for (int i = 0; i < FN / 2; ++i) f.dn[i] >>= 8 * half;
+    unrolled(std::make_integer_sequence<int, FN>{}, [&](auto I) {
+      unrolled(std::make_integer_sequence<int, FM>{}, [&](auto J) {
+        constexpr int i = decltype(I)::value, j = decltype(J)::value;
+        acc[i][j] = mfma4<(i & 2), (j & 3)>(f.n[i], f.m[j], acc[i][j], static_cast<int>(f.dn[(i / 4) * 2 + (i & 1)]), f.dm[j / 4]);
+      });
+    });
+  };
+
+  ld_open();
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i) issue();
+  int done = 0;                         // stages whose operands were read from LDS
+  // stores of a whole tile, and the stages whose loads were issued before them
+  constexpr int NSTORE = FM * FN / 2 * (ODT == kBF16 ? 1 : 2);
+  int covered = 0;
+  // this wave's loads of stage `done` have landed
+  const bool scales_too = wave < 2;
+  auto wait_next = [&]() {
+    if (scales_too) wait_stage<NST - 2, PER + 1, NSTORE>(issued - done - 1, done < covered);
+    else wait_stage<NST - 2, PER, NSTORE>(issued - done - 1, done < covered);
+  };
+  Frags<FN, FM> f;
+
+  for (uint32_t item = first + loc; item < last; item += step) {
+    const Item it = item_of<TM, TN>(args, item);
+    const MxProduct& p = *it.p;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int k = it.k0; k < it.k1; ++k) {
+      wait_next();
+      lds_barrier();
+      read(f);
+      ++done;
+      // reads first, then the loads, then the products at raised priority
+      __builtin_amdgcn_sched_barrier(0);
+      issue();
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);
+      multiply(f);
+      __builtin_amdgcn_s_setprio(0);
+    }
+
+    const uint64_t seed = DROP ? seed_of(args.drop_seed) : 0;
+    T* out = static_cast<T*>(p.out) + it.split * p.stride;
+    const bool whole = args.vec && !args.accumulate && it.m0 + TM <= p.M && it.n0 + TN <= p.N;
+    covered = whole ? issued : 0;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int row = it.m0 + (wm * FM + j) * 16 + (lane & 15);
+      if (row >= p.M) continue;
+#pragma unroll
+      for (int i = 0; i < FN; i += 2) {
+        const int c = it.n0 + (wn * FN + i) * 16 + 8 * (lane >> 4);
+        if (c >= p.N) continue;
+        const bool swap = lane >= 32;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = swap ? acc[i + 1][j][e] : acc[i][j][e];
+          v[4 + e] = swap ? acc[i][j][e] : acc[i + 1][j][e];
+        }
+        if constexpr (DROP) {
+          const Words w = philox(c / 8, row, kTagDropout, p.index, seed);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = ((w.w[e / 2] >> (16 * (e & 1))) & 0xffffu) >= args.drop ? v[e] * args.drop_scale : 0.f;
+        }
+        T* o = out + row * p.ld + c;
+        if (whole) {
+          store8nt(o, v);
+        } else if (args.vec && c + 8 <= p.N) {
+          if (args.accumulate) {
+            float w[8];
+            load8(o, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = w[e] + v[e];
+          }
+          store8(o, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e < p.N) store_out(o + e, args.accumulate ? load_out(o + e) + v[e] : v[e]);
+        }
+      }
+    }
+  }
+}
+
+constexpr int kCUs = 256;
+
+template <int ODT, int TM, int TN, int NST, int PER_CU, bool DROP>
+hipError_t launch_tile(const MxGemmArgs& a, hipStream_t s) {
+  constexpr int WM = 2, WN = 2, NW = WM * WN;
+  using OpN = Operand<TN, NW, 0>;
+  using OpM = Operand<TM, NW, 1>;
+  constexpr int lds = NST * (OpN::kBytes + OpM::kBytes + OpN::kScales + OpM::kScales);
+  static_assert(lds * PER_CU <= 160 * 1024, "LDS");
+  auto* k = &k_mx_gemm<ODT, TM, TN, WM, WN, NST, PER_CU, DROP>;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_mx_gemm<ODT, TM, TN, WM, WN, NST>), dim3(static_cast<uint32_t>(blocks)),
-                     dim3(64 * NW), lds, s, a);
+  const int blocks = a.items < kCUs * PER_CU ? a.items : kCUs * PER_CU;
+  hipLaunchKernelGGL(k, dim3(blocks), dim3(64 * NW), lds, s, a);
   return hipGetLastError();
 }
 
+template <int ODT, bool DROP>
+hipError_t launch_drop(const MxGemmArgs& a, int tile_m, hipStream_t s) {
+  return tile_m == 256 ? launch_tile<ODT, 256, 128, 3, 2, DROP>(a, s)
+                       : launch_tile<ODT, 128, 128, 3, 3, DROP>(a, s);
+}
+
+// Sum of the partial products of a split contraction, in the order of the
+// splits; eight columns a thread.
 template <int ODT>
-hipError_t launch_odt(const MxGemmArgs& a, int tile, int64_t blocks, hipStream_t s) {
-  return launch_tile<ODT, 128, 128, 2, 2, 4>(a, blocks, s);
+__global__ __launch_bounds__(256) void k_mx_reduce(MxReduceArgs args) {
+  using T = typename std::conditional<ODT == kBF16, uint16_t, float>::type;
+  const int g = find_in_list(args.base, args.n, blockIdx.x);
+  const MxReduce& p = args.p[g];
+  const uint32_t t = (blockIdx.x - args.base[g]) * 256 + threadIdx.x;
+  const uint32_t per_row = p.ldp / 8;
+  const uint32_t row = t / per_row, c = (t % per_row) * 8;
+  if (row >= static_cast<uint32_t>(p.M)) return;
+  const float* in = p.in + static_cast<int64_t>(row) * p.ldp + c;
+  float v[8];
+  load8(in, v);
+  for (int s = 1; s < p.splits; ++s) {
+    float w[8];
+    load8(in + s * p.stride, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += w[e];
+  }
+  if (args.drop) {
+    const Words w = philox(c / 8, row, kTagDropout, p.index, seed_of(args.drop_seed));
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = ((w.w[e / 2] >> (16 * (e & 1))) & 0xffffu) >= args.drop ? v[e] * args.drop_scale : 0.f;
+  }
+  T* o = static_cast<T*>(p.out) + row * p.ld + c;
+  if (p.vec && c + 8 <= static_cast<uint32_t>(p.N)) {
+    if (args.accumulate) {
+      float w[8];
+      load8(o, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = w[e] + v[e];
+    }
+    store8(o, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < static_cast<uint32_t>(p.N)) store_out(o + e, args.accumulate ? load_out(o + e) + v[e] : v[e]);
+  }
+}
+
+// At most 16 rows of x, quantised on the way, times b: the waves of a block
+// take the steps of 128 columns in turn for R row tiles of b and join their
+// sums in LDS in wave order.  Of a step a lane loads eight consecutive
+// elements of x (16 lanes a row, so that the loads are whole lines), four lanes
+// share a block of 32, and the codes pass through LDS to the lane that feeds
+// them to the matrix instruction.  H: groups of four rows of x (1 or 4).
+template <int XDT, int ODT, int NW, int R, int U, int H>
+__global__ __launch_bounds__(64 * NW) void k_mx_rows(MxRowsArgs a) {
+  using X = typename std::conditional<XDT == kBF16, uint16_t, float>::type;
+  using T = typename std::conditional<ODT == kBF16, uint16_t, float>::type;
+  __shared__ __attribute__((aligned(16))) uint32_t xcodes[NW][256], xscales[NW][64];
+  __shared__ f32x4_t part[NW][R][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rt0 = blockIdx.x * R, rt = (a.N + 15) / 16, st = (a.N + 63) / 64;
+  const int kt = (a.K + kMxTileK - 1) / kMxTileK;
+  f32x4_t acc[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  constexpr int NQ = XDT == kBF16 ? 1 : 2;   // 16-byte loads of eight elements
+  const int row = lane >> 4, ch = lane & 15;
+  struct Step {
+    i32x4_t w[R];
+    uint32_t ws;
+    u32x4_t x[H][NQ];
+  };
+  auto load = [&](Step& s, int k) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int t = rt0 + i < rt ? rt0 + i : rt - 1;
+      s.w[i] = *glb(reinterpret_cast<const i32x4_t*>(a.bc + (static_cast<int64_t>(k) * rt + t) * kMxTileBytes) + lane);
+    }
+    s.ws = *glb(reinterpret_cast<const uint32_t*>(a.bs + (static_cast<int64_t>(k) * st + (rt0 >> 2)) * kMxScaleBytes) + lane);
+    const int c = k * kMxTileK + ch * 8;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) s.x[h][q] = u32x4_t{0, 0, 0, 0};
+      const int r = 4 * h + row;
+      if (4 * h >= a.M || r >= a.M) continue;
+      const X* p = static_cast<const X*>(a.x) + static_cast<int64_t>(r) * a.ldx + c;
+      if (a.vec && c + 8 <= a.K) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) s.x[h][q] = *glb(reinterpret_cast<const u32x4_t*>(p) + q);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < a.K) {
+            if constexpr (XDT == kBF16) s.x[h][0][e / 2] |= static_cast<uint32_t>(*glb(p + e)) << (16 * (e & 1));
+            else s.x[h][e / 4][e & 3] = __float_as_uint(*glb(p + e));
+          }
+      }
+    }
+  };
+  auto multiply = [&](const Step& s) {
+    uint32_t byte[H], code[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      byte[h] = scale_byte(max_quad(top_of<XDT, NQ * 4>(reinterpret_cast<const uint32_t*>(s.x[h]))));
+      if constexpr (XDT == kBF16) code[h] = encode8_near(s.x[h][0], byte[h]);
+      else code[h] = encode8_near(reinterpret_cast<const float*>(s.x[h]), byte[h]);
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int slot = (ch >> 2) * 16 + 4 * h + row;
+      xcodes[wave][slot * 4 + (ch & 3)] = code[h];
+      if ((ch & 3) == 0) xscales[wave][slot] = byte[h];
+    }
+    // only this wave's own part of LDS, which it reads in order
+    __builtin_amdgcn_wave_barrier();
+    const i32x4_t xq = *reinterpret_cast<const i32x4_t*>(&xcodes[wave][lane * 4]);
+    const int xs = static_cast<int>(xscales[wave][lane]);
+    __builtin_amdgcn_wave_barrier();
+    const int sw = static_cast<int>(s.ws >> (8 * (rt0 & 3)));
+    unrolled(std::make_integer_sequence<int, R>{}, [&](auto I) {
+      constexpr int i = decltype(I)::value;
+      acc[i] = mfma4<i, 0>(s.w[i], xq, acc[i], sw, xs);
+    });
+  };
+  for (int k0 = wave; k0 < kt; k0 += NW * U) {
+    Step s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u * NW < kt) load(s[u], k0 + u * NW);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u * NW < kt) multiply(s[u]);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  // result (row m, column 4 g + e of tile i) is element e of lane 16 g + m
+  for (int t = threadIdx.x; t < R * 256; t += 64 * NW) {
+    const int i = t >> 8, m = (t >> 4) & 15, col = t & 15;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) s += part[w][i][(col >> 2) * 16 + m][col & 3];
+    const int n = (rt0 + i) * 16 + col;
+    if (m < a.M && n < a.N) store_out(static_cast<T*>(a.out) + m * a.ldo + n, s);
+  }
+}
+
+template <int XDT, int ODT, int NW, int R, int U>
+void launch_rows_of(const MxRowsArgs& a, hipStream_t s) {
+  const dim3 grid(((a.N + 15) / 16 + R - 1) / R), block(64 * NW);
+  if (a.M <= 4) hipLaunchKernelGGL((k_mx_rows<XDT, ODT, NW, R, U, 1>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_mx_rows<XDT, ODT, NW, R, U, 4>), grid, block, 0, s, a);
+}
+
+// Row tiles of b a block and waves along the contraction, measured on MI355X
+// with b from memory, us (4 tiles x 8 waves | 1 x 16 | 1 x 8):
+//   1 x 2560 x 10240 (x rows, K, b rows): 5.2 | 5.9 | 5.4;  16 rows 6.6 | 11.2 | 8.7
+//   1 x 10240 x 2560: 10.0 | 6.2 | 8.9;  13 rows 14.4 | 10.6 | 13.2
+//   1 x 768 x 768: 2.5 | 2.1 | 2.0;  16 x 768 x 2304: 3.6 | 3.2 | 3.1
+// Many rows of b amortise x; a long contraction with few of them needs the waves.
+template <int XDT, int ODT>
+hipError_t launch_rows(const MxRowsArgs& a, hipStream_t s) {
+  if (a.N >= 8192) launch_rows_of<XDT, ODT, 8, 4, 1>(a, s);
+  else if (a.K >= 4096) launch_rows_of<XDT, ODT, 16, 1, 2>(a, s);
+  else launch_rows_of<XDT, ODT, 8, 1, 1>(a, s);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_mx_gemm(const MxGemmArgs& a, int odt, int tile, int64_t blocks, hipStream_t s) {
-  return odt == kBF16 ? launch_odt<kBF16>(a, tile, blocks, s) : launch_odt<kF32>(a, tile, blocks, s);
+hipError_t launch_mx_gemm(const MxGemmArgs& a, int odt, int tile_m, hipStream_t s) {
+  if (odt == kBF16) return a.drop ? launch_drop<kBF16, true>(a, tile_m, s) : launch_drop<kBF16, false>(a, tile_m, s);
+  return a.drop ? launch_drop<kF32, true>(a, tile_m, s) : launch_drop<kF32, false>(a, tile_m, s);
+}
+
+hipError_t launch_mx_rows(const MxRowsArgs& a, int xdt, int odt, hipStream_t s) {
+  if (xdt == kBF16) return odt == kBF16 ? launch_rows<kBF16, kBF16>(a, s) : launch_rows<kBF16, kF32>(a, s);
+  return odt == kBF16 ? launch_rows<kF32, kBF16>(a, s) : launch_rows<kF32, kF32>(a, s);
+}
+
+hipError_t launch_mx_reduce(const MxReduceArgs& a, int odt, int64_t blocks, hipStream_t s) {
+  const dim3 grid(static_cast<uint32_t>(blocks));
+  if (odt == kBF16) hipLaunchKernelGGL((k_mx_reduce<kBF16>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_mx_reduce<kF32>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace muon

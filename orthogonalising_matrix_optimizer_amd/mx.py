@@ -5,19 +5,22 @@ matrices, the linear layer with its gradients, and dropout whose mask is a
 function of a seed and is never stored.  The number format and the random
 numbers are stated in include/muon.h.  As in the rest of the package all
 computation runs in the HIP library; this module allocates outputs and passes
-pointers with the current stream of the tensors' device.
+pointers with the current stream of the tensors' device.  Descriptors are
+packed as bytes (a call on a single token costs less than its launches).
 """
 from __future__ import annotations
 
-import contextlib
-import ctypes
-from typing import List, NamedTuple, Optional, Sequence, Tuple, Union
+from struct import Struct
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
 from . import _lib
 
 _DT = {torch.bfloat16: _lib.MUON_BF16, torch.float32: _lib.MUON_F32}
+_MAT, _MX = "Pqqqii", "PPqq"      # muon_mat, muon_mx
+_MAT1, _MX1 = Struct(_MAT), Struct(_MX)
+_SPLIT = _lib.CODES["MUON_E_WORKSPACE"]
 
 Seed = Union[int, torch.Tensor]
 
@@ -26,20 +29,15 @@ class MX4:
     """A rows x cols matrix in 4 bits (blocks of 32 along the columns share a scale).
 
     `data` holds codes and scales in the order in which the matrix
-    instructions read them; use mx_dequantize for values."""
+    instructions read them; use dequantize() for values.  The matrices that
+    one call returns for a list share an allocation."""
 
-    __slots__ = ("data", "rows", "cols", "c")
+    __slots__ = ("buffer", "offset", "rows", "cols", "desc")
 
-    def __init__(self, rows: int, cols: int, device):
-        lib = _lib.load()
-        codes = int(lib.muon_mx_codes_bytes(rows, cols))
-        if codes == 0 and rows * cols != 0:
-            raise ValueError(f"no 4-bit matrix of shape {rows} x {cols}")
-        self.data = torch.empty(codes + int(lib.muon_mx_scales_bytes(rows, cols)), dtype=torch.uint8,
-                                device=device)
-        self.rows, self.cols = rows, cols
-        p = self.data.data_ptr()
-        self.c = _lib.MuonMX(p if codes else None, p + codes if codes else None, rows, cols)
+    def __init__(self, buffer: torch.Tensor, offset: int, rows: int, cols: int):
+        self.buffer, self.offset, self.rows, self.cols = buffer, offset, rows, cols
+        p = buffer.data_ptr() + offset
+        self.desc = (p, p + _codes_bytes(rows, cols), rows, cols) if rows and cols else (0, 0, rows, cols)
 
     @property
     def shape(self) -> Tuple[int, int]:
@@ -47,11 +45,15 @@ class MX4:
 
     @property
     def device(self) -> torch.device:
-        return self.data.device
+        return self.buffer.device
 
     @property
     def nbytes(self) -> int:
-        return self.data.numel()
+        return _mx_bytes(self.rows, self.cols)
+
+    @property
+    def data(self) -> torch.Tensor:
+        return self.buffer[self.offset:self.offset + self.nbytes]
 
     def dequantize(self, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         return mx_dequantize(self, dtype)
@@ -74,73 +76,129 @@ class MXSaved(NamedTuple):
     dropout_seed: Optional[Seed]
 
 
+# Storage sizes (muon_mx_codes_bytes, muon_mx_scales_bytes): tiles of 16 x 128
+# codes in 1024 bytes, of 64 x 128 elements' scales in 256.
+def _codes_bytes(rows: int, cols: int) -> int:
+    return -(-rows // 16) * -(-cols // 128) * 1024
+
+
+def _mx_bytes(rows: int, cols: int) -> int:
+    return (-(-rows // 16) * 1024 + -(-rows // 64) * 256) * -(-cols // 128)
+
+
+def _new_mx(shapes, device):
+    """MX4 matrices of the shapes, in one allocation."""
+    if len(shapes) == 1:
+        r, c = shapes[0]
+        return [MX4(torch.empty(_mx_bytes(r, c), dtype=torch.uint8, device=device), 0, r, c)]
+    at = [0]
+    for r, c in shapes:
+        at.append(at[-1] + _mx_bytes(r, c))
+    buf = torch.empty(at[-1], dtype=torch.uint8, device=device)
+    return [MX4(buf, o, r, c) for o, (r, c) in zip(at, shapes)]
+
+
+def _new_dense(shapes, dtype, device):
+    """Dense tensors of the shapes; equally wide ones share an allocation."""
+    if dtype not in _DT:
+        raise ValueError(f"unsupported dtype {dtype}")
+    width = shapes[0][1]
+    if len(shapes) > 1 and all(c == width for _, c in shapes):
+        rows = [r for r, _ in shapes]
+        return list(torch.empty((sum(rows), width), dtype=dtype, device=device).split(rows))
+    return [torch.empty(s, dtype=dtype, device=device) for s in shapes]
+
+
 def _rows_of(t: torch.Tensor) -> torch.Tensor:
     """`t` as a 2-D view of its rows (last dimension)."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"expected a tensor, got {type(t).__name__}")
-    if not t.is_cuda:
-        raise ValueError("tensors must be on a GPU")
-    if t.dtype not in _DT:
-        raise ValueError(f"unsupported dtype {t.dtype}")
     if t.dim() == 2:
         return t
     if t.dim() == 0:
         raise ValueError("tensors must have at least one dimension")
+    c = t.shape[-1]
     try:
-        return t.view(t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1])
+        return t.view(t.numel() // c if c else 0, c)
     except RuntimeError:
         raise ValueError("the leading dimensions must be one run of evenly spaced rows") from None
 
 
-def _mat(t: torch.Tensor):
-    """(ptr, rows, cols, pitch, dtype) of a 2-D tensor whose rows are contiguous."""
+def _mat(t: torch.Tensor, dev: torch.device):
+    """muon_mat of a 2-D tensor whose rows are contiguous."""
+    d = _DT.get(t.dtype)
+    if d is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    if t.device != dev:
+        raise ValueError("operands must be on one device" if t.is_cuda else "tensors must be on a GPU")
     r, c = t.shape
-    if c > 1 and r > 0 and t.stride(1) != 1:
-        raise ValueError("rows must be contiguous (stride(-1) == 1)")
-    ld = t.stride(0) if r > 1 else c
-    if r > 1 and c > 0 and ld < c:
+    s, one = t.stride()
+    if r == 1 or c == 0:
+        s = c
+    elif s < c and r:
         raise ValueError("rows must not overlap (an expanded tensor needs .contiguous())")
-    return _lib.MuonMat(t.data_ptr() or None, r, c, ld, _DT[t.dtype], 0)
+    if one != 1 and c > 1 and r:
+        raise ValueError("rows must be contiguous (stride(-1) == 1)")
+    return t.data_ptr(), r, c, s, d, 0
 
 
-def _array(kind, items):
-    return (kind * len(items))(*items)
+def _mats(ts, dev) -> bytes:
+    if len(ts) == 1:
+        return _MAT1.pack(*_mat(ts[0], dev))
+    return Struct(_MAT * len(ts)).pack(*[v for t in ts for v in _mat(t, dev)])
 
 
-def _seed(opt_field: str, opt: "_lib.MXOptions", seed: Seed, device) -> None:
-    if isinstance(seed, torch.Tensor):
-        if seed.dtype != torch.int64 or seed.numel() != 1 or seed.device != device:
-            raise ValueError("a seed tensor holds one int64 on the operands' device")
-        setattr(opt, opt_field + "_dev", seed.data_ptr())
-    else:
-        setattr(opt, opt_field, int(seed) & 0xFFFFFFFFFFFFFFFF)
-
-
-def _same_device(items) -> torch.device:
-    dev = items[0].device
-    for t in items[1:]:
-        if t.device != dev:
+def _mxs(ms, dev) -> bytes:
+    for m in ms:
+        if not isinstance(m, MX4):
+            raise ValueError(f"expected an MX4, got {type(m).__name__}")
+        if m.buffer.device != dev:
             raise ValueError("operands must be on one device")
+    if len(ms) == 1:
+        return _MX1.pack(*ms[0].desc)
+    return Struct(_MX * len(ms)).pack(*[v for m in ms for v in m.desc])
+
+
+def _gpu(dev: torch.device) -> torch.device:
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a GPU")
     return dev
 
 
-def _on(device):
-    """Context that makes `device` current (free when it already is)."""
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _call(name: str, dev: torch.device, *args) -> int:
+    """A library call on `dev` and its current stream; the status."""
+    i = dev.index
+    if torch._C._cuda_getDevice() == i:
+        return getattr(_lib.load(), name)(*args, torch._C._cuda_getCurrentRawStream(i))
+    with torch.cuda.device(i):
+        return getattr(_lib.load(), name)(*args, torch._C._cuda_getCurrentRawStream(i))
 
 
-def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _set_seed(opt: "_lib.MXOptions", field: str, seed: Seed, dev) -> None:
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype != torch.int64 or seed.numel() != 1 or seed.device != dev:
+            raise ValueError("a seed tensor holds one int64 on the operands' device")
+        setattr(opt, field + "_dev", seed.data_ptr())
+    else:
+        setattr(opt, field, int(seed) & 0xFFFFFFFFFFFFFFFF)
 
 
-def _drop_options(opt, dropout: float, seed: Optional[Seed], device) -> None:
+def _options(dev, seed: Optional[Seed] = None, dropout: float = 0.0,
+             dropout_seed: Optional[Seed] = None, accumulate: bool = False):
+    """muon_mx_options, or None for the defaults."""
+    if seed is None and not dropout and not accumulate:
+        return None
+    opt = _lib.MXOptions()
+    opt.accumulate = int(bool(accumulate))
+    if seed is not None:
+        opt.stochastic = 1
+        _set_seed(opt, "seed", seed, dev)
     if dropout:
-        if seed is None:
+        if dropout_seed is None:
             raise ValueError("dropout needs a seed")
         opt.dropout = float(dropout)
-        _seed("dropout_seed", opt, seed, device)
+        _set_seed(opt, "dropout_seed", dropout_seed, dev)
+    return opt
 
 
 def mx_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], transpose: Union[bool, str] = False,
@@ -159,31 +217,32 @@ def mx_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], transpose: Union
     xs = [_rows_of(t) for t in ([x] if single else x)]
     if not xs:
         return []
-    dev = _same_device(xs)
-    lib = _lib.load()
+    dev = _gpu(xs[0].device)
+    mats = _mats(xs, dev)
     both = transpose == "both"
+    rows = cols = None
     if out is None:
-        rows = [MX4(t.shape[0], t.shape[1], dev) for t in xs] if transpose is not True else None
-        cols = [MX4(t.shape[1], t.shape[0], dev) for t in xs] if transpose is not False else None
+        if transpose is not True:
+            rows = _new_mx([tuple(t.shape) for t in xs], dev)
+        if transpose is not False:
+            cols = _new_mx([tuple(t.shape)[::-1] for t in xs], dev)
     else:
         outs = [out] if single else list(out)
         if len(outs) != len(xs):
             raise ValueError(f"{len(xs)} matrices, {len(outs)} outputs")
-        rows = [o[0] if both else o for o in outs] if transpose is not True else None
-        cols = [o[1] if both else o for o in outs] if transpose is not False else None
-        _same_device(xs + (rows or []) + (cols or []))
-    opt = _lib.MXOptions()
-    if seed is not None:
-        opt.stochastic = 1
-        _seed("seed", opt, seed, dev)
-    _drop_options(opt, dropout, dropout_seed, dev)
-    with _on(dev):
-        code = lib.muon_mx_quantize(_array(_lib.MuonMat, [_mat(t) for t in xs]),
-                                    _array(_lib.MuonMX, [m.c for m in rows]) if rows else None,
-                                    _array(_lib.MuonMX, [m.c for m in cols]) if cols else None,
-                                    len(xs), opt, _stream(dev))
-    _lib.check(code, "muon_mx_quantize")
-    res = [MXPair(a, b) for a, b in zip(rows, cols)] if both else rows or cols
+        if transpose is not True:
+            rows = [o[0] if both else o for o in outs]
+        if transpose is not False:
+            cols = [o[1] if both else o for o in outs]
+    code = _call("muon_mx_quantize", dev, mats, _mxs(rows, dev) if rows else None,
+                 _mxs(cols, dev) if cols else None, len(xs),
+                 _options(dev, seed, dropout, dropout_seed))
+    if code:
+        _lib.check(code, "muon_mx_quantize")
+    if both:
+        res = [MXPair(a, b) for a, b in zip(rows, cols)]
+    else:
+        res = rows if rows else cols
     return res[0] if single else res
 
 
@@ -194,21 +253,19 @@ def mx_dequantize(m: Union[MX4, Sequence[MX4]], dtype: torch.dtype = torch.bfloa
     ms = [m] if single else list(m)
     if not ms:
         return []
-    dev = _same_device(ms)
+    dev = ms[0].device
+    mxs = _mxs(ms, dev)
     if out is None:
-        if dtype not in _DT:
-            raise ValueError(f"unsupported dtype {dtype}")
-        outs = [torch.empty(q.rows, q.cols, dtype=dtype, device=dev) for q in ms]
+        outs = _new_dense([q.shape for q in ms], dtype, dev)
     else:
         outs = [_rows_of(t) for t in ([out] if single else out)]
         if len(outs) != len(ms):
             raise ValueError(f"{len(ms)} matrices, {len(outs)} outputs")
-        _same_device(ms + outs)
-    with _on(dev):
-        code = _lib.load().muon_mx_dequantize(_array(_lib.MuonMX, [q.c for q in ms]),
-                                              _array(_lib.MuonMat, [_mat(t) for t in outs]), len(ms),
-                                              _stream(dev))
-    _lib.check(code, "muon_mx_dequantize")
+    code = _call("muon_mx_dequantize", dev, mxs, _mats(outs, dev), len(ms))
+    if code:
+        _lib.check(code, "muon_mx_dequantize")
+    if out is not None:
+        return out
     return outs[0] if single else outs
 
 
@@ -222,38 +279,33 @@ def mx_matmul(a: Union[MX4, Sequence[MX4]], b: Union[MX4, Sequence[MX4]],
     elements as dropout() does."""
     single = isinstance(a, MX4)
     la, lb = ([a], [b]) if single else (list(a), list(b))
-    if len(la) != len(lb):
-        raise ValueError(f"{len(la)} left and {len(lb)} right operands")
+    n = len(la)
+    if n != len(lb):
+        raise ValueError(f"{n} left and {len(lb)} right operands")
     if not la:
         return []
-    dev = _same_device(la + lb)
+    dev = la[0].device
+    ca, cb = _mxs(la, dev), _mxs(lb, dev)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        if dtype not in _DT:
-            raise ValueError(f"unsupported dtype {dtype}")
-        outs = [torch.empty(p.rows, q.rows, dtype=dtype, device=dev) for p, q in zip(la, lb)]
+        outs = _new_dense([(p.rows, q.rows) for p, q in zip(la, lb)], dtype, dev)
     else:
         outs = [_rows_of(t) for t in ([out] if single else out)]
-        if len(outs) != len(la):
-            raise ValueError(f"{len(la)} products, {len(outs)} outputs")
-        _same_device(la + outs)
-    _matmul(la, lb, outs, dev, accumulate, dropout, dropout_seed)
+        if len(outs) != n:
+            raise ValueError(f"{n} products, {len(outs)} outputs")
+    co = _mats(outs, dev)
+    opt = _options(dev, None, dropout, dropout_seed, accumulate)
+    code = _call("muon_mx_matmul", dev, ca, cb, co, n, opt, None, 0)
+    if code == _SPLIT:   # the list's contraction is split: give it room for the partial products
+        ws = torch.empty(int(_lib.load().muon_mx_matmul_workspace_bytes(ca, cb, n)), dtype=torch.uint8,
+                         device=dev)
+        code = _call("muon_mx_matmul", dev, ca, cb, co, n, opt, ws.data_ptr(), ws.numel())
+    if code:
+        _lib.check(code, "muon_mx_matmul")
     if out is not None:
         return out
     return outs[0] if single else outs
-
-
-def _matmul(la, lb, outs, dev, accumulate=False, dropout=0.0, dropout_seed=None) -> None:
-    opt = _lib.MXOptions()
-    opt.accumulate = int(bool(accumulate))
-    _drop_options(opt, dropout, dropout_seed, dev)
-    with _on(dev):
-        code = _lib.load().muon_mx_matmul(_array(_lib.MuonMX, [m.c for m in la]),
-                                          _array(_lib.MuonMX, [m.c for m in lb]),
-                                          _array(_lib.MuonMat, [_mat(t) for t in outs]), len(outs),
-                                          opt, _stream(dev))
-    _lib.check(code, "muon_mx_matmul")
 
 
 def mx_linear(x: torch.Tensor, w: MX4, save: bool = False, dropout: float = 0.0,
@@ -263,12 +315,24 @@ def mx_linear(x: torch.Tensor, w: MX4, save: bool = False, dropout: float = 0.0,
     dropout(x, dropout, dropout_seed).  With `save` returns (y, saved), saved
     being what mx_linear_grad needs: the input's transpose in 4 bits."""
     x2 = _rows_of(x)
-    if x2.shape[1] != w.cols:
-        raise ValueError(f"x has {x2.shape[1]} features, the layer takes {w.cols}")
-    q = mx_quantize(x2, "both" if save else False, dropout=dropout, dropout_seed=dropout_seed)
-    y = mx_matmul(q[0] if save else q, w, dtype=x.dtype)
-    y = y.view(*x.shape[:-1], w.rows)
-    return (y, MXSaved(q[1], float(dropout), dropout_seed)) if save else y
+    rows, cols = x2.shape
+    if cols != w.cols:
+        raise ValueError(f"x has {cols} features, the layer takes {w.cols}")
+    if not save and not dropout and rows <= _lib.MX_FEW_ROWS:
+        dev = _gpu(x.device)
+        y = torch.empty((rows, w.rows), dtype=x.dtype, device=dev)
+        code = _call("muon_mx_matmul_rows", dev, _MAT1.pack(*_mat(x2, dev)), _mxs([w], dev),
+                     _MAT1.pack(*_mat(y, dev)))
+        if code:
+            _lib.check(code, "muon_mx_matmul_rows")
+        saved = None
+    else:
+        q = mx_quantize(x2, "both" if save else False, dropout=dropout, dropout_seed=dropout_seed)
+        y = mx_matmul(q[0] if save else q, w, dtype=x.dtype)
+        saved = MXSaved(q[1], float(dropout), dropout_seed) if save else None
+    if x.dim() != 2:
+        y = y.view(*x.shape[:-1], w.rows)
+    return (y, saved) if save else y
 
 
 def mx_linear_grad(dy: torch.Tensor, w_t: Optional[MX4], saved: MXSaved, seed: Optional[Seed] = None,
@@ -285,12 +349,13 @@ def mx_linear_grad(dy: torch.Tensor, w_t: Optional[MX4], saved: MXSaved, seed: O
     if w_t is not None and (w_t.cols != dy2.shape[1] or w_t.rows != saved.x_t.rows):
         raise ValueError(f"w_t is {w_t.rows} x {w_t.cols}, not {saved.x_t.rows} x {dy2.shape[1]}")
     q = mx_quantize(dy2, True if w_t is None else "both", seed=seed)
-    dx = None
-    dy_t = q
+    dx, dy_t = None, q
     if w_t is not None:
         dy_t = q[1]
         dx = mx_matmul(q[0], w_t, dtype=dy.dtype, dropout=saved.dropout,
-                       dropout_seed=saved.dropout_seed).view(*dy.shape[:-1], w_t.rows)
+                       dropout_seed=saved.dropout_seed)
+        if dy.dim() != 2:
+            dx = dx.view(*dy.shape[:-1], w_t.rows)
     if pair:
         return dx, (dy_t, saved.x_t)
     return dx, mx_matmul(dy_t, saved.x_t, dtype=grad_dtype, out=out, accumulate=accumulate)
@@ -301,14 +366,19 @@ def dropout(x: torch.Tensor, p: float, seed: Seed, out: Optional[torch.Tensor] =
     1 / (1 - p), or zeroed; the same call on a gradient is the backward pass.
     `out` may be x itself."""
     x2 = _rows_of(x)
-    res = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    if out is not None and out.shape != x.shape:
-        raise ValueError(f"out is {tuple(out.shape)}, not {tuple(x.shape)}")
-    o2 = _rows_of(res)
-    dev = _same_device([x2, o2])
+    dev = _gpu(x.device)
+    if out is None:
+        res = o2 = torch.empty(x2.shape, dtype=x.dtype, device=dev)
+        if x.dim() != 2:
+            res = o2.view(x.shape)
+    else:
+        if out.shape != x.shape:
+            raise ValueError(f"out is {tuple(out.shape)}, not {tuple(x.shape)}")
+        res, o2 = out, _rows_of(out)
     opt = _lib.MXOptions()
-    _seed("seed", opt, seed, dev)
-    with _on(dev):
-        code = _lib.load().muon_dropout(_mat(x2), _mat(o2), p, opt.seed, opt.seed_dev, _stream(dev))
-    _lib.check(code, "muon_dropout")
+    _set_seed(opt, "seed", seed, dev)
+    code = _call("muon_dropout", dev, _MAT1.pack(*_mat(x2, dev)), _MAT1.pack(*_mat(o2, dev)), p,
+                 opt.seed, opt.seed_dev)
+    if code:
+        _lib.check(code, "muon_dropout")
     return res
