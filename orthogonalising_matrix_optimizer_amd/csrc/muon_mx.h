@@ -35,7 +35,9 @@ constexpr uint32_t kMxNan = 255;   // scale byte of a block that is NaN
 constexpr uint32_t kTagDropout = 0x44524F50u, kTagRound = 0x53523430u, kTagRoundT = 0x53523431u;
 
 // Descriptors travel as kernel arguments (under the 4 KiB limit), so the calls
-// need no device table, no workspace for one and no staging memory.
+// need no device table, no workspace for one and no staging memory.  A call on
+// one matrix passes a list of one: kernel arguments are read from host memory,
+// and small ones keep the shortest launches short.
 constexpr int kMxMaxList = 36;
 
 // A seed given by value, or by the device address of one (then read by the
@@ -45,6 +47,35 @@ struct MxSeed {
   const uint64_t* dev;   // or null
 };
 
+struct MxDrop {
+  uint32_t threshold;    // in steps of 2^-16; 0: no dropout
+  float scale;
+  MxSeed seed;
+};
+
+// Arguments of a grouped launch: what all matrices share, the matrices, and
+// the first block (work item) of each.
+template <class Common, class Mat, int CAP>
+struct MxList {
+  static constexpr int kCap = CAP;
+  Common c;
+  int32_t n;
+  int32_t _pad;
+  Mat m[CAP];
+  uint32_t base[CAP];
+};
+
+template <class Common, class Mat, int CAP>
+MxList<Common, Mat, 1> list_of_one(const MxList<Common, Mat, CAP>& a) {
+  MxList<Common, Mat, 1> o;
+  o.c = a.c;
+  o.n = 1;
+  o._pad = 0;
+  o.m[0] = a.m[0];
+  o.base[0] = a.base[0];
+  return o;
+}
+
 struct MxQuantMat {
   const void* in;        // rows x cols, row pitch ld elements
   uint8_t* codes;        // the matrix in 4 bits, or null
@@ -53,18 +84,15 @@ struct MxQuantMat {
   uint8_t* scales_t;
   int64_t ld;
   int32_t rows, cols;
-  int32_t vec;           // rows allow 16-byte access
   int32_t index;         // place in the caller's list (fourth counter word)
+  int32_t _pad;
 };
-struct MxQuantArgs {
-  MxQuantMat m[kMxMaxList];
-  uint32_t base[kMxMaxList];   // first block of each matrix
-  int32_t n;
-  uint32_t drop;               // dropout threshold in steps of 2^-16, 0: none
-  float drop_scale;
-  MxSeed seed;                 // stochastic rounding
-  MxSeed drop_seed;
+struct MxQuantCommon {
+  MxSeed seed;           // stochastic rounding
+  MxDrop drop;
 };
+template <int CAP> using MxQuantList = MxList<MxQuantCommon, MxQuantMat, CAP>;
+using MxQuantArgs = MxQuantList<kMxMaxList>;
 
 struct MxDequantMat {
   const uint8_t* codes;
@@ -72,15 +100,10 @@ struct MxDequantMat {
   void* out;
   int64_t ld;
   int32_t rows, cols;
-  int32_t vec;
-  int32_t _pad;
 };
-struct MxDequantArgs {
-  MxDequantMat m[kMxMaxList];
-  uint32_t base[kMxMaxList];
-  int32_t n;
-  int32_t _pad;
-};
+struct MxDequantCommon {};
+template <int CAP> using MxDequantList = MxList<MxDequantCommon, MxDequantMat, CAP>;
+using MxDequantArgs = MxDequantList<kMxMaxList>;
 
 // out (M x N) = a (M x K) * b (N x K)^T, or with a split contraction the
 // partial products over `chunk` code tiles each, `stride` elements apart
@@ -98,17 +121,13 @@ struct MxProduct {
   int32_t tiles;           // output tiles; item = split * tiles + tile
   int32_t index;           // place in the caller's list
 };
-struct MxGemmArgs {
-  MxProduct p[kMxMaxList];
-  uint32_t base[kMxMaxList];   // first work item of each product
-  int32_t n;
+struct MxGemmCommon {
+  MxDrop drop;
   int32_t items;           // work items of the launch
   int32_t accumulate;      // out += product
-  int32_t vec;             // every out allows 16-byte access
-  uint32_t drop;
-  float drop_scale;
-  MxSeed drop_seed;
 };
+template <int CAP> using MxGemmList = MxList<MxGemmCommon, MxProduct, CAP>;
+using MxGemmArgs = MxGemmList<kMxMaxList>;
 
 // out (M x N) = sum over the splits of the partial products (fp32, row pitch
 // ldp, `stride` elements apart)
@@ -119,29 +138,26 @@ struct MxReduce {
   int64_t stride;
   int32_t M, N, ldp;
   int32_t splits;
-  int32_t vec;
   int32_t index;
+  int32_t _pad;
 };
-struct MxReduceArgs {
-  MxReduce p[kMxMaxList];
-  uint32_t base[kMxMaxList];
-  int32_t n;
+struct MxReduceCommon {
+  MxDrop drop;
   int32_t accumulate;
-  uint32_t drop;
-  float drop_scale;
-  MxSeed drop_seed;
+  int32_t _pad;
 };
+template <int CAP> using MxReduceList = MxList<MxReduceCommon, MxReduce, CAP>;
+using MxReduceArgs = MxReduceList<kMxMaxList>;
+
+static_assert(sizeof(MxQuantArgs) <= 4096 && sizeof(MxGemmArgs) <= 4096 && sizeof(MxReduceArgs) <= 4096 &&
+              sizeof(MxDequantArgs) <= 4096, "kernel argument limit");
 
 struct MxDropArgs {
   const void* in;
   void* out;
   int64_t ldi, ldo;
   int32_t rows, cols;
-  int32_t vec;             // both rows allow 16-byte access
-  uint32_t drop;
-  float scale;
-  int32_t _pad;
-  MxSeed seed;
+  MxDrop drop;
 };
 
 // out (M x N) = x (M x K, not in 4 bits) * b (N x K)^T, M <= 16
@@ -152,7 +168,7 @@ struct MxRowsArgs {
   void* out;
   int64_t ldx, ldo;
   int32_t M, N, K;
-  int32_t vec;             // rows of x allow 16-byte access
+  int32_t _pad;
 };
 
 hipError_t launch_mx_quantize(const MxQuantArgs& a, int dt, bool rows, bool cols, bool stochastic,
@@ -166,6 +182,6 @@ hipError_t launch_dropout(const MxDropArgs& a, int dt, int64_t blocks, hipStream
 
 // Work of one block of each kernel (the host sizes the grids with these).
 constexpr int kMxQuantTile = 128;              // quantise, dequantise: square tile edge
-constexpr int kDropItems = 1024;               // dropout: groups of 8 elements per block
+constexpr int kDropItems = 256;                // dropout: groups of 8 elements per block
 
 }  // namespace muon

@@ -21,7 +21,9 @@ namespace {
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 // the products address a panel of 256 rows with 32-bit offsets
 constexpr int64_t kMaxCols = int64_t(1) << 24;
-constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;   // of 256 threads: the grid limit
+// a grid has fewer than 2^32 threads: blocks of 256, and of the quantiser's 1024
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;
+constexpr int64_t kMaxQuantBlocks = (int64_t(1) << 22) - 1;
 
 int esize(int dt) { return dt == MUON_BF16 ? 2 : 4; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -48,10 +50,6 @@ int check_mx(const muon_mx& m) {
   if (reinterpret_cast<uintptr_t>(m.codes) % 16 || reinterpret_cast<uintptr_t>(m.scales) % 16)
     return MUON_E_ALIGN;
   return MUON_OK;
-}
-
-bool vec_ok(const muon_mat& m) {
-  return reinterpret_cast<uintptr_t>(m.ptr) % 16 == 0 && (m.ld * esize(m.dtype)) % 16 == 0;
 }
 
 // Memory that a call reads or writes: `width` bytes in every `pitch` from lo
@@ -112,12 +110,14 @@ bool conflict(std::vector<Span>& v) {
 }
 
 // Dropout probability -> threshold in steps of 2^-16 and the kept elements' factor.
-int drop_of(float p, uint32_t* thr, float* scale) {
+int drop_of(float p, uint64_t seed, const uint64_t* dev, MxDrop* d) {
   if (!(p >= 0.f && p < 1.f)) return MUON_E_HPARAM;
   const uint32_t t = uint32_t(std::floor(double(p) * 65536.0 + 0.5));
   if (t >= 65536) return MUON_E_HPARAM;
-  *thr = t;
-  *scale = 65536.f / float(65536 - t);
+  if (reinterpret_cast<uintptr_t>(dev) % 8) return MUON_E_ALIGN;
+  d->threshold = t;
+  d->scale = 65536.f / float(65536 - t);
+  d->seed = {seed, t ? dev : nullptr};
   return MUON_OK;
 }
 
@@ -202,10 +202,6 @@ ProductPlan plan_products(const muon_mx* a, const muon_mx* b, int n) {
   return p;
 }
 
-int seed_ok(const uint64_t* dev) {
-  return reinterpret_cast<uintptr_t>(dev) % 8 ? MUON_E_ALIGN : MUON_OK;
-}
-
 }  // namespace
 
 extern "C" {
@@ -232,11 +228,12 @@ int muon_mx_quantize(const muon_mat* in, const muon_mx* out, const muon_mx* out_
   muon_mx_options o;
   muon_mx_default_options(&o);
   if (opt) o = *opt;
-  uint32_t thr = 0;
-  float scale = 1.f;
+  MxQuantArgs a;
+  std::memset(&a, 0, sizeof(a));
   int rc;
-  if ((rc = drop_of(o.dropout, &thr, &scale)) != MUON_OK) return rc;
-  if ((rc = seed_ok(o.seed_dev)) != MUON_OK || (rc = seed_ok(o.dropout_seed_dev)) != MUON_OK) return rc;
+  if ((rc = drop_of(o.dropout, o.dropout_seed, o.dropout_seed_dev, &a.c.drop)) != MUON_OK) return rc;
+  if (reinterpret_cast<uintptr_t>(o.seed_dev) % 8) return MUON_E_ALIGN;
+  a.c.seed = {o.seed, o.stochastic ? o.seed_dev : nullptr};
   std::vector<Span> spans;
   for (int i = 0; i < n; ++i) {
     if ((rc = check_dense(in[i])) != MUON_OK) return rc;
@@ -252,20 +249,14 @@ int muon_mx_quantize(const muon_mat* in, const muon_mx* out, const muon_mx* out_
       if (out_t[i].rows != c || out_t[i].cols != r) return MUON_E_SHAPE;
       add_span(spans, out_t[i], true);
     }
-    if (ceil_div(r, kMxQuantTile) * ceil_div(c, kMxQuantTile) > kMaxBlocks) return MUON_E_SHAPE;
+    if (ceil_div(r, kMxQuantTile) * ceil_div(c, kMxQuantTile) > kMaxQuantBlocks) return MUON_E_SHAPE;
     add_span(spans, in[i], false);
   }
-  if (o.stochastic) add_span(spans, o.seed_dev, sizeof(uint64_t), false);
-  if (thr) add_span(spans, o.dropout_seed_dev, sizeof(uint64_t), false);
+  add_span(spans, a.c.seed.dev, sizeof(uint64_t), false);
+  add_span(spans, a.c.drop.seed.dev, sizeof(uint64_t), false);
   if (conflict(spans)) return MUON_E_ALIAS;
 
   hipStream_t s = static_cast<hipStream_t>(stream);
-  MxQuantArgs a;
-  std::memset(&a, 0, sizeof(a));
-  a.drop = thr;
-  a.drop_scale = scale;
-  a.seed = {o.seed, o.stochastic ? o.seed_dev : nullptr};
-  a.drop_seed = {o.dropout_seed, thr ? o.dropout_seed_dev : nullptr};
   int64_t blocks = 0;
   auto flush = [&]() {
     if (a.n && launch_mx_quantize(a, in[0].dtype, out, out_t, o.stochastic, blocks, s) != hipSuccess)
@@ -277,7 +268,7 @@ int muon_mx_quantize(const muon_mat* in, const muon_mx* out, const muon_mx* out_
   for (int i = 0; i < n; ++i) {
     const int64_t nb = ceil_div(in[i].rows, kMxQuantTile) * ceil_div(in[i].cols, kMxQuantTile);
     if (nb == 0) continue;
-    if (a.n == kMxMaxList || blocks + nb > kMaxBlocks)
+    if (a.n == kMxMaxList || blocks + nb > kMaxQuantBlocks)
       if ((rc = int(flush())) != MUON_OK) return rc;
     MxQuantMat& m = a.m[a.n];
     std::memset(&m, 0, sizeof(m));
@@ -285,7 +276,6 @@ int muon_mx_quantize(const muon_mat* in, const muon_mx* out, const muon_mx* out_
     m.ld = in[i].ld;
     m.rows = int32_t(in[i].rows);
     m.cols = int32_t(in[i].cols);
-    m.vec = vec_ok(in[i]);
     m.index = i;
     if (out) {
       m.codes = static_cast<uint8_t*>(out[i].codes);
@@ -341,7 +331,6 @@ int muon_mx_dequantize(const muon_mx* in, const muon_mat* out, int32_t n, void* 
     m.ld = out[i].ld;
     m.rows = int32_t(in[i].rows);
     m.cols = int32_t(in[i].cols);
-    m.vec = vec_ok(out[i]);
     a.base[a.n++] = uint32_t(blocks);
     blocks += nb;
   }
@@ -374,10 +363,8 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
   MxReduceArgs red;
   std::memset(&red, 0, sizeof(red));
   int rc;
-  if ((rc = drop_of(o.dropout, &red.drop, &red.drop_scale)) != MUON_OK) return rc;
-  if ((rc = seed_ok(o.dropout_seed_dev)) != MUON_OK) return rc;
-  red.accumulate = o.accumulate != 0;
-  red.drop_seed = {o.dropout_seed, red.drop ? o.dropout_seed_dev : nullptr};
+  if ((rc = drop_of(o.dropout, o.dropout_seed, o.dropout_seed_dev, &red.c.drop)) != MUON_OK) return rc;
+  red.c.accumulate = o.accumulate != 0;
   std::vector<Span> spans;
   for (int i = 0; i < n; ++i) {
     if ((rc = check_mx(a[i])) != MUON_OK || (rc = check_mx(b[i])) != MUON_OK ||
@@ -397,7 +384,7 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
     if (reinterpret_cast<uintptr_t>(workspace) % 16) return MUON_E_ALIGN;
     add_span(spans, workspace, plan.bytes, true);
   }
-  if (red.drop) add_span(spans, o.dropout_seed_dev, sizeof(uint64_t), false);
+  add_span(spans, red.c.drop.seed.dev, sizeof(uint64_t), false);
   if (conflict(spans)) return MUON_E_ALIAS;
   hipStream_t s = static_cast<hipStream_t>(stream);
 
@@ -405,19 +392,15 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
   for (const bool split : {false, true}) {
     int64_t items = 0, blocks = 0;
     g.n = red.n = 0;
-    g.vec = 1;
-    g.accumulate = split ? 0 : red.accumulate;
-    g.drop = split ? 0 : red.drop;
-    g.drop_scale = red.drop_scale;
-    g.drop_seed = red.drop_seed;
+    g.c.accumulate = split ? 0 : red.c.accumulate;
+    g.c.drop = split ? MxDrop{} : red.c.drop;
     auto flush = [&]() {
-      g.items = int32_t(items);
+      g.c.items = int32_t(items);
       if (g.n && launch_mx_gemm(g, split ? int(kF32) : out[0].dtype, plan.tile_m, s) != hipSuccess)
         return MUON_E_HIP;
       if (split && g.n && launch_mx_reduce(red, out[0].dtype, blocks, s) != hipSuccess)
         return MUON_E_HIP;
       g.n = red.n = 0;
-      g.vec = 1;
       items = blocks = 0;
       return MUON_OK;
     };
@@ -430,7 +413,7 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
       const int64_t nb = split ? ceil_div(M * (round_up(N, 8) / 8), 256) : 0;
       if (g.n == kMxMaxList || items + tiles * splits > kMaxBlocks || blocks + nb > kMaxBlocks)
         if ((rc = int(flush())) != MUON_OK) return rc;
-      MxProduct& p = g.p[g.n];
+      MxProduct& p = g.m[g.n];
       p.ac = static_cast<const uint8_t*>(a[i].codes);
       p.as = static_cast<const uint8_t*>(a[i].scales);
       p.bc = static_cast<const uint8_t*>(b[i].codes);
@@ -442,7 +425,7 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
       p.tiles = int32_t(tiles);
       p.index = i;
       if (split) {
-        MxReduce& r = red.p[g.n];
+        MxReduce& r = red.m[g.n];
         r.ldp = int32_t(round_up(N, 8));
         r.stride = M * r.ldp;
         r.in = reinterpret_cast<const float*>(static_cast<char*>(workspace) + plan.offset[i]);
@@ -451,7 +434,6 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
         r.M = p.M;
         r.N = p.N;
         r.splits = int32_t(splits);
-        r.vec = vec_ok(out[i]);
         r.index = i;
         red.base[g.n] = uint32_t(blocks);
         red.n = g.n + 1;
@@ -462,7 +444,6 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
         p.out = out[i].ptr;
         p.ld = out[i].ld;
         p.stride = 0;
-        g.vec = g.vec && vec_ok(out[i]);
       }
       g.base[g.n++] = uint32_t(items);
       items += tiles * splits;
@@ -501,7 +482,6 @@ int muon_mx_matmul_rows(const muon_mat* x, const muon_mx* b, const muon_mat* out
   a.M = int32_t(x->rows);
   a.N = int32_t(b->rows);
   a.K = int32_t(x->cols);
-  a.vec = x->cols == 0 || vec_ok(*x);
   return launch_mx_rows(a, x->dtype, out->dtype, static_cast<hipStream_t>(stream)) == hipSuccess
              ? MUON_OK : MUON_E_HIP;
 } catch (...) {   // an allocation of the host's failed
@@ -514,7 +494,7 @@ int muon_dropout(const muon_mat* in, const muon_mat* out, float p, uint64_t seed
   MxDropArgs a;
   std::memset(&a, 0, sizeof(a));
   int rc;
-  if ((rc = drop_of(p, &a.drop, &a.scale)) != MUON_OK || (rc = seed_ok(seed_dev)) != MUON_OK) return rc;
+  if ((rc = drop_of(p, seed, seed_dev, &a.drop)) != MUON_OK) return rc;
   if ((rc = check_dense(*in)) != MUON_OK || (rc = check_dense(*out)) != MUON_OK) return rc;
   if (in->dtype != out->dtype) return MUON_E_DTYPE;
   if (in->rows != out->rows || in->cols != out->cols) return MUON_E_SHAPE;
@@ -525,7 +505,7 @@ int muon_dropout(const muon_mat* in, const muon_mat* out, float p, uint64_t seed
   add_span(spans, *out, true);
   // in place is allowed: every element is read by the lane that writes it
   if (!(in->ptr == out->ptr && in->ld == out->ld)) add_span(spans, *in, false);
-  if (a.drop) add_span(spans, seed_dev, sizeof(uint64_t), false);
+  add_span(spans, a.drop.seed.dev, sizeof(uint64_t), false);
   if (conflict(spans)) return MUON_E_ALIAS;
   a.in = in->ptr;
   a.out = out->ptr;
@@ -533,8 +513,6 @@ int muon_dropout(const muon_mat* in, const muon_mat* out, float p, uint64_t seed
   a.ldo = out->ld;
   a.rows = int32_t(in->rows);
   a.cols = int32_t(in->cols);
-  a.vec = vec_ok(*in) && vec_ok(*out);
-  a.seed = {seed, a.drop ? seed_dev : nullptr};
   return launch_dropout(a, in->dtype, blocks, static_cast<hipStream_t>(stream)) == hipSuccess
              ? MUON_OK : MUON_E_HIP;
 } catch (...) {   // an allocation of the host's failed

@@ -50,11 +50,78 @@ __device__ __forceinline__ Words philox(uint32_t c0, uint32_t c1, uint32_t c2, u
 
 // Matrix of a grouped launch that block b belongs to: the bases are in rising
 // order, so it is the number of bases at or below b, counted across a wave.
-__device__ __forceinline__ int find_in_list(const uint32_t* base, int n, uint32_t b) {
-  if (n == 1) return 0;
+template <class L>
+__device__ __forceinline__ int find_in_list(const L& l, uint32_t b) {
+  if constexpr (L::kCap == 1) return 0;
   const int lane = threadIdx.x & 63;
-  const bool below = lane < n && base[lane < n ? lane : 0] <= b;
+  const bool below = lane < l.n && l.base[lane < l.n ? lane : 0] <= b;
   return __builtin_amdgcn_readfirstlane(__popcll(__ballot(below))) - 1;
+}
+
+// 16 bytes at any element's address: the hardware needs no more alignment.
+typedef u32x4_t u32x4_any __attribute__((aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+template <class T>
+__device__ __forceinline__ u32x4_t load16b(const T* p) {
+  return *reinterpret_cast<const GAS u32x4_any*>(glb(p));
+}
+template <class T>
+__device__ __forceinline__ void store16b(T* p, u32x4_t q) {
+  *reinterpret_cast<GAS u32x4_any*>(glb(p)) = q;
+}
+// Output written past the caches' keeping (operand panels stay in L2).
+template <class T>
+__device__ __forceinline__ void stream16b(T* p, u32x4_t q) {
+  __builtin_nontemporal_store(q, reinterpret_cast<GAS u32x4_any*>(glb(p)));
+}
+
+// Eight consecutive elements of a row as fp32, and back.
+__device__ __forceinline__ void widen8(u32x4_t q, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(q[i] << 16);
+    v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ u32x4_t narrow8(const float* v) {
+  return u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+}
+__device__ __forceinline__ u32x4_t bits4(const float* v) {
+  return u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float* v) { widen8(load16b(p), v); }
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const u32x4_t a = load16b(p), b = load16b(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = __uint_as_float(a[i]);
+    v[4 + i] = __uint_as_float(b[i]);
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float* v) { store16b(p, narrow8(v)); }
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  store16b(p, bits4(v));
+  store16b(p + 4, bits4(v + 4));
+}
+__device__ __forceinline__ void stream8(uint16_t* p, const float* v) { stream16b(p, narrow8(v)); }
+__device__ __forceinline__ void stream8(float* p, const float* v) {
+  stream16b(p, bits4(v));
+  stream16b(p + 4, bits4(v + 4));
+}
+__device__ __forceinline__ float load1(const uint16_t* p) {
+  return __uint_as_float(static_cast<uint32_t>(*glb(p)) << 16);
+}
+__device__ __forceinline__ float load1(const float* p) { return *glb(p); }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *glb(p) = f2bf(v); }
+__device__ __forceinline__ void store1(float* p, float v) { *glb(p) = v; }
+
+// Eight elements of the dropout mask applied: element i of group g of a row.
+__device__ __forceinline__ void drop8(float* v, uint32_t g, uint32_t row, uint32_t index,
+                                      uint64_t seed, const MxDrop& d) {
+  const Words w = philox(g, row, kTagDropout, index, seed);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = ((w.w[i / 2] >> (16 * (i & 1))) & 0xffffu) >= d.threshold ? v[i] * d.scale : 0.f;
 }
 
 // Eight codes of a block in a dword, element i in bits 4 i, rounded to nearest

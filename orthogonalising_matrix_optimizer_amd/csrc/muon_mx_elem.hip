@@ -9,6 +9,8 @@
 // the exponent exactly when the significand exceeds 1.5.
 #pragma clang fp contract(off)
 
+#include <type_traits>
+
 #include "muon_common.h"
 #include "muon_device.h"
 #include "muon_mx.h"
@@ -17,235 +19,214 @@
 namespace muon {
 namespace {
 
-// Code of |t| <= 6 (t already divided by the scale) rounded stochastically:
-// up where 256 times the fraction of the step exceeds r + 1/2.
-__device__ __forceinline__ uint32_t code_sr(float t, uint32_t r) {
-  const float a = fabsf(t);
-  const float inv = a >= 4.f ? 0.5f : a >= 2.f ? 1.f : 2.f;
-  const uint32_t base = a >= 4.f ? 4u : a >= 2.f ? 2u : 0u;
-  const float q = a * inv, low = floorf(q);
-  const uint32_t up = (q - low) * 256.f > static_cast<float>(r) + 0.5f;
-  return static_cast<uint32_t>(low) + up + base + ((__float_as_uint(t) >> 28) & 8u);
-}
+constexpr int kQuantThreads = 1024;
 
-// 16 loaded elements of a row as fp32 (exact for both types).
+// Elements of a row as they are in memory: a dword holds two bf16 or one fp32.
+template <int DT> struct Elem;
+template <> struct Elem<kBF16> {
+  using S = uint16_t;
+  static constexpr int kPerDword = 2;
+};
+template <> struct Elem<kF32> {
+  using S = float;
+  static constexpr int kPerDword = 1;
+};
+
+// Sixteen elements of a row from column c on; zeros past the last column.
 template <int DT>
-__device__ __forceinline__ void load16(const void* row, int c0, int cols, bool vec, float* v) {
-  if constexpr (DT == kBF16) {
-    const uint16_t* p = static_cast<const uint16_t*>(row) + c0;
-    if (vec && c0 + 16 <= cols) {
+__device__ __forceinline__ void load16(const typename Elem<DT>::S* row, int c, int cols, uint32_t* q) {
+  constexpr int NV = 4 / Elem<DT>::kPerDword;   // 16-byte loads
+  if (c + 16 <= cols) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4_t q = *glb(reinterpret_cast<const u32x4_t*>(p) + h);
+    for (int h = 0; h < NV; ++h) {
+      const u32x4_t v = load16b(row + c + h * (16 / NV));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[8 * h + 2 * i] = __uint_as_float(q[i] << 16);
-          v[8 * h + 2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        v[i] = c0 + i < cols ? __uint_as_float(static_cast<uint32_t>(*glb(p + i)) << 16) : 0.f;
+      for (int i = 0; i < 4; ++i) q[4 * h + i] = v[i];
     }
   } else {
-    const float* p = static_cast<const float*>(row) + c0;
-    if (vec && c0 + 16 <= cols) {
+    // every load is in range, so that all are in flight at once
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const u32x4_t q = *glb(reinterpret_cast<const u32x4_t*>(p) + h);
+    for (int i = 0; i < 4 * NV; ++i) q[i] = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 * h + i] = __uint_as_float(q[i]);
+    for (int i = 0; i < 16; ++i) {
+      const int at = c + i < cols ? c + i : cols - 1;
+      if constexpr (DT == kBF16) {
+        const uint32_t v = *glb(row + at);
+        q[i / 2] |= (c + i < cols ? v : 0u) << (16 * (i & 1));
+      } else {
+        const uint32_t v = __float_as_uint(*glb(row + at));
+        q[i] = c + i < cols ? v : 0u;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = c0 + i < cols ? *glb(p + i) : 0.f;
     }
   }
 }
 
+// Dropout of sixteen elements (columns c .. c + 15, c a multiple of 16), rounded
+// to the element type as a stored result would be.
 template <int DT>
-__device__ __forceinline__ float rounded(float v) {
-  if constexpr (DT == kBF16) return __uint_as_float(static_cast<uint32_t>(f2bf(v)) << 16);
-  else return v;
-}
-
-// Dropout of 16 consecutive elements of a row (c0 a multiple of 16): eight
-// 16-bit numbers a counter.
-template <int DT>
-__device__ __forceinline__ void drop16(float* v, uint32_t row, uint32_t c0, uint32_t index,
-                                       uint64_t seed, uint32_t thr, float scale) {
+__device__ __forceinline__ void drop16(uint32_t* q, uint32_t row, uint32_t c, uint32_t index,
+                                       uint64_t seed, const MxDrop& d) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const Words w = philox(c0 / 8 + h, row, kTagDropout, index, seed);
+    float v[8];
+    if constexpr (DT == kBF16) {
+      widen8(u32x4_t{q[4 * h], q[4 * h + 1], q[4 * h + 2], q[4 * h + 3]}, v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t r = (w.w[i / 2] >> (16 * (i & 1))) & 0xffffu;
-      v[8 * h + i] = r >= thr ? rounded<DT>(v[8 * h + i] * scale) : 0.f;
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(q[8 * h + i]);
+    }
+    drop8(v, c / 8 + h, row, index, seed, d);
+    if constexpr (DT == kBF16) {
+      const u32x4_t n = narrow8(v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[4 * h + i] = n[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[8 * h + i] = __float_as_uint(v[i]);
     }
   }
 }
 
-// Eight codes of a block in a dword, element i in bits 4 i.
-template <bool SR>
-__device__ __forceinline__ uint32_t encode8(const float* v, uint32_t byte, const uint32_t* r8) {
-  if constexpr (SR) {
-    uint32_t out = 0;
-    // 2^(127 - byte), an ordinary number: a finite block's byte is at most 253
-    const float inv = __uint_as_float((254u - byte) << 23);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      out |= code_sr(v[i] * inv, (r8[i / 4] >> (8 * (i & 3))) & 255u) << (4 * i);
-    return byte == kMxNan ? 0u : out;
+// Code of x 2^-e (magnitude at most 6) rounded stochastically: up where 256
+// times the fraction of the step exceeds r + 1/2.
+//
+// bf16: x is scaled to 2^-126 times its place on the grid, where the grid's
+// steps are fp32 bit patterns a multiple of 2^22 apart (the subnormal grid
+// falls on the fp32 subnormals), so adding the random byte below bit 22 carries
+// into the code exactly when the element goes up, the threshold (2 r + 1) /
+// 512 of a step being ((255 - r) << 14) + 0x1FFF below the next step.  What
+// scaling rounds away of a bf16's eight digits is below every threshold.
+template <int DT>
+__device__ __forceinline__ uint32_t code_sr(float x, uint32_t byte, uint32_t not_r) {
+  if constexpr (DT == kBF16) {
+    const uint32_t s = __float_as_uint(__builtin_ldexpf(x, 1 - static_cast<int>(byte))) + 0x1FFFu +
+                       (not_r << 14);
+    return ((s >> 22) & 7u) | ((s >> 28) & 8u);
   } else {
-    return encode8_near(v, byte);
+    // 2^(127 - byte), an ordinary number: a finite block's byte is at most 253
+    const float t = x * __uint_as_float((254u - byte) << 23), a = fabsf(t);
+    const float inv = a >= 4.f ? 0.5f : a >= 2.f ? 1.f : 2.f;
+    const uint32_t base = a >= 4.f ? 4u : a >= 2.f ? 2u : 0u;
+    const float q = a * inv, low = floorf(q);
+    const uint32_t up = (q - low) * 256.f > static_cast<float>(255u - not_r) + 0.5f;
+    return static_cast<uint32_t>(low) + up + base + ((__float_as_uint(t) >> 28) & 8u);
   }
 }
 
-// One 128 x 128 tile of the input per block of four waves.  A lane reads 16
-// consecutive elements of a row, so a block of 32 is a pair of lanes; waves 0
-// and 1 take the tile's first 64 rows, waves 2 and 3 the others, each wave
-// eight rows of every 16-row tile, so a lane ends up with the scale dword of
-// its four row tiles.  For the transpose the tile passes through LDS, and a
-// lane takes two columns of 32 rows.
-template <int DT, bool ROWS, bool COLS, bool SR>
-__global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs args) {
-  constexpr int T = kMxQuantTile;
-  using S = typename std::conditional<DT == kBF16, uint16_t, float>::type;
-  __shared__ __attribute__((aligned(16))) S tile[COLS ? T * T : 16];
-  const int g = find_in_list(args.base, args.n, blockIdx.x);
+// Eight codes of a block in a dword, element i in bits 4 i; r8: their random
+// bytes.  (q: dwords of the eight elements.)
+template <int DT, bool SR>
+__device__ __forceinline__ uint32_t encode8(const uint32_t* q, uint32_t byte, const uint32_t* r8) {
+  if constexpr (SR) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float x;
+      if constexpr (DT == kBF16) x = __uint_as_float(i & 1 ? q[i / 2] & 0xffff0000u : q[i / 2] << 16);
+      else x = __uint_as_float(q[i]);
+      out |= code_sr<DT>(x, byte, (~r8[i / 4] >> (8 * (i & 3))) & 255u) << (4 * i);
+    }
+    return byte == kMxNan ? 0u : out;
+  } else if constexpr (DT == kBF16) {
+    return encode8_near(u32x4_t{q[0], q[1], q[2], q[3]}, byte);
+  } else {
+    return encode8_near(reinterpret_cast<const float*>(q), byte);
+  }
+}
+
+// One 128 x 128 tile of the input per block of sixteen waves.  A lane reads 16
+// consecutive elements of one row, so a block of 32 is a pair of lanes; for the
+// transpose the tile passes through LDS and half of the lanes take 32 rows of a
+// column each.  Short work per lane keeps small matrices quick and costs large
+// ones nothing: with four waves of four times the work, both orientations of
+// bf16 on MI355X, us (4 | 16 waves): 1 x 2560 3.8 | 3.1; 1024 x 1024 4.1 | 3.4;
+// 8192 x 2560 14.8 | 14.5; 16384 x 10240 98.8 | 96.5 (5.3 TB/s, as a copy).
+// Stochastically 1001 x 777 of fp32 17.0 | 9.8; 16384 x 10240 of bf16 151 | 157:
+// there the generator's products and the roundings are the bound.
+template <class Args, int DT, bool ROWS, bool COLS, bool SR>
+__global__ __launch_bounds__(kQuantThreads) void k_mx_quantize(Args args) {
+  constexpr int T = kMxQuantTile, PD = Elem<DT>::kPerDword, ND = 16 / PD;   // dwords of 16 elements
+  using S = typename Elem<DT>::S;
+  static_assert(kQuantThreads * 16 == T * T, "a lane takes 16 elements");
+  __shared__ __attribute__((aligned(16))) uint32_t tile[COLS ? T * T / PD : 4];
+  const int g = find_in_list(args, blockIdx.x);
   const MxQuantMat& m = args.m[g];
   const uint32_t b = blockIdx.x - args.base[g];
   const int kt = (m.cols + T - 1) / T;               // tiles along the columns
   const int tr = b / kt, tc = b % kt;
   const int t = threadIdx.x;
-  const int ch = t & 7;                              // 16-column chunk of the tile
-  const int c0 = tc * T + ch * 16;
-  const int r16 = (t >> 3) & 15;                     // row inside a 16-row tile
-  const uint64_t seed = SR ? seed_of(args.seed) : 0;
-  const uint64_t dseed = args.drop ? seed_of(args.drop_seed) : 0;
-  uint32_t sdw = 0;
+  const int ch = t & 7, lr = t >> 3;                 // 16-column chunk and row of the tile
+  const int c0 = tc * T + ch * 16, r = tr * T + lr;
+  uint32_t q[ND];
+  load16<DT>(static_cast<const S*>(m.in) + static_cast<int64_t>(r < m.rows ? r : m.rows - 1) * m.ld,
+             c0, m.cols, q);
+  const uint64_t seed = SR ? seed_of(args.c.seed) : 0;
+  if (r >= m.rows)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int lr = (t >> 7) * 64 + i * 16 + r16;
-    const int r = tr * T + lr;
-    float v[16];
-    if (r < m.rows) {
-      const char* row = static_cast<const char*>(m.in) + static_cast<int64_t>(r) * m.ld * sizeof(S);
-      load16<DT>(row, c0, m.cols, m.vec, v);
-      if (args.drop) drop16<DT>(v, r, c0, m.index, dseed, args.drop, args.drop_scale);
-    } else {
+    for (int j = 0; j < ND; ++j) q[j] = 0;
+  if (args.c.drop.threshold) drop16<DT>(q, r, c0, m.index, seed_of(args.c.drop.seed), args.c.drop);
+  if constexpr (COLS) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = 0.f;
-    }
-    if constexpr (COLS) {
-      if constexpr (DT == kBF16) {
-        u32x4_t q[2];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          q[j / 4][j & 3] = (__float_as_uint(v[2 * j]) >> 16) | (__float_as_uint(v[2 * j + 1]) & 0xffff0000u);
-        *reinterpret_cast<u32x4_t*>(tile + lr * T + ch * 16) = q[0];
-        *reinterpret_cast<u32x4_t*>(tile + lr * T + ch * 16 + 8) = q[1];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<float4*>(tile + lr * T + ch * 16 + 4 * j) =
-              make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      }
-    }
-    if constexpr (ROWS) {
-      const uint32_t byte = scale_byte(max_pair(top_of<kF32, 16>(reinterpret_cast<const uint32_t*>(v))));
-      Words w = {{0, 0, 0, 0}};
-      if constexpr (SR) w = philox(c0 / 16, r, kTagRound, m.index, seed);
-      uint2 code;
-      code.x = encode8<SR>(v, byte, w.w);
-      code.y = encode8<SR>(v + 8, byte, w.w + 2);
-      const int rt = tr * (T / 16) + (t >> 7) * 4 + i;   // 16-row tile
-      if (rt * 16 < m.rows) {
-        const int64_t o = (static_cast<int64_t>(tc) * ((m.rows + 15) / 16) + rt) * kMxTileBytes +
-                          ((ch >> 1) * 16 + r16) * 16 + (ch & 1) * 8;
-        *glb(reinterpret_cast<uint2*>(m.codes + o)) = code;
-      }
-      sdw |= byte << (8 * i);
-    }
+    for (int j = 0; j < ND; j += 4)
+      *reinterpret_cast<u32x4_t*>(tile + (lr * T + ch * 16) / PD + j) =
+          u32x4_t{q[j], q[j + 1], q[j + 2], q[j + 3]};
   }
   if constexpr (ROWS) {
-    const int sg = tr * 2 + (t >> 7);                    // 64-row scale tile
-    if ((ch & 1) == 0 && sg * 64 < m.rows)
-      *glb(reinterpret_cast<uint32_t*>(m.scales + (static_cast<int64_t>(tc) * ((m.rows + 63) / 64) + sg) * kMxScaleBytes +
-                                       ((ch >> 1) * 16 + r16) * 4)) = sdw;
+    const uint32_t byte = scale_byte(max_pair(top_of<DT, ND>(q)));
+    Words w = {{0, 0, 0, 0}};
+    if constexpr (SR) w = philox(c0 / 16, r, kTagRound, m.index, seed);
+    uint2 code;
+    code.x = encode8<DT, SR>(q, byte, w.w);
+    code.y = encode8<DT, SR>(q + ND / 2, byte, w.w + 2);
+    const int rt = r >> 4, slot = (ch >> 1) * 16 + (r & 15);
+    if (rt * 16 < m.rows) {
+      const int64_t o = (static_cast<int64_t>(tc) * ((m.rows + 15) / 16) + rt) * kMxTileBytes;
+      *glb(reinterpret_cast<uint2*>(m.codes + o + slot * 16 + (ch & 1) * 8)) = code;
+      if ((ch & 1) == 0)
+        *glb(m.scales + (static_cast<int64_t>(tc) * ((m.rows + 63) / 64) + (r >> 6)) * kMxScaleBytes +
+             slot * 4 + (rt & 3)) = static_cast<uint8_t>(byte);
+    }
   }
   if constexpr (COLS) {
     __syncthreads();
-    const int cp = t & 63, rb = t >> 6;                  // column pair, block of 32 rows
-    float v[2][32];
+    if (t >= 4 * T) return;
+    const int rb = t >> 7, lc = t & 127;                 // block of 32 rows, column
+    uint32_t v[32 / PD];
+    if constexpr (DT == kBF16) {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(tile) + rb * 32 * T + lc;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if constexpr (DT == kBF16) {
-        const uint32_t q = *reinterpret_cast<const uint32_t*>(tile + (rb * 32 + j) * T + 2 * cp);
-        v[0][j] = __uint_as_float(q << 16);
-        v[1][j] = __uint_as_float(q & 0xffff0000u);
-      } else {
-        const float2 q = *reinterpret_cast<const float2*>(tile + (rb * 32 + j) * T + 2 * cp);
-        v[0][j] = q.x;
-        v[1][j] = q.y;
-      }
+      for (int j = 0; j < 32; j += 2) v[j / 2] = h[j * T] | static_cast<uint32_t>(h[(j + 1) * T]) << 16;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = tile[(rb * 32 + j) * T + lc];
     }
-    const int rtt = (m.cols + 15) / 16, sgt = (m.cols + 63) / 64;   // the transpose's row and scale tiles
-    uint32_t sb = 0;
+    const int c = tc * T + lc;                           // row of the transpose
+    const uint32_t byte = scale_byte(top_of<DT, 32 / PD>(v));
+    u32x4_t code;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int c = tc * T + 2 * cp + e;                 // row of the transpose
-      const uint32_t byte = scale_byte(top_of<kF32, 32>(reinterpret_cast<const uint32_t*>(v[e])));
-      sb |= byte << (8 * e);
-      u32x4_t code;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        Words w = {{0, 0, 0, 0}};
-        if constexpr (SR) w = philox((tr * T + rb * 32) / 16 + h, c, kTagRoundT, m.index, seed);
-        code[2 * h] = encode8<SR>(v[e] + 16 * h, byte, w.w);
-        code[2 * h + 1] = encode8<SR>(v[e] + 16 * h + 8, byte, w.w + 2);
-      }
-      const int rt = c >> 4;
-      if (rt * 16 < m.cols)
-        *glb(reinterpret_cast<u32x4_t*>(m.codes_t + (static_cast<int64_t>(tr) * rtt + rt) * kMxTileBytes +
-                                        (rb * 16 + (c & 15)) * 16)) = code;
+    for (int h = 0; h < 2; ++h) {
+      Words w = {{0, 0, 0, 0}};
+      if constexpr (SR) w = philox((tr * T + rb * 32) / 16 + h, c, kTagRoundT, m.index, seed);
+      code[2 * h] = encode8<DT, SR>(v + 16 / PD * h, byte, w.w);
+      code[2 * h + 1] = encode8<DT, SR>(v + 16 / PD * h + 8 / PD, byte, w.w + 2);
     }
-    // the four columns c, c + 16, c + 32, c + 48 of a scale dword are eight lanes apart
-    const uint32_t s1 = __shfl_down(sb, 8, 64), s2 = __shfl_down(sb, 16, 64), s3 = __shfl_down(sb, 24, 64);
-    const int c = tc * T + 2 * cp;
-    if ((cp & 24) == 0 && (c & ~63) < m.cols) {
-      uint2 d;
-      d.x = (sb & 255) | (s1 & 255) << 8 | (s2 & 255) << 16 | (s3 & 255) << 24;
-      d.y = (sb >> 8) | (s1 >> 8) << 8 | (s2 >> 8) << 16 | (s3 >> 8) << 24;
-      *glb(reinterpret_cast<uint2*>(m.scales_t + (static_cast<int64_t>(tr) * sgt + (c >> 6)) * kMxScaleBytes +
-                                    (rb * 16 + (c & 15)) * 4)) = d;
+    const int rt = c >> 4, slot = rb * 16 + (c & 15);
+    if (rt * 16 < m.cols) {
+      *glb(reinterpret_cast<u32x4_t*>(m.codes_t + (static_cast<int64_t>(tr) * ((m.cols + 15) / 16) + rt) * kMxTileBytes +
+                                      slot * 16)) = code;
+      *glb(m.scales_t + (static_cast<int64_t>(tr) * ((m.cols + 63) / 64) + (c >> 6)) * kMxScaleBytes +
+           slot * 4 + (rt & 3)) = static_cast<uint8_t>(byte);
     }
   }
 }
 
-__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-  uint4 q;
-  q.x = pack_bf16(v[0], v[1]);
-  q.y = pack_bf16(v[2], v[3]);
-  q.z = pack_bf16(v[4], v[5]);
-  q.w = pack_bf16(v[6], v[7]);
-  *glb(reinterpret_cast<u32x4_t*>(p)) = u32x4_t{q.x, q.y, q.z, q.w};
-}
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  *glb(reinterpret_cast<float4*>(p)) = make_float4(v[0], v[1], v[2], v[3]);
-  *glb(reinterpret_cast<float4*>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store1(uint16_t* p, float v) { *glb(p) = f2bf(v); }
-__device__ __forceinline__ void store1(float* p, float v) { *glb(p) = v; }
-
 // A lane turns four bytes (eight codes) into eight consecutive elements of a
 // row, so 16 lanes write 128 consecutive elements.
-template <int DT>
-__global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs args) {
+template <class Args, int DT>
+__global__ __launch_bounds__(256) void k_mx_dequantize(Args args) {
   constexpr int T = kMxQuantTile;
-  using S = typename std::conditional<DT == kBF16, uint16_t, float>::type;
-  const int g = find_in_list(args.base, args.n, blockIdx.x);
+  using S = typename Elem<DT>::S;
+  const int g = find_in_list(args, blockIdx.x);
   const MxDequantMat& m = args.m[g];
   const uint32_t b = blockIdx.x - args.base[g];
   const int kt = (m.cols + T - 1) / T;
@@ -254,99 +235,114 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs args) {
   const int ch = t & 15, r16 = t >> 4;
   const int c = tc * T + ch * 8;
   if (c >= m.cols) return;
+  const int slot = (ch >> 2) * 16 + r16;
+  const int rts = (m.rows + 15) / 16, sgs = (m.rows + 63) / 64;
+  uint32_t codes[T / 16], scales[T / 64];
 #pragma unroll
   for (int i = 0; i < T / 16; ++i) {
-    const int rt = tr * (T / 16) + i, r = rt * 16 + r16;
+    const int rt = tr * (T / 16) + i < rts ? tr * (T / 16) + i : rts - 1;
+    codes[i] = *glb(reinterpret_cast<const uint32_t*>(
+        m.codes + (static_cast<int64_t>(tc) * rts + rt) * kMxTileBytes + slot * 16 + (ch & 3) * 4));
+  }
+#pragma unroll
+  for (int i = 0; i < T / 64; ++i) {
+    const int sg = tr * (T / 64) + i < sgs ? tr * (T / 64) + i : sgs - 1;
+    scales[i] = *glb(reinterpret_cast<const uint32_t*>(
+        m.scales + (static_cast<int64_t>(tc) * sgs + sg) * kMxScaleBytes + slot * 4));
+  }
+#pragma unroll
+  for (int i = 0; i < T / 16; ++i) {
+    const int r = tr * T + i * 16 + r16;
     if (r >= m.rows) return;
-    const int slot = (ch >> 2) * 16 + r16;
-    const uint32_t code = *glb(reinterpret_cast<const uint32_t*>(
-        m.codes + (static_cast<int64_t>(tc) * ((m.rows + 15) / 16) + rt) * kMxTileBytes + slot * 16 + (ch & 3) * 4));
-    const uint32_t byte = *glb(m.scales + (static_cast<int64_t>(tc) * ((m.rows + 63) / 64) + (rt >> 2)) * kMxScaleBytes +
-                               slot * 4 + (rt & 3));
+    const uint32_t byte = (scales[i / 4] >> (8 * (i & 3))) & 255u;
     // 2^(byte - 127) in fp32 (2^-127 is subnormal); 255 is NaN
     const float sc = byte == kMxNan ? __uint_as_float(0x7fc00000u)
                                     : byte ? __uint_as_float(byte << 23) : 0x1p-127f;
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t q = code >> (4 * j);
+      const uint32_t q = codes[i] >> (4 * j);
       // magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 doubled are the digits of this word
       const uint32_t d = (0xC8643210u >> (4 * (q & 7u))) & 15u;
       v[j] = static_cast<float>(d) * 0.5f * sc;
       v[j] = __uint_as_float(__float_as_uint(v[j]) ^ ((q & 8u) << 28));
     }
-    S* row = static_cast<S*>(m.out) + static_cast<int64_t>(r) * m.ld;
-    if (m.vec && c + 8 <= m.cols) {
-      store8(row + c, v);
+    S* o = static_cast<S*>(m.out) + static_cast<int64_t>(r) * m.ld + c;
+    if (c + 8 <= m.cols) {
+      store8(o, v);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (c + j < m.cols) store1(row + c + j, v[j]);
+        if (c + j < m.cols) store1(o + j, v[j]);
     }
   }
 }
 
-// Groups of eight consecutive elements of a row, one counter each.
+// Groups of eight consecutive elements of a row, one counter and one lane each.
 template <int DT>
-__global__ __launch_bounds__(256) void k_dropout(MxDropArgs a) {
-  using S = typename std::conditional<DT == kBF16, uint16_t, float>::type;
-  const int groups = (a.cols + 7) / 8;
-  const int64_t total = static_cast<int64_t>(a.rows) * groups;
-  const uint64_t seed = seed_of(a.seed);
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kDropItems;
-#pragma unroll
-  for (int u = 0; u < kDropItems / 256; ++u) {
-    const int64_t it = first + u * 256 + threadIdx.x;
-    if (it >= total) return;
-    const int r = static_cast<int>(it / groups), c = static_cast<int>(it - static_cast<int64_t>(r) * groups) * 8;
-    const S* in = static_cast<const S*>(a.in) + r * a.ldi + c;
-    S* out = static_cast<S*>(a.out) + r * a.ldo + c;
-    const bool whole = a.vec && c + 8 <= a.cols;
-    float v[8];
-    if (whole) {
-      if constexpr (DT == kBF16) {
-        const u32x4_t q = *glb(reinterpret_cast<const u32x4_t*>(in));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[2 * i] = __uint_as_float(q[i] << 16);
-          v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4_t q = *glb(reinterpret_cast<const u32x4_t*>(in) + h);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[4 * h + i] = __uint_as_float(q[i]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (DT == kBF16) v[i] = c + i < a.cols ? __uint_as_float(static_cast<uint32_t>(*glb(in + i)) << 16) : 0.f;
-        else v[i] = c + i < a.cols ? *glb(in + i) : 0.f;
-      }
+__global__ __launch_bounds__(kDropItems) void k_dropout(MxDropArgs a) {
+  using S = typename Elem<DT>::S;
+  const uint32_t groups = (a.cols + 7) / 8;
+  const uint64_t seed = seed_of(a.drop.seed);
+  // the block's first group (a scalar division), then this lane's
+  const uint64_t first = static_cast<uint64_t>(blockIdx.x) * kDropItems;
+  uint32_t r = static_cast<uint32_t>(first / groups);
+  uint32_t g = static_cast<uint32_t>(first - static_cast<uint64_t>(r) * groups) + threadIdx.x;
+  if (groups >= kDropItems) {
+    if (g >= groups) {
+      g -= groups;
+      ++r;
     }
-    const Words w = philox(c / 8, r, kTagDropout, 0, seed);
+  } else {
+    const uint32_t over = g / groups;
+    g -= over * groups;
+    r += over;
+  }
+  if (r >= static_cast<uint32_t>(a.rows)) return;
+  const int c = g * 8;
+  const S* in = static_cast<const S*>(a.in) + r * a.ldi + c;
+  S* out = static_cast<S*>(a.out) + r * a.ldo + c;
+  const bool whole = c + 8 <= a.cols;
+  float v[8];
+  if (whole) {
+    load8(in, v);
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t q = (w.w[i / 2] >> (16 * (i & 1))) & 0xffffu;
-      v[i] = q >= a.drop ? v[i] * a.scale : 0.f;
-    }
-    if (whole) {
-      store8(out, v);
-    } else {
+    for (int i = 0; i < 8; ++i) v[i] = load1(c + i < a.cols ? in + i : in);
+  }
+  drop8(v, g, r, 0, seed, a.drop);
+  if (whole) {
+    store8(out, v);
+  } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < a.cols) store1(out + i, v[i]);
-    }
+    for (int i = 0; i < 8; ++i)
+      if (c + i < a.cols) store1(out + i, v[i]);
   }
 }
 
-template <int DT, bool SR>
-void quantize_rc(const MxQuantArgs& a, bool rows, bool cols, dim3 grid, hipStream_t s) {
-  if (rows && cols) hipLaunchKernelGGL((k_mx_quantize<DT, true, true, SR>), grid, dim3(256), 0, s, a);
-  else if (rows) hipLaunchKernelGGL((k_mx_quantize<DT, true, false, SR>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_mx_quantize<DT, false, true, SR>), grid, dim3(256), 0, s, a);
+template <class Args, int DT, bool SR>
+void quantize_rc(const Args& a, bool rows, bool cols, dim3 grid, hipStream_t s) {
+  const dim3 block(kQuantThreads);
+  if (rows && cols) hipLaunchKernelGGL((k_mx_quantize<Args, DT, true, true, SR>), grid, block, 0, s, a);
+  else if (rows) hipLaunchKernelGGL((k_mx_quantize<Args, DT, true, false, SR>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_mx_quantize<Args, DT, false, true, SR>), grid, block, 0, s, a);
+}
+
+template <class Args>
+void quantize_dt(const Args& a, int dt, bool rows, bool cols, bool stochastic, dim3 grid, hipStream_t s) {
+  if (dt == kBF16) {
+    if (stochastic) quantize_rc<Args, kBF16, true>(a, rows, cols, grid, s);
+    else quantize_rc<Args, kBF16, false>(a, rows, cols, grid, s);
+  } else {
+    if (stochastic) quantize_rc<Args, kF32, true>(a, rows, cols, grid, s);
+    else quantize_rc<Args, kF32, false>(a, rows, cols, grid, s);
+  }
+}
+
+template <class Args>
+void dequantize_dt(const Args& a, int dt, dim3 grid, hipStream_t s) {
+  if (dt == kBF16) hipLaunchKernelGGL((k_mx_dequantize<Args, kBF16>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_mx_dequantize<Args, kF32>), grid, dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -354,27 +350,22 @@ void quantize_rc(const MxQuantArgs& a, bool rows, bool cols, dim3 grid, hipStrea
 hipError_t launch_mx_quantize(const MxQuantArgs& a, int dt, bool rows, bool cols, bool stochastic,
                               int64_t blocks, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(blocks));
-  if (dt == kBF16) {
-    if (stochastic) quantize_rc<kBF16, true>(a, rows, cols, grid, s);
-    else quantize_rc<kBF16, false>(a, rows, cols, grid, s);
-  } else {
-    if (stochastic) quantize_rc<kF32, true>(a, rows, cols, grid, s);
-    else quantize_rc<kF32, false>(a, rows, cols, grid, s);
-  }
+  if (a.n == 1) quantize_dt(list_of_one(a), dt, rows, cols, stochastic, grid, s);
+  else quantize_dt(a, dt, rows, cols, stochastic, grid, s);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_dequantize(const MxDequantArgs& a, int dt, int64_t blocks, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(blocks));
-  if (dt == kBF16) hipLaunchKernelGGL((k_mx_dequantize<kBF16>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_mx_dequantize<kF32>), grid, dim3(256), 0, s, a);
+  if (a.n == 1) dequantize_dt(list_of_one(a), dt, grid, s);
+  else dequantize_dt(a, dt, grid, s);
   return hipGetLastError();
 }
 
 hipError_t launch_dropout(const MxDropArgs& a, int dt, int64_t blocks, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(blocks));
-  if (dt == kBF16) hipLaunchKernelGGL((k_dropout<kBF16>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_dropout<kF32>), grid, dim3(256), 0, s, a);
+  if (dt == kBF16) hipLaunchKernelGGL((k_dropout<kBF16>), grid, dim3(kDropItems), 0, s, a);
+  else hipLaunchKernelGGL((k_dropout<kF32>), grid, dim3(kDropItems), 0, s, a);
   return hipGetLastError();
 }
 

@@ -8,6 +8,7 @@
 // lane holds the bytes of four row tiles, picked by the instruction's byte
 // select.  b is the instruction's first operand, so a lane's four results are
 // consecutive columns of out.
+#include <atomic>
 #include <type_traits>
 #include <utility>
 
@@ -88,10 +89,10 @@ struct Item {
   const MxProduct* p;
   int m0, n0, k0, k1, split;
 };
-template <int TM, int TN>
-__device__ __forceinline__ Item item_of(const MxGemmArgs& args, uint32_t b) {
-  const int g = find_in_list(args.base, args.n, b);
-  const MxProduct& p = args.p[g];
+template <int TM, int TN, class Args>
+__device__ __forceinline__ Item item_of(const Args& args, uint32_t b) {
+  const int g = find_in_list(args, b);
+  const MxProduct& p = args.m[g];
   const int in_product = static_cast<int>(b - args.base[g]);
   Item it;
   it.p = &p;
@@ -126,48 +127,6 @@ struct Frags {
   int dm[FM / 4];
 };
 
-__device__ __forceinline__ float load_out(const uint16_t* p) {
-  return __uint_as_float(static_cast<uint32_t>(*p) << 16);
-}
-__device__ __forceinline__ float load_out(const float* p) { return *p; }
-__device__ __forceinline__ void store_out(uint16_t* p, float v) { *p = f2bf(v); }
-__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
-__device__ __forceinline__ void load8(const uint16_t* p, float* v) {
-  const u32x4_t q = *reinterpret_cast<const u32x4_t*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(q[i] << 16);
-    v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = a[i];
-    v[4 + i] = b[i];
-  }
-}
-__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-  *reinterpret_cast<u32x4_t*>(p) = u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                           pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
-}
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  *reinterpret_cast<f32x4_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
-  *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
-}
-
-// Output written past the caches' keeping: the operand panels stay in L2.
-__device__ __forceinline__ void store8nt(uint16_t* p, const float* v) {
-  const u32x4_t q = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                     pack_bf16(v[6], v[7])};
-  __builtin_nontemporal_store(q, reinterpret_cast<u32x4_t*>(p));
-}
-__device__ __forceinline__ void store8nt(float* p, const float* v) {
-  __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_t*>(p));
-  __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4_t*>(p) + 1);
-}
-
 // Wait until a stage has landed when `ahead` (at most MAXA) later stages of PER
 // loads each, and EXTRA stores if `extra`, were issued after it.
 template <int MAXA, int PER, int EXTRA>
@@ -199,8 +158,8 @@ __device__ __forceinline__ void wait_stage(int ahead, bool extra) {
 // LDS loads of a stage need as long as its products (skipping parts at 16384 x
 // 4096 x 10240: all 312 us, without loads 228, without LDS reads 280, without
 // products 215, loads alone 215).
-template <int ODT, int TM, int TN, int WM, int WN, int NST, int PER_CU, bool DROP>
-__global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(MxGemmArgs args) {
+template <class Args, int ODT, int TM, int TN, int WM, int WN, int NST, int PER_CU, bool DROP>
+__global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(Args args) {
   using T = typename std::conditional<ODT == kBF16, uint16_t, float>::type;
   constexpr int NW = WM * WN;
   using OpN = Operand<TN, NW, 0>;
@@ -215,7 +174,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(
   const uint32_t lds = lds_addr(smem);
 
   // items of this block: XCD x (blocks b = x mod 8) owns a contiguous range
-  const uint32_t total = args.items, grid = gridDim.x, x = blockIdx.x & 7, loc = blockIdx.x >> 3;
+  const uint32_t total = args.c.items, grid = gridDim.x, x = blockIdx.x & 7, loc = blockIdx.x >> 3;
   const uint32_t q = total >> 3, rem = total & 7;
   const uint32_t first = x * q + (x < rem ? x : rem), last = first + q + (x < rem ? 1 : 0);
   const uint32_t step = (grid + 7 - x) >> 3;
@@ -336,9 +295,9 @@ __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(
       __builtin_amdgcn_s_setprio(0);
     }
 
-    const uint64_t seed = DROP ? seed_of(args.drop_seed) : 0;
+    const uint64_t seed = DROP ? seed_of(args.c.drop.seed) : 0;
     T* out = static_cast<T*>(p.out) + it.split * p.stride;
-    const bool whole = args.vec && !args.accumulate && it.m0 + TM <= p.M && it.n0 + TN <= p.N;
+    const bool whole = !args.c.accumulate && it.m0 + TM <= p.M && it.n0 + TN <= p.N;
     covered = whole ? issued : 0;
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
@@ -355,17 +314,12 @@ __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(
           v[e] = swap ? acc[i + 1][j][e] : acc[i][j][e];
           v[4 + e] = swap ? acc[i][j][e] : acc[i + 1][j][e];
         }
-        if constexpr (DROP) {
-          const Words w = philox(c / 8, row, kTagDropout, p.index, seed);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            v[e] = ((w.w[e / 2] >> (16 * (e & 1))) & 0xffffu) >= args.drop ? v[e] * args.drop_scale : 0.f;
-        }
+        if constexpr (DROP) drop8(v, c / 8, row, p.index, seed, args.c.drop);
         T* o = out + row * p.ld + c;
         if (whole) {
-          store8nt(o, v);
-        } else if (args.vec && c + 8 <= p.N) {
-          if (args.accumulate) {
+          stream8(o, v);
+        } else if (c + 8 <= p.N) {
+          if (args.c.accumulate) {
             float w[8];
             load8(o, w);
 #pragma unroll
@@ -375,7 +329,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (c + e < p.N) store_out(o + e, args.accumulate ? load_out(o + e) + v[e] : v[e]);
+            if (c + e < p.N) store1(o + e, args.c.accumulate ? load1(o + e) + v[e] : v[e]);
         }
       }
     }
@@ -384,38 +338,54 @@ __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(
 
 constexpr int kCUs = 256;
 
-template <int ODT, int TM, int TN, int NST, int PER_CU, bool DROP>
-hipError_t launch_tile(const MxGemmArgs& a, hipStream_t s) {
+template <class Args, int ODT, int TM, int TN, int NST, int PER_CU, bool DROP>
+hipError_t launch_tile(const Args& a, hipStream_t s) {
   constexpr int WM = 2, WN = 2, NW = WM * WN;
   using OpN = Operand<TN, NW, 0>;
   using OpM = Operand<TM, NW, 1>;
   constexpr int lds = NST * (OpN::kBytes + OpM::kBytes + OpN::kScales + OpM::kScales);
   static_assert(lds * PER_CU <= 160 * 1024, "LDS");
-  auto* k = &k_mx_gemm<ODT, TM, TN, WM, WN, NST, PER_CU, DROP>;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  auto* k = &k_mx_gemm<Args, ODT, TM, TN, WM, WN, NST, PER_CU, DROP>;
+  // the LDS limit is raised once per device
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
-  const int blocks = a.items < kCUs * PER_CU ? a.items : kCUs * PER_CU;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(raised.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int blocks = a.c.items < kCUs * PER_CU ? a.c.items : kCUs * PER_CU;
   hipLaunchKernelGGL(k, dim3(blocks), dim3(64 * NW), lds, s, a);
   return hipGetLastError();
 }
 
-template <int ODT, bool DROP>
-hipError_t launch_drop(const MxGemmArgs& a, int tile_m, hipStream_t s) {
-  return tile_m == 256 ? launch_tile<ODT, 256, 128, 3, 2, DROP>(a, s)
-                       : launch_tile<ODT, 128, 128, 3, 3, DROP>(a, s);
+template <class Args, int ODT, bool DROP>
+hipError_t launch_drop(const Args& a, int tile_m, hipStream_t s) {
+  return tile_m == 256 ? launch_tile<Args, ODT, 256, 128, 3, 2, DROP>(a, s)
+                       : launch_tile<Args, ODT, 128, 128, 3, 3, DROP>(a, s);
+}
+
+template <class Args>
+hipError_t launch_gemm_of(const Args& a, int odt, int tile_m, hipStream_t s) {
+  const bool drop = a.c.drop.threshold != 0;
+  if (odt == kBF16)
+    return drop ? launch_drop<Args, kBF16, true>(a, tile_m, s) : launch_drop<Args, kBF16, false>(a, tile_m, s);
+  return drop ? launch_drop<Args, kF32, true>(a, tile_m, s) : launch_drop<Args, kF32, false>(a, tile_m, s);
 }
 
 // Sum of the partial products of a split contraction, in the order of the
 // splits; eight columns a thread.
-template <int ODT>
-__global__ __launch_bounds__(256) void k_mx_reduce(MxReduceArgs args) {
+template <class Args, int ODT>
+__global__ __launch_bounds__(256) void k_mx_reduce(Args args) {
   using T = typename std::conditional<ODT == kBF16, uint16_t, float>::type;
-  const int g = find_in_list(args.base, args.n, blockIdx.x);
-  const MxReduce& p = args.p[g];
+  const int g = find_in_list(args, blockIdx.x);
+  const MxReduce& p = args.m[g];
   const uint32_t t = (blockIdx.x - args.base[g]) * 256 + threadIdx.x;
   const uint32_t per_row = p.ldp / 8;
-  const uint32_t row = t / per_row, c = (t % per_row) * 8;
+  const uint32_t row = t / per_row, c = (t % per_row) * 8, N = p.N;
   if (row >= static_cast<uint32_t>(p.M)) return;
   const float* in = p.in + static_cast<int64_t>(row) * p.ldp + c;
   float v[8];
@@ -426,15 +396,10 @@ __global__ __launch_bounds__(256) void k_mx_reduce(MxReduceArgs args) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += w[e];
   }
-  if (args.drop) {
-    const Words w = philox(c / 8, row, kTagDropout, p.index, seed_of(args.drop_seed));
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = ((w.w[e / 2] >> (16 * (e & 1))) & 0xffffu) >= args.drop ? v[e] * args.drop_scale : 0.f;
-  }
+  if (args.c.drop.threshold) drop8(v, c / 8, row, p.index, seed_of(args.c.drop.seed), args.c.drop);
   T* o = static_cast<T*>(p.out) + row * p.ld + c;
-  if (p.vec && c + 8 <= static_cast<uint32_t>(p.N)) {
-    if (args.accumulate) {
+  if (c + 8 <= N) {
+    if (args.c.accumulate) {
       float w[8];
       load8(o, w);
 #pragma unroll
@@ -444,7 +409,7 @@ __global__ __launch_bounds__(256) void k_mx_reduce(MxReduceArgs args) {
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (c + e < static_cast<uint32_t>(p.N)) store_out(o + e, args.accumulate ? load_out(o + e) + v[e] : v[e]);
+      if (c + e < N) store1(o + e, args.c.accumulate ? load1(o + e) + v[e] : v[e]);
   }
 }
 
@@ -489,9 +454,9 @@ __global__ __launch_bounds__(64 * NW) void k_mx_rows(MxRowsArgs a) {
       const int r = 4 * h + row;
       if (4 * h >= a.M || r >= a.M) continue;
       const X* p = static_cast<const X*>(a.x) + static_cast<int64_t>(r) * a.ldx + c;
-      if (a.vec && c + 8 <= a.K) {
+      if (c + 8 <= a.K) {
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) s.x[h][q] = *glb(reinterpret_cast<const u32x4_t*>(p) + q);
+        for (int q = 0; q < NQ; ++q) s.x[h][q] = load16b(p + q * (8 / NQ));
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -546,7 +511,7 @@ __global__ __launch_bounds__(64 * NW) void k_mx_rows(MxRowsArgs a) {
 #pragma unroll
     for (int w = 0; w < NW; ++w) s += part[w][i][(col >> 2) * 16 + m][col & 3];
     const int n = (rt0 + i) * 16 + col;
-    if (m < a.M && n < a.N) store_out(static_cast<T*>(a.out) + m * a.ldo + n, s);
+    if (m < a.M && n < a.N) store1(static_cast<T*>(a.out) + m * a.ldo + n, s);
   }
 }
 
@@ -574,8 +539,7 @@ hipError_t launch_rows(const MxRowsArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_mx_gemm(const MxGemmArgs& a, int odt, int tile_m, hipStream_t s) {
-  if (odt == kBF16) return a.drop ? launch_drop<kBF16, true>(a, tile_m, s) : launch_drop<kBF16, false>(a, tile_m, s);
-  return a.drop ? launch_drop<kF32, true>(a, tile_m, s) : launch_drop<kF32, false>(a, tile_m, s);
+  return a.n == 1 ? launch_gemm_of(list_of_one(a), odt, tile_m, s) : launch_gemm_of(a, odt, tile_m, s);
 }
 
 hipError_t launch_mx_rows(const MxRowsArgs& a, int xdt, int odt, hipStream_t s) {
@@ -585,8 +549,8 @@ hipError_t launch_mx_rows(const MxRowsArgs& a, int xdt, int odt, hipStream_t s) 
 
 hipError_t launch_mx_reduce(const MxReduceArgs& a, int odt, int64_t blocks, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(blocks));
-  if (odt == kBF16) hipLaunchKernelGGL((k_mx_reduce<kBF16>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_mx_reduce<kF32>), grid, dim3(256), 0, s, a);
+  if (odt == kBF16) hipLaunchKernelGGL((k_mx_reduce<MxReduceArgs, kBF16>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_mx_reduce<MxReduceArgs, kF32>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

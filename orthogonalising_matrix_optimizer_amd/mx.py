@@ -34,10 +34,9 @@ class MX4:
 
     __slots__ = ("buffer", "offset", "rows", "cols", "desc")
 
-    def __init__(self, buffer: torch.Tensor, offset: int, rows: int, cols: int):
-        self.buffer, self.offset, self.rows, self.cols = buffer, offset, rows, cols
-        p = buffer.data_ptr() + offset
-        self.desc = (p, p + _codes_bytes(rows, cols), rows, cols) if rows and cols else (0, 0, rows, cols)
+    def __init__(self, buffer: torch.Tensor, offset: int, desc: Tuple[int, int, int, int]):
+        self.buffer, self.offset, self.desc = buffer, offset, desc   # desc: a muon_mx
+        self.rows, self.cols = desc[2], desc[3]
 
     @property
     def shape(self) -> Tuple[int, int]:
@@ -78,35 +77,40 @@ class MXSaved(NamedTuple):
 
 # Storage sizes (muon_mx_codes_bytes, muon_mx_scales_bytes): tiles of 16 x 128
 # codes in 1024 bytes, of 64 x 128 elements' scales in 256.
-def _codes_bytes(rows: int, cols: int) -> int:
-    return -(-rows // 16) * -(-cols // 128) * 1024
-
-
 def _mx_bytes(rows: int, cols: int) -> int:
     return (-(-rows // 16) * 1024 + -(-rows // 64) * 256) * -(-cols // 128)
 
 
-def _new_mx(shapes, device):
-    """MX4 matrices of the shapes, in one allocation."""
-    if len(shapes) == 1:
-        r, c = shapes[0]
-        return [MX4(torch.empty(_mx_bytes(r, c), dtype=torch.uint8, device=device), 0, r, c)]
-    at = [0]
-    for r, c in shapes:
-        at.append(at[-1] + _mx_bytes(r, c))
-    buf = torch.empty(at[-1], dtype=torch.uint8, device=device)
-    return [MX4(buf, o, r, c) for o, (r, c) in zip(at, shapes)]
+def _new_mx(rows, cols, device):
+    """MX4 matrices of rows[i] x cols[i], in one allocation."""
+    sizes = [(-(-r // 16) * 1024 + -(-r // 64) * 256) * -(-c // 128) for r, c in zip(rows, cols)]
+    buf = torch.empty(sum(sizes), dtype=torch.uint8, device=device)
+    p, at, out = buf.data_ptr(), 0, []
+    for r, c, n in zip(rows, cols, sizes):
+        out.append(MX4(buf, at, (p + at, p + at + -(-r // 16) * -(-c // 128) * 1024, r, c) if n else (0, 0, r, c)))
+        at += n
+    return out
 
 
-def _new_dense(shapes, dtype, device):
-    """Dense tensors of the shapes; equally wide ones share an allocation."""
-    if dtype not in _DT:
+def _new_dense(rows, cols, dtype, device):
+    """Dense rows[i] x cols[i] tensors and their packed muon_mat array; equally
+    wide ones share an allocation."""
+    d = _DT.get(dtype)
+    if d is None:
         raise ValueError(f"unsupported dtype {dtype}")
-    width = shapes[0][1]
-    if len(shapes) > 1 and all(c == width for _, c in shapes):
-        rows = [r for r, _ in shapes]
-        return list(torch.empty((sum(rows), width), dtype=dtype, device=device).split(rows))
-    return [torch.empty(s, dtype=dtype, device=device) for s in shapes]
+    n, width = len(rows), cols[0]
+    if n == 1:
+        t = torch.empty((rows[0], width), dtype=dtype, device=device)
+        return [t], _MAT1.pack(t.data_ptr(), rows[0], width, width, d, 0)
+    if cols.count(width) == n:
+        buf = torch.empty((sum(rows), width), dtype=dtype, device=device)
+        p, step, flat = buf.data_ptr(), width * dtype.itemsize, []
+        for r in rows:
+            flat += (p, r, width, width, d, 0)
+            p += r * step
+        return list(buf.split(rows)), Struct(_MAT * n).pack(*flat)
+    ts = [torch.empty(s, dtype=dtype, device=device) for s in zip(rows, cols)]
+    return ts, _mats(ts, device)
 
 
 def _rows_of(t: torch.Tensor) -> torch.Tensor:
@@ -142,15 +146,28 @@ def _mat(t: torch.Tensor, dev: torch.device):
     return t.data_ptr(), r, c, s, d, 0
 
 
+def _flat(ts, dev):
+    """The fields of the muon_mats of 2-D tensors, one after the other."""
+    flat = []
+    for t in ts:
+        r, c = t.shape
+        s, one = t.stride()
+        if t.dtype in _DT and t.device == dev and one == 1 and s >= c:
+            flat += (t.data_ptr(), r, c, s, _DT[t.dtype], 0)
+        else:
+            flat += _mat(t, dev)
+    return flat
+
+
 def _mats(ts, dev) -> bytes:
     if len(ts) == 1:
         return _MAT1.pack(*_mat(ts[0], dev))
-    return Struct(_MAT * len(ts)).pack(*[v for t in ts for v in _mat(t, dev)])
+    return Struct(_MAT * len(ts)).pack(*_flat(ts, dev))
 
 
 def _mxs(ms, dev) -> bytes:
     for m in ms:
-        if not isinstance(m, MX4):
+        if type(m) is not MX4:
             raise ValueError(f"expected an MX4, got {type(m).__name__}")
         if m.buffer.device != dev:
             raise ValueError("operands must be on one device")
@@ -218,14 +235,16 @@ def mx_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], transpose: Union
     if not xs:
         return []
     dev = _gpu(xs[0].device)
-    mats = _mats(xs, dev)
+    flat = _flat(xs, dev)
+    mats = _MAT1.pack(*flat) if len(xs) == 1 else Struct(_MAT * len(xs)).pack(*flat)
     both = transpose == "both"
     rows = cols = None
     if out is None:
+        r, c = flat[1::6], flat[2::6]
         if transpose is not True:
-            rows = _new_mx([tuple(t.shape) for t in xs], dev)
+            rows = _new_mx(r, c, dev)
         if transpose is not False:
-            cols = _new_mx([tuple(t.shape)[::-1] for t in xs], dev)
+            cols = _new_mx(c, r, dev)
     else:
         outs = [out] if single else list(out)
         if len(outs) != len(xs):
@@ -246,6 +265,20 @@ def mx_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], transpose: Union
     return res[0] if single else res
 
 
+def quantize_again(xs: Sequence[torch.Tensor], pairs: Sequence[MXPair]):
+    """The call mx_quantize(xs, "both", out=pairs) with its descriptors packed
+    once, for a list that is quantised again and again in the same memory."""
+    dev = xs[0].device
+    mats = _mats(xs, dev)
+    rows, cols = _mxs([p.w for p in pairs], dev), _mxs([p.w_t for p in pairs], dev)
+
+    def again() -> None:
+        code = _call("muon_mx_quantize", dev, mats, rows, cols, len(xs), None)
+        if code:
+            _lib.check(code, "muon_mx_quantize")
+    return again
+
+
 def mx_dequantize(m: Union[MX4, Sequence[MX4]], dtype: torch.dtype = torch.bfloat16,
                   out: Union[None, torch.Tensor, Sequence[torch.Tensor]] = None):
     """The values that 4-bit matrices stand for, as rows x cols tensors."""
@@ -256,12 +289,13 @@ def mx_dequantize(m: Union[MX4, Sequence[MX4]], dtype: torch.dtype = torch.bfloa
     dev = ms[0].device
     mxs = _mxs(ms, dev)
     if out is None:
-        outs = _new_dense([q.shape for q in ms], dtype, dev)
+        outs, mats = _new_dense([q.rows for q in ms], [q.cols for q in ms], dtype, dev)
     else:
         outs = [_rows_of(t) for t in ([out] if single else out)]
         if len(outs) != len(ms):
             raise ValueError(f"{len(ms)} matrices, {len(outs)} outputs")
-    code = _call("muon_mx_dequantize", dev, mxs, _mats(outs, dev), len(ms))
+        mats = _mats(outs, dev)
+    code = _call("muon_mx_dequantize", dev, mxs, mats, len(ms))
     if code:
         _lib.check(code, "muon_mx_dequantize")
     if out is not None:
@@ -289,12 +323,12 @@ def mx_matmul(a: Union[MX4, Sequence[MX4]], b: Union[MX4, Sequence[MX4]],
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        outs = _new_dense([(p.rows, q.rows) for p, q in zip(la, lb)], dtype, dev)
+        outs, co = _new_dense([p.rows for p in la], [q.rows for q in lb], dtype, dev)
     else:
         outs = [_rows_of(t) for t in ([out] if single else out)]
         if len(outs) != n:
             raise ValueError(f"{n} products, {len(outs)} outputs")
-    co = _mats(outs, dev)
+        co = _mats(outs, dev)
     opt = _options(dev, None, dropout, dropout_seed, accumulate)
     code = _call("muon_mx_matmul", dev, ca, cb, co, n, opt, None, 0)
     if code == _SPLIT:   # the list's contraction is split: give it room for the partial products
@@ -320,9 +354,9 @@ def mx_linear(x: torch.Tensor, w: MX4, save: bool = False, dropout: float = 0.0,
         raise ValueError(f"x has {cols} features, the layer takes {w.cols}")
     if not save and not dropout and rows <= _lib.MX_FEW_ROWS:
         dev = _gpu(x.device)
-        y = torch.empty((rows, w.rows), dtype=x.dtype, device=dev)
-        code = _call("muon_mx_matmul_rows", dev, _MAT1.pack(*_mat(x2, dev)), _mxs([w], dev),
-                     _MAT1.pack(*_mat(y, dev)))
+        xm = _mats([x2], dev)
+        (y,), ym = _new_dense([rows], [w.rows], x.dtype, dev)
+        code = _call("muon_mx_matmul_rows", dev, xm, _mxs([w], dev), ym)
         if code:
             _lib.check(code, "muon_mx_matmul_rows")
         saved = None

@@ -13,6 +13,7 @@ import numpy as np
 import torch
 
 from . import _lib
+from . import mx as _mx
 
 # Coefficient rows (a, b, c) of the map x -> a x + b x^3 + c x^5.
 CUBIC = (1.5, -0.5, 0.0)                       # Newton-Schulz for the polar factor
@@ -87,6 +88,14 @@ class Muon:
     `beta_ema` from step `ema_start`, Nesterov look-ahead, bf16 or fp32
     Newton-Schulz operands.  `diagnostics` allocates per-matrix buffers that
     receive the applied mask and update O on every step.
+
+    With `mx` the optimizer keeps each weight and its transpose in 4 bits for
+    mx_linear and mx_linear_grad: `mx` is a list of MXPair, written again in
+    the same buffers by every step (and by mx_refresh after the weights were
+    changed otherwise).  A gradient may be given as the pair of its 4-bit
+    factors (dy_t, x_t) that mx_linear_grad returns with pair=True: the step
+    then forms the products of all such gradients in one call, in fp32 buffers
+    that it keeps.
     """
 
     def __init__(self, params: List[torch.Tensor], lr: float = 0.02, wd: float = 0.0,
@@ -95,7 +104,7 @@ class Muon:
                  beta_slow: Optional[float] = None, beta_ema: Optional[float] = None,
                  ema_start: int = 1, cautious: bool = False, nesterov: bool = False,
                  ns_dtype: str = "bf16", eps: float = 1e-7, diagnostics: bool = False,
-                 avg: str = "ema"):
+                 avg: str = "ema", mx: bool = False):
         self.lib = _lib.load()
         self.params = list(params)
         self.lr, self.wd, self.beta, self.steps = float(lr), float(wd), float(beta), int(steps)
@@ -129,6 +138,18 @@ class Muon:
         self._bind_state()
         self._gkey = None
         self._gmats = None
+        self._pgrads = {}
+        self.mx, self._mx_calls = None, []
+        if mx:
+            self.mx = [None] * len(self.params)
+            for dt in (torch.bfloat16, torch.float32):   # a call takes one element type
+                at = [i for i, p in enumerate(self.params) if p.dtype == dt]
+                if at:
+                    ps = [self.params[i] for i in at]
+                    pairs = _mx.mx_quantize(ps, "both")
+                    for i, q in zip(at, pairs):
+                        self.mx[i] = q
+                    self._mx_calls.append(_mx.quantize_again(ps, pairs))
 
     def _bind_state(self):
         st = self.state
@@ -168,6 +189,31 @@ class Muon:
     def avg_weight(self, w: float) -> None:
         self.state.avg_weight = float(w)
 
+    def mx_refresh(self) -> None:
+        """Write the 4-bit copies again from the weights (every step does)."""
+        for again in self._mx_calls:
+            again()
+
+    def _products(self, grads):
+        """`grads` with the gradients given as 4-bit factors multiplied out."""
+        at = [i for i, g in enumerate(grads) if not isinstance(g, torch.Tensor)]
+        if not at:
+            return grads
+        grads = list(grads)
+        for i in at:
+            a, b = grads[i]
+            if (a.rows, b.rows) != tuple(self.params[i].shape):
+                raise ValueError(f"factors of a {a.rows} x {b.rows} gradient for a parameter of shape "
+                                 f"{tuple(self.params[i].shape)}")
+            if i not in self._pgrads:
+                self._pgrads[i] = torch.empty(self.params[i].shape, dtype=torch.float32,
+                                              device=self.params[i].device)
+        _mx.mx_matmul([grads[i][0] for i in at], [grads[i][1] for i in at],
+                      out=[self._pgrads[i] for i in at])
+        for i in at:
+            grads[i] = self._pgrads[i]
+        return grads
+
     def _grad_mats(self, grads: List[torch.Tensor]):
         key = tuple((g.data_ptr(), g.stride(0), g.dtype) for g in grads)
         if key != self._gkey:
@@ -178,8 +224,8 @@ class Muon:
     def step_prepare(self, grads: List[torch.Tensor]) -> None:
         """Make the device descriptor table for these gradient buffers resident
         (no launch, counters unchanged), so a step with them can be captured."""
-        code = self.lib.muon_step_prepare(self._pmats, self._grad_mats(grads), self.state,
-                                          _stream())
+        code = self.lib.muon_step_prepare(self._pmats, self._grad_mats(self._products(grads)),
+                                          self.state, _stream())
         _lib.check(code, "muon_step_prepare")
 
     def graph(self, grads: List[torch.Tensor], lr: Optional[float] = None,
@@ -189,11 +235,12 @@ class Muon:
 
     def step(self, grads: List[torch.Tensor], lr: Optional[float] = None,
              wd: Optional[float] = None) -> None:
-        self._grad_mats(grads)
+        self._grad_mats(self._products(grads))
         code = self.lib.muon_step(self._pmats, self._gmats, self.state, self._coeffs_c,
                                   self.steps, self.lr if lr is None else lr,
                                   self.wd if wd is None else wd, self.beta, _stream())
         _lib.check(code, "muon_step")
+        self.mx_refresh()
 
     def blend(self, outputs: List[torch.Tensor], w_final: float = 0.35) -> None:
         outs = _lib.mat_array(_mat(t) for t in outputs)
