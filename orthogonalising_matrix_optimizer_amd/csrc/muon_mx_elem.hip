@@ -165,10 +165,13 @@ __global__ __launch_bounds__(kQuantThreads) void k_mx_quantize(Args args) {
 #pragma unroll
     for (int j = 0; j < ND; ++j) q[j] = 0;
   if (args.c.drop.threshold) drop16<DT>(q, r, c0, m.index, seed_of(args.c.drop.seed), args.c.drop);
+  // a tile row's quarters swap in pairs every sixteen rows, so that lanes that
+  // read rows sixteen apart find them in different banks
+  constexpr int kSwap = T / PD / 4;
   if constexpr (COLS) {
 #pragma unroll
     for (int j = 0; j < ND; j += 4)
-      *reinterpret_cast<u32x4_t*>(tile + (lr * T + ch * 16) / PD + j) =
+      *reinterpret_cast<u32x4_t*>(tile + lr * (T / PD) + ((ch * ND + j) ^ ((lr >> 4 & 1) * kSwap))) =
           u32x4_t{q[j], q[j + 1], q[j + 2], q[j + 3]};
   }
   if constexpr (ROWS) {
@@ -189,33 +192,32 @@ __global__ __launch_bounds__(kQuantThreads) void k_mx_quantize(Args args) {
   }
   if constexpr (COLS) {
     __syncthreads();
-    if (t >= 4 * T) return;
-    const int rb = t >> 7, lc = t & 127;                 // block of 32 rows, column
-    uint32_t v[32 / PD];
+    const int half = t & 1, lc = (t >> 1) & 127, rb = t >> 8;   // half of a block of 32 rows, column
+    const int row0 = rb * 32 + half * 16;
+    uint32_t v[ND];                                      // 16 rows of the column
     if constexpr (DT == kBF16) {
-      const uint16_t* h = reinterpret_cast<const uint16_t*>(tile) + rb * 32 * T + lc;
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(tile) + row0 * T + (lc ^ (half * 2 * kSwap));
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) v[j / 2] = h[j * T] | static_cast<uint32_t>(h[(j + 1) * T]) << 16;
+      for (int j = 0; j < 16; j += 2) v[j / 2] = h[j * T] | static_cast<uint32_t>(h[(j + 1) * T]) << 16;
     } else {
+      const uint32_t* h = tile + row0 * T + (lc ^ (half * kSwap));
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = tile[(rb * 32 + j) * T + lc];
+      for (int j = 0; j < 16; ++j) v[j] = h[j * T];
     }
     const int c = tc * T + lc;                           // row of the transpose
-    const uint32_t byte = scale_byte(top_of<DT, 32 / PD>(v));
-    u32x4_t code;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      Words w = {{0, 0, 0, 0}};
-      if constexpr (SR) w = philox((tr * T + rb * 32) / 16 + h, c, kTagRoundT, m.index, seed);
-      code[2 * h] = encode8<DT, SR>(v + 16 / PD * h, byte, w.w);
-      code[2 * h + 1] = encode8<DT, SR>(v + 16 / PD * h + 8 / PD, byte, w.w + 2);
-    }
+    const uint32_t byte = scale_byte(max_pair(top_of<DT, ND>(v)));
+    Words w = {{0, 0, 0, 0}};
+    if constexpr (SR) w = philox((tr * T + row0) / 16, c, kTagRoundT, m.index, seed);
+    uint2 code;
+    code.x = encode8<DT, SR>(v, byte, w.w);
+    code.y = encode8<DT, SR>(v + ND / 2, byte, w.w + 2);
     const int rt = c >> 4, slot = rb * 16 + (c & 15);
     if (rt * 16 < m.cols) {
-      *glb(reinterpret_cast<u32x4_t*>(m.codes_t + (static_cast<int64_t>(tr) * ((m.cols + 15) / 16) + rt) * kMxTileBytes +
-                                      slot * 16)) = code;
-      *glb(m.scales_t + (static_cast<int64_t>(tr) * ((m.cols + 63) / 64) + (c >> 6)) * kMxScaleBytes +
-           slot * 4 + (rt & 3)) = static_cast<uint8_t>(byte);
+      *glb(reinterpret_cast<uint2*>(m.codes_t + (static_cast<int64_t>(tr) * ((m.cols + 15) / 16) + rt) * kMxTileBytes +
+                                    slot * 16 + half * 8)) = code;
+      if (half == 0)
+        *glb(m.scales_t + (static_cast<int64_t>(tr) * ((m.cols + 63) / 64) + (c >> 6)) * kMxScaleBytes +
+             slot * 4 + (rt & 3)) = static_cast<uint8_t>(byte);
     }
   }
 }
