@@ -32,19 +32,24 @@ class MX4:
     instructions read them; use dequantize() for values.  The matrices that
     one call returns for a list share an allocation."""
 
-    __slots__ = ("buffer", "offset", "rows", "cols", "desc")
+    __slots__ = ("buffer", "offset", "device", "desc")
 
-    def __init__(self, buffer: torch.Tensor, offset: int, desc: Tuple[int, int, int, int]):
-        self.buffer, self.offset, self.desc = buffer, offset, desc   # desc: a muon_mx
-        self.rows, self.cols = desc[2], desc[3]
+    def __init__(self, buffer: torch.Tensor, offset: int, device: torch.device,
+                 desc: Tuple[int, int, int, int]):
+        # desc: a muon_mx (codes, scales, rows, columns)
+        self.buffer, self.offset, self.device, self.desc = buffer, offset, device, desc
+
+    @property
+    def rows(self) -> int:
+        return self.desc[2]
+
+    @property
+    def cols(self) -> int:
+        return self.desc[3]
 
     @property
     def shape(self) -> Tuple[int, int]:
-        return (self.rows, self.cols)
-
-    @property
-    def device(self) -> torch.device:
-        return self.buffer.device
+        return self.desc[2:]
 
     @property
     def nbytes(self) -> int:
@@ -83,11 +88,18 @@ def _mx_bytes(rows: int, cols: int) -> int:
 
 def _new_mx(rows, cols, device):
     """MX4 matrices of rows[i] x cols[i], in one allocation."""
+    if len(rows) == 1:
+        r, c = rows[0], cols[0]
+        k, t = -(-c // 128), -(-r // 16) * 1024
+        buf = torch.empty(k * (t + -(-r // 64) * 256), dtype=torch.uint8, device=device)
+        p = buf.data_ptr()
+        return [MX4(buf, 0, device, (p, p + k * t, r, c) if p else (0, 0, r, c))]
     sizes = [(-(-r // 16) * 1024 + -(-r // 64) * 256) * -(-c // 128) for r, c in zip(rows, cols)]
     buf = torch.empty(sum(sizes), dtype=torch.uint8, device=device)
     p, at, out = buf.data_ptr(), 0, []
     for r, c, n in zip(rows, cols, sizes):
-        out.append(MX4(buf, at, (p + at, p + at + -(-r // 16) * -(-c // 128) * 1024, r, c) if n else (0, 0, r, c)))
+        q = p + at
+        out.append(MX4(buf, at, device, (q, q + -(-r // 16) * -(-c // 128) * 1024, r, c) if n else (0, 0, r, c)))
         at += n
     return out
 
@@ -117,9 +129,10 @@ def _rows_of(t: torch.Tensor) -> torch.Tensor:
     """`t` as a 2-D view of its rows (last dimension)."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"expected a tensor, got {type(t).__name__}")
-    if t.dim() == 2:
+    n = t.dim()
+    if n == 2:
         return t
-    if t.dim() == 0:
+    if n == 0:
         raise ValueError("tensors must have at least one dimension")
     c = t.shape[-1]
     try:
@@ -148,12 +161,13 @@ def _mat(t: torch.Tensor, dev: torch.device):
 
 def _flat(ts, dev):
     """The fields of the muon_mats of 2-D tensors, one after the other."""
-    flat = []
+    flat, at = [], dev.index
     for t in ts:
         r, c = t.shape
         s, one = t.stride()
-        if t.dtype in _DT and t.device == dev and one == 1 and s >= c:
-            flat += (t.data_ptr(), r, c, s, _DT[t.dtype], 0)
+        d = _DT.get(t.dtype)
+        if d is not None and one == 1 and s >= c and t.get_device() == at:
+            flat += (t.data_ptr(), r, c, s, d, 0)
         else:
             flat += _mat(t, dev)
     return flat
@@ -165,15 +179,25 @@ def _mats(ts, dev) -> bytes:
     return Struct(_MAT * len(ts)).pack(*_flat(ts, dev))
 
 
+def _pack_mx(ms) -> bytes:
+    if len(ms) == 1:
+        return _MX1.pack(*ms[0].desc)
+    return Struct(_MX * len(ms)).pack(*[v for m in ms for v in m.desc])
+
+
 def _mxs(ms, dev) -> bytes:
     for m in ms:
         if type(m) is not MX4:
             raise ValueError(f"expected an MX4, got {type(m).__name__}")
-        if m.buffer.device != dev:
+        if m.device is not dev and m.device != dev:
             raise ValueError("operands must be on one device")
-    if len(ms) == 1:
-        return _MX1.pack(*ms[0].desc)
-    return Struct(_MX * len(ms)).pack(*[v for m in ms for v in m.desc])
+    return _pack_mx(ms)
+
+
+def _device_of(m) -> torch.device:
+    if type(m) is not MX4:
+        raise ValueError(f"expected an MX4, got {type(m).__name__}")
+    return m.device
 
 
 def _gpu(dev: torch.device) -> torch.device:
@@ -182,13 +206,28 @@ def _gpu(dev: torch.device) -> torch.device:
     return dev
 
 
+_functions = {}
+
+
 def _call(name: str, dev: torch.device, *args) -> int:
-    """A library call on `dev` and its current stream; the status."""
+    """A library call on `dev` and its current stream; raises on an error, but
+    hands MUON_E_WORKSPACE back."""
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(_lib.load(), name)
     i = dev.index
-    if torch._C._cuda_getDevice() == i:
-        return getattr(_lib.load(), name)(*args, torch._C._cuda_getCurrentRawStream(i))
-    with torch.cuda.device(i):
-        return getattr(_lib.load(), name)(*args, torch._C._cuda_getCurrentRawStream(i))
+    if _current_device() == i:
+        code = f(*args, _current_stream(i))
+    else:
+        with torch.cuda.device(i):
+            code = f(*args, _current_stream(i))
+    if code and code != _SPLIT:
+        _lib.check(code, name)
+    return code
+
+
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _set_seed(opt: "_lib.MXOptions", field: str, seed: Seed, dev) -> None:
@@ -231,12 +270,13 @@ def mx_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], transpose: Union
     if transpose not in (False, True, "both"):
         raise ValueError(f"transpose is False, True or 'both', not {transpose!r}")
     single = isinstance(x, torch.Tensor)
-    xs = [_rows_of(t) for t in ([x] if single else x)]
+    xs = [_rows_of(x)] if single else [_rows_of(t) for t in x]
+    n = len(xs)
     if not xs:
         return []
     dev = _gpu(xs[0].device)
     flat = _flat(xs, dev)
-    mats = _MAT1.pack(*flat) if len(xs) == 1 else Struct(_MAT * len(xs)).pack(*flat)
+    mats = _MAT1.pack(*flat) if n == 1 else Struct(_MAT * n).pack(*flat)
     both = transpose == "both"
     rows = cols = None
     if out is None:
@@ -247,17 +287,18 @@ def mx_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], transpose: Union
             cols = _new_mx(c, r, dev)
     else:
         outs = [out] if single else list(out)
-        if len(outs) != len(xs):
-            raise ValueError(f"{len(xs)} matrices, {len(outs)} outputs")
+        if len(outs) != n:
+            raise ValueError(f"{n} matrices, {len(outs)} outputs")
         if transpose is not True:
             rows = [o[0] if both else o for o in outs]
         if transpose is not False:
             cols = [o[1] if both else o for o in outs]
-    code = _call("muon_mx_quantize", dev, mats, _mxs(rows, dev) if rows else None,
-                 _mxs(cols, dev) if cols else None, len(xs),
-                 _options(dev, seed, dropout, dropout_seed))
-    if code:
-        _lib.check(code, "muon_mx_quantize")
+    opt = None
+    if seed is not None or dropout:
+        opt = _options(dev, seed, dropout, dropout_seed)
+    pack = _pack_mx if out is None else lambda ms: _mxs(ms, dev)
+    _call("muon_mx_quantize", dev, mats, pack(rows) if rows else None, pack(cols) if cols else None,
+          n, opt)
     if both:
         res = [MXPair(a, b) for a, b in zip(rows, cols)]
     else:
@@ -273,9 +314,7 @@ def quantize_again(xs: Sequence[torch.Tensor], pairs: Sequence[MXPair]):
     rows, cols = _mxs([p.w for p in pairs], dev), _mxs([p.w_t for p in pairs], dev)
 
     def again() -> None:
-        code = _call("muon_mx_quantize", dev, mats, rows, cols, len(xs), None)
-        if code:
-            _lib.check(code, "muon_mx_quantize")
+        _call("muon_mx_quantize", dev, mats, rows, cols, len(xs), None)
     return again
 
 
@@ -286,18 +325,16 @@ def mx_dequantize(m: Union[MX4, Sequence[MX4]], dtype: torch.dtype = torch.bfloa
     ms = [m] if single else list(m)
     if not ms:
         return []
-    dev = ms[0].device
+    dev = _device_of(ms[0])
     mxs = _mxs(ms, dev)
     if out is None:
-        outs, mats = _new_dense([q.rows for q in ms], [q.cols for q in ms], dtype, dev)
+        outs, mats = _new_dense([q.desc[2] for q in ms], [q.desc[3] for q in ms], dtype, dev)
     else:
         outs = [_rows_of(t) for t in ([out] if single else out)]
         if len(outs) != len(ms):
             raise ValueError(f"{len(ms)} matrices, {len(outs)} outputs")
         mats = _mats(outs, dev)
-    code = _call("muon_mx_dequantize", dev, mxs, mats, len(ms))
-    if code:
-        _lib.check(code, "muon_mx_dequantize")
+    _call("muon_mx_dequantize", dev, mxs, mats, len(ms))
     if out is not None:
         return out
     return outs[0] if single else outs
@@ -318,12 +355,12 @@ def mx_matmul(a: Union[MX4, Sequence[MX4]], b: Union[MX4, Sequence[MX4]],
         raise ValueError(f"{n} left and {len(lb)} right operands")
     if not la:
         return []
-    dev = la[0].device
+    dev = _device_of(la[0])
     ca, cb = _mxs(la, dev), _mxs(lb, dev)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        outs, co = _new_dense([p.rows for p in la], [q.rows for q in lb], dtype, dev)
+        outs, co = _new_dense([p.desc[2] for p in la], [q.desc[2] for q in lb], dtype, dev)
     else:
         outs = [_rows_of(t) for t in ([out] if single else out)]
         if len(outs) != n:
@@ -334,9 +371,7 @@ def mx_matmul(a: Union[MX4, Sequence[MX4]], b: Union[MX4, Sequence[MX4]],
     if code == _SPLIT:   # the list's contraction is split: give it room for the partial products
         ws = torch.empty(int(_lib.load().muon_mx_matmul_workspace_bytes(ca, cb, n)), dtype=torch.uint8,
                          device=dev)
-        code = _call("muon_mx_matmul", dev, ca, cb, co, n, opt, ws.data_ptr(), ws.numel())
-    if code:
-        _lib.check(code, "muon_mx_matmul")
+        _call("muon_mx_matmul", dev, ca, cb, co, n, opt, ws.data_ptr(), ws.numel())
     if out is not None:
         return out
     return outs[0] if single else outs
@@ -356,9 +391,7 @@ def mx_linear(x: torch.Tensor, w: MX4, save: bool = False, dropout: float = 0.0,
         dev = _gpu(x.device)
         xm = _mats([x2], dev)
         (y,), ym = _new_dense([rows], [w.rows], x.dtype, dev)
-        code = _call("muon_mx_matmul_rows", dev, xm, _mxs([w], dev), ym)
-        if code:
-            _lib.check(code, "muon_mx_matmul_rows")
+        _call("muon_mx_matmul_rows", dev, xm, _mxs([w], dev), ym)
         saved = None
     else:
         q = mx_quantize(x2, "both" if save else False, dropout=dropout, dropout_seed=dropout_seed)
@@ -401,18 +434,19 @@ def dropout(x: torch.Tensor, p: float, seed: Seed, out: Optional[torch.Tensor] =
     `out` may be x itself."""
     x2 = _rows_of(x)
     dev = _gpu(x.device)
+    xm = _MAT1.pack(*_mat(x2, dev))
     if out is None:
-        res = o2 = torch.empty(x2.shape, dtype=x.dtype, device=dev)
+        (res,), om = _new_dense([x2.shape[0]], [x2.shape[1]], x.dtype, dev)
         if x.dim() != 2:
-            res = o2.view(x.shape)
+            res = res.view(x.shape)
     else:
         if out.shape != x.shape:
             raise ValueError(f"out is {tuple(out.shape)}, not {tuple(x.shape)}")
-        res, o2 = out, _rows_of(out)
-    opt = _lib.MXOptions()
-    _set_seed(opt, "seed", seed, dev)
-    code = _call("muon_dropout", dev, _MAT1.pack(*_mat(x2, dev)), _MAT1.pack(*_mat(o2, dev)), p,
-                 opt.seed, opt.seed_dev)
-    if code:
-        _lib.check(code, "muon_dropout")
+        res, om = out, _MAT1.pack(*_mat(_rows_of(out), dev))
+    if isinstance(seed, torch.Tensor):
+        opt = _lib.MXOptions()
+        _set_seed(opt, "seed", seed, dev)
+        _call("muon_dropout", dev, xm, om, p, 0, opt.seed_dev)
+    else:
+        _call("muon_dropout", dev, xm, om, p, seed & 0xFFFFFFFFFFFFFFFF, None)
     return res

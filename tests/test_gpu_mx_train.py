@@ -107,7 +107,7 @@ def test_captured_step_with_factors_and_4bit_weights():
     twin = [p.clone() for p in ps]
     opt, ref = mo.Muon(ps, mx=True), mo.Muon(twin, mx=True)
     pairs = _pairs(opt, _batch(9000, 0), 5)     # long enough for split products
-    mirror = [(mo.MX4(a.buffer, a.offset, a.desc), mo.MX4(b.buffer, b.offset, b.desc)) for a, b in pairs]
+    mirror = [tuple(mo.MX4(m.buffer, m.offset, m.device, m.desc) for m in p) for p in pairs]
     g = opt.graph(pairs)
     for t in range(4):
         new = _pairs(opt, _batch(9000, t + 1), 100 + t)
