@@ -123,7 +123,7 @@ struct MxProduct {
 };
 struct MxGemmCommon {
   MxDrop drop;
-  int32_t items;           // work items of the launch
+  int32_t xcd[9];          // items [xcd[x], xcd[x + 1]) are XCD x's: as many stages each
   int32_t accumulate;      // out += product
 };
 template <int CAP> using MxGemmList = MxList<MxGemmCommon, MxProduct, CAP>;

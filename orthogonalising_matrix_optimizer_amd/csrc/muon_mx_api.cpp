@@ -136,7 +136,9 @@ struct ProductPlan {
 };
 
 // The splits of a contraction of kt code tiles have the same length (but the last).
-int64_t even_chunk(int64_t kt, int64_t chunk) { return ceil_div(kt, ceil_div(kt, chunk)); }
+int64_t even_chunk(int64_t kt, int64_t chunk) {
+  return kt ? ceil_div(kt, ceil_div(kt, chunk)) : 1;
+}
 
 // Microseconds a stage (128 columns) of a work item takes with 1, 2, 3 blocks
 // on its CU, measured on MI355X: 256 x 128 tiles (two blocks a CU) and 128 x
@@ -170,19 +172,20 @@ ProductPlan plan_products(const muon_mx* a, const muon_mx* b, int n) {
   double best = list_us(kStage128, 3, i128, w128, longest);
   p.tile_m = t256 < best ? 256 : 128;
   best = std::min(best, t256);
-  // Splitting adds the partial products' way to memory and back (4 TB/s) and
-  // a launch (5 us); it pays for few tiles with a long contraction and for
-  // lists with one much longer than the rest: 768 x 768 x 8192 21 us against
-  // 32, 128 x 2560 x 10240 20 against 39, twelve 768 x 768 with K of 1630 to
-  // 23201 75 against 98, but 2560 x 2560 x 16384 98 against 86.
+  // Splitting adds the partial products' way through the caches and back (6
+  // TB/s) and a launch (5 us); it pays for few tiles with a long contraction and
+  // for lists with one much longer than the rest, us (whole | split): 768 x 768
+  // x 8192 33 | 20, 128 x 2560 x 10240 40 | 18, 1408 x 2048 x 16384 65 | 50,
+  // twelve 768 x 768 with K of 1630 to 23201 100 | 66; but 2560 x 2560 x 16384
+  // 81 | 88 and 512 x 2048 x 4096 19 | 20.
   for (int64_t c = kMinChunk; c < longest; c += c / 2) {
     double items = 0, bytes = 0;
     for (int i = 0; i < n; ++i) {
       const int64_t kt = ceil_div(a[i].cols, kMxTileK), splits = std::max<int64_t>(1, ceil_div(kt, c));
       items += double(splits) * ceil_div(a[i].rows, 128) * ceil_div(b[i].rows, kTileN);
-      if (splits > 1) bytes += 8.0 * splits * a[i].rows * b[i].rows;
+      bytes += 8.0 * splits * a[i].rows * b[i].rows;
     }
-    const double t = list_us(kStage128, 3, items, w128, double(c)) + bytes / 4e6 + 5;
+    const double t = list_us(kStage128, 3, items, w128, double(c)) + bytes / 6e6 + 5;
     if (t < 0.9 * best) {
       best = t / 0.9;
       p.chunk = c;
@@ -193,13 +196,35 @@ ProductPlan plan_products(const muon_mx* a, const muon_mx* b, int n) {
     p.offset.assign(n, 0);
     for (int i = 0; i < n; ++i) {
       const int64_t kt = ceil_div(a[i].cols, kMxTileK);
-      if (kt <= p.chunk || a[i].rows == 0 || b[i].rows == 0) continue;
+      const int64_t splits = std::max<int64_t>(1, ceil_div(kt, even_chunk(kt, p.chunk)));
       p.offset[i] = p.bytes;
-      p.bytes += size_t(ceil_div(kt, even_chunk(kt, p.chunk))) * a[i].rows * round_up(b[i].rows, 8) * 4;
+      p.bytes += size_t(splits) * a[i].rows * round_up(b[i].rows, 8) * 4;
       p.bytes = round_up(p.bytes, 256);
     }
   }
   return p;
+}
+
+// Deals a launch's work items to the eight XCDs: contiguous ranges (items that
+// follow each other share operands) with an eighth of the stages each.  An empty
+// item counts as one stage.
+void share_out(MxGemmArgs& g, int64_t items, double stages) {
+  int64_t at = 0;
+  double before = 0;
+  int x = 0;
+  g.c.xcd[0] = 0;
+  for (int i = 0; i < g.n && x < 7; ++i) {
+    const MxProduct& p = g.m[i];
+    const int64_t own = (i + 1 < g.n ? g.base[i + 1] : items) - at;
+    const double per = std::max(1.0, double(p.tiles) * p.kt / own);
+    while (x < 7 && before + own * per >= stages * (x + 1) / 8) {
+      const double want = (stages * (x + 1) / 8 - before) / per;
+      g.c.xcd[++x] = int32_t(at + std::min<int64_t>(own, std::max<int64_t>(0, int64_t(want + 0.5))));
+    }
+    at += own;
+    before += own * per;
+  }
+  while (x < 8) g.c.xcd[++x] = int32_t(items);
 }
 
 }  // namespace
@@ -388,70 +413,70 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
   if (conflict(spans)) return MUON_E_ALIAS;
   hipStream_t s = static_cast<hipStream_t>(stream);
 
-  // products whose contraction is split write fp32 partials, the others their result
-  for (const bool split : {false, true}) {
-    int64_t items = 0, blocks = 0;
+  // with a split contraction every product of the list writes fp32 partials, so
+  // that one launch holds them all
+  const bool split = plan.chunk != 0;
+  int64_t items = 0, blocks = 0;
+  double stages = 0;
+  g.c.accumulate = split ? 0 : red.c.accumulate;
+  if (!split) g.c.drop = red.c.drop;
+  auto flush = [&]() {
+    share_out(g, items, stages);
+    if (g.n && launch_mx_gemm(g, split ? int(kF32) : out[0].dtype, plan.tile_m, s) != hipSuccess)
+      return MUON_E_HIP;
+    if (red.n && launch_mx_reduce(red, out[0].dtype, blocks, s) != hipSuccess) return MUON_E_HIP;
     g.n = red.n = 0;
-    g.c.accumulate = split ? 0 : red.c.accumulate;
-    g.c.drop = split ? MxDrop{} : red.c.drop;
-    auto flush = [&]() {
-      g.c.items = int32_t(items);
-      if (g.n && launch_mx_gemm(g, split ? int(kF32) : out[0].dtype, plan.tile_m, s) != hipSuccess)
-        return MUON_E_HIP;
-      if (split && g.n && launch_mx_reduce(red, out[0].dtype, blocks, s) != hipSuccess)
-        return MUON_E_HIP;
-      g.n = red.n = 0;
-      items = blocks = 0;
-      return MUON_OK;
-    };
-    for (int i = 0; i < n; ++i) {
-      const int64_t M = a[i].rows, N = b[i].rows, kt = ceil_div(a[i].cols, kMxTileK);
-      const int64_t tiles = ceil_div(M, plan.tile_m) * ceil_div(N, kTileN);
-      const int64_t chunk = plan.chunk && kt > plan.chunk ? even_chunk(kt, plan.chunk) : std::max<int64_t>(kt, 1);
-      const int64_t splits = std::max<int64_t>(1, ceil_div(kt, chunk));
-      if (tiles == 0 || (splits > 1) != split) continue;
-      const int64_t nb = split ? ceil_div(M * (round_up(N, 8) / 8), 256) : 0;
-      if (g.n == kMxMaxList || items + tiles * splits > kMaxBlocks || blocks + nb > kMaxBlocks)
-        if ((rc = int(flush())) != MUON_OK) return rc;
-      MxProduct& p = g.m[g.n];
-      p.ac = static_cast<const uint8_t*>(a[i].codes);
-      p.as = static_cast<const uint8_t*>(a[i].scales);
-      p.bc = static_cast<const uint8_t*>(b[i].codes);
-      p.bs = static_cast<const uint8_t*>(b[i].scales);
-      p.M = int32_t(M);
-      p.N = int32_t(N);
-      p.kt = int32_t(kt);
-      p.chunk = int32_t(chunk);
-      p.tiles = int32_t(tiles);
-      p.index = i;
-      if (split) {
-        MxReduce& r = red.m[g.n];
-        r.ldp = int32_t(round_up(N, 8));
-        r.stride = M * r.ldp;
-        r.in = reinterpret_cast<const float*>(static_cast<char*>(workspace) + plan.offset[i]);
-        r.out = out[i].ptr;
-        r.ld = out[i].ld;
-        r.M = p.M;
-        r.N = p.N;
-        r.splits = int32_t(splits);
-        r.index = i;
-        red.base[g.n] = uint32_t(blocks);
-        red.n = g.n + 1;
-        p.out = const_cast<float*>(r.in);
-        p.ld = r.ldp;
-        p.stride = r.stride;
-      } else {
-        p.out = out[i].ptr;
-        p.ld = out[i].ld;
-        p.stride = 0;
-      }
-      g.base[g.n++] = uint32_t(items);
-      items += tiles * splits;
-      blocks += nb;
+    items = blocks = 0;
+    stages = 0;
+    return MUON_OK;
+  };
+  for (int i = 0; i < n; ++i) {
+    const int64_t M = a[i].rows, N = b[i].rows, kt = ceil_div(a[i].cols, kMxTileK);
+    const int64_t tiles = ceil_div(M, plan.tile_m) * ceil_div(N, kTileN);
+    if (tiles == 0) continue;
+    const int64_t chunk = split ? even_chunk(kt, plan.chunk) : std::max<int64_t>(kt, 1);
+    const int64_t splits = std::max<int64_t>(1, ceil_div(kt, chunk));
+    const int64_t nb = split ? ceil_div(M * (round_up(N, 8) / 8), 256) : 0;
+    if (g.n == kMxMaxList || items + tiles * splits > kMaxBlocks || blocks + nb > kMaxBlocks)
+      if ((rc = int(flush())) != MUON_OK) return rc;
+    MxProduct& p = g.m[g.n];
+    p.ac = static_cast<const uint8_t*>(a[i].codes);
+    p.as = static_cast<const uint8_t*>(a[i].scales);
+    p.bc = static_cast<const uint8_t*>(b[i].codes);
+    p.bs = static_cast<const uint8_t*>(b[i].scales);
+    p.out = out[i].ptr;
+    p.ld = out[i].ld;
+    p.stride = 0;
+    p.M = int32_t(M);
+    p.N = int32_t(N);
+    p.kt = int32_t(kt);
+    p.chunk = int32_t(chunk);
+    p.tiles = int32_t(tiles);
+    p.index = i;
+    if (split) {
+      MxReduce& r = red.m[g.n];
+      std::memset(&r, 0, sizeof(r));
+      r.ldp = int32_t(round_up(N, 8));
+      r.stride = M * r.ldp;
+      r.in = reinterpret_cast<const float*>(static_cast<char*>(workspace) + plan.offset[i]);
+      r.out = out[i].ptr;
+      r.ld = out[i].ld;
+      r.M = p.M;
+      r.N = p.N;
+      r.splits = int32_t(splits);
+      r.index = i;
+      red.base[g.n] = uint32_t(blocks);
+      red.n = g.n + 1;
+      p.out = const_cast<float*>(r.in);
+      p.ld = r.ldp;
+      p.stride = r.stride;
     }
-    if ((rc = int(flush())) != MUON_OK) return rc;
+    g.base[g.n++] = uint32_t(items);
+    items += tiles * splits;
+    blocks += nb;
+    stages += double(tiles) * kt;
   }
-  return MUON_OK;
+  return flush();
 } catch (...) {   // an allocation of the host's failed
   return MUON_E_HIP;
 }

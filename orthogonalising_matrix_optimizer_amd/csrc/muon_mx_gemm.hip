@@ -8,6 +8,7 @@
 // lane holds the bytes of four row tiles, picked by the instruction's byte
 // select.  b is the instruction's first operand, so a lane's four results are
 // consecutive columns of out.
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 #include <utility>
@@ -174,9 +175,8 @@ __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(
   const uint32_t lds = lds_addr(smem);
 
   // items of this block: XCD x (blocks b = x mod 8) owns a contiguous range
-  const uint32_t total = args.c.items, grid = gridDim.x, x = blockIdx.x & 7, loc = blockIdx.x >> 3;
-  const uint32_t q = total >> 3, rem = total & 7;
-  const uint32_t first = x * q + (x < rem ? x : rem), last = first + q + (x < rem ? 1 : 0);
+  const uint32_t grid = gridDim.x, x = blockIdx.x & 7, loc = blockIdx.x >> 3;
+  const uint32_t first = args.c.xcd[x], last = args.c.xcd[x + 1];
   const uint32_t step = (grid + 7 - x) >> 3;
 
   const int t = threadIdx.x, lane = t & 63;
@@ -317,7 +317,9 @@ __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(
         if constexpr (DROP) drop8(v, c / 8, row, p.index, seed, args.c.drop);
         T* o = out + row * p.ld + c;
         if (whole) {
-          stream8(o, v);
+          // partial products are read again at once
+          if (p.stride) store8(o, v);
+          else stream8(o, v);
         } else if (c + 8 <= p.N) {
           if (args.c.accumulate) {
             float w[8];
@@ -357,7 +359,10 @@ hipError_t launch_tile(const Args& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     raised.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int blocks = a.c.items < kCUs * PER_CU ? a.c.items : kCUs * PER_CU;
+  // as many blocks on every XCD as the longest range has items, if they fit
+  int most = 0;
+  for (int x = 0; x < 8; ++x) most = std::max(most, a.c.xcd[x + 1] - a.c.xcd[x]);
+  const int blocks = std::min(8 * most, kCUs * PER_CU);
   hipLaunchKernelGGL(k, dim3(blocks), dim3(64 * NW), lds, s, a);
   return hipGetLastError();
 }
