@@ -185,7 +185,7 @@ ProductPlan plan_products(const muon_mx* a, const muon_mx* b, int n) {
       items += double(splits) * ceil_div(a[i].rows, 128) * ceil_div(b[i].rows, kTileN);
       bytes += 8.0 * splits * a[i].rows * b[i].rows;
     }
-    const double t = list_us(kStage128, 3, items, w128, double(c)) + bytes / 6e6 + 5;
+    const double t = list_us(kStage128, 3, items, w128, double(even_chunk(int64_t(longest), c))) + bytes / 6e6 + 5;
     if (t < 0.9 * best) {
       best = t / 0.9;
       p.chunk = c;
