@@ -172,20 +172,21 @@ ProductPlan plan_products(const muon_mx* a, const muon_mx* b, int n) {
   double best = list_us(kStage128, 3, i128, w128, longest);
   p.tile_m = t256 < best ? 256 : 128;
   best = std::min(best, t256);
-  // Splitting adds the partial products' way through the caches and back (6
+  // Splitting adds the partial products' way through the caches and back (8
   // TB/s) and a launch (5 us); it pays for few tiles with a long contraction and
   // for lists with one much longer than the rest, us (whole | split): 768 x 768
   // x 8192 33 | 20, 128 x 2560 x 10240 40 | 18, 1408 x 2048 x 16384 65 | 50,
   // twelve 768 x 768 with K of 1630 to 23201 100 | 66; but 2560 x 2560 x 16384
   // 81 | 88 and 512 x 2048 x 4096 19 | 20.
   for (int64_t c = kMinChunk; c < longest; c += c / 2) {
-    double items = 0, bytes = 0;
+    double items = 0, bytes = 0, part = 0;
     for (int i = 0; i < n; ++i) {
       const int64_t kt = ceil_div(a[i].cols, kMxTileK), splits = std::max<int64_t>(1, ceil_div(kt, c));
+      part = std::max(part, double(even_chunk(kt, c)));
       items += double(splits) * ceil_div(a[i].rows, 128) * ceil_div(b[i].rows, kTileN);
       bytes += 8.0 * splits * a[i].rows * b[i].rows;
     }
-    const double t = list_us(kStage128, 3, items, w128, double(even_chunk(int64_t(longest), c))) + bytes / 6e6 + 5;
+    const double t = list_us(kStage128, 3, items, w128, part) + bytes / 8e6 + 5;
     if (t < 0.9 * best) {
       best = t / 0.9;
       p.chunk = c;
