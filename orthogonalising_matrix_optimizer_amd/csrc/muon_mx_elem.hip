@@ -87,30 +87,46 @@ __device__ __forceinline__ void drop16(uint32_t* q, uint32_t row, uint32_t c, ui
   }
 }
 
-// Code of x 2^-e (magnitude at most 6) rounded stochastically: up where 256
-// times the fraction of the step exceeds r + 1/2.
-//
-// bf16: x is scaled to 2^-126 times its place on the grid, where the grid's
-// steps are fp32 bit patterns a multiple of 2^22 apart (the subnormal grid
-// falls on the fp32 subnormals), so adding the random byte below bit 22 carries
-// into the code exactly when the element goes up, the threshold (2 r + 1) /
-// 512 of a step being ((255 - r) << 14) + 0x1FFF below the next step.  What
-// scaling rounds away of a bf16's eight digits is below every threshold.
-template <int DT>
-__device__ __forceinline__ uint32_t code_sr(float x, uint32_t byte, uint32_t not_r) {
-  if constexpr (DT == kBF16) {
-    const uint32_t s = __float_as_uint(__builtin_ldexpf(x, 1 - static_cast<int>(byte))) + 0x1FFFu +
-                       (not_r << 14);
-    return ((s >> 22) & 7u) | ((s >> 28) & 8u);
-  } else {
-    // 2^(127 - byte), an ordinary number: a finite block's byte is at most 253
-    const float t = x * __uint_as_float((254u - byte) << 23), a = fabsf(t);
-    const float inv = a >= 4.f ? 0.5f : a >= 2.f ? 1.f : 2.f;
-    const uint32_t base = a >= 4.f ? 4u : a >= 2.f ? 2u : 0u;
-    const float q = a * inv, low = floorf(q);
-    const uint32_t up = (q - low) * 256.f > static_cast<float>(255u - not_r) + 0.5f;
-    return static_cast<uint32_t>(low) + up + base + ((__float_as_uint(t) >> 28) & 8u);
+// Code of an fp32 x over its scale (magnitude at most 6) rounded
+// stochastically: up where 256 times the fraction of the step exceeds r + 1/2.
+__device__ __forceinline__ uint32_t code_sr(float x, uint32_t byte, uint32_t r) {
+  // 2^(127 - byte), an ordinary number: a finite block's byte is at most 253
+  const float t = x * __uint_as_float((254u - byte) << 23), a = fabsf(t);
+  const float inv = a >= 4.f ? 0.5f : a >= 2.f ? 1.f : 2.f;
+  const uint32_t base = a >= 4.f ? 4u : a >= 2.f ? 2u : 0u;
+  const float q = a * inv, low = floorf(q);
+  const uint32_t up = (q - low) * 256.f > static_cast<float>(r) + 0.5f;
+  return static_cast<uint32_t>(low) + up + base + ((__float_as_uint(t) >> 28) & 8u);
+}
+
+// The same for eight bf16 elements in four dwords.  Each is scaled to 2^-126
+// times its place on the grid, where the grid's steps are fp32 bit patterns 2^22
+// apart (the subnormal grid falls on the fp32 subnormals), so with the pattern
+// shifted up by two the code is its top byte, and adding the random byte below
+// carries into the code exactly when the element goes up: the threshold
+// (2 r + 1) / 512 of a step lies ((255 - r) << 16) + 0x7FFC below the next
+// (three more change nothing: the pattern's last two bits are zero).  What
+// scaling rounds away of a bf16's eight digits is below every threshold.  The
+// signs come from the elements' own top bytes.  Byte selects throughout: the
+// instruction count bounds the kernel.
+__device__ __forceinline__ uint32_t bytes(uint32_t hi, uint32_t lo, uint32_t select) {
+  return __builtin_amdgcn_perm(hi, lo, select);
+}
+__device__ __forceinline__ uint32_t encode8_sr(const uint32_t* q, uint32_t byte, const uint32_t* r8) {
+  const int up = 1 - static_cast<int>(byte);
+  uint32_t t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x = i & 1 ? q[i / 2] & 0xffff0000u : q[i / 2] << 16;
+    const uint32_t s = __float_as_uint(__builtin_ldexpf(__uint_as_float(x), up));
+    t[i] = (s << 2) + bytes(0x7FFFu, ~r8[i / 4], 0x06000504u | (i & 3) << 16);
   }
+  constexpr uint32_t kLow = 0x0c0c0703u, kHigh = 0x07030c0cu;   // the two top bytes, below or above
+  const uint32_t even = bytes(t[2], t[0], kLow) | bytes(t[6], t[4], kHigh);
+  const uint32_t odd = bytes(t[3], t[1], kLow) | bytes(t[7], t[5], kHigh);
+  const uint32_t neg_even = (bytes(q[1], q[0], 0x0c0c0501u) | bytes(q[3], q[2], 0x05010c0cu)) & 0x80808080u;
+  const uint32_t neg_odd = (bytes(q[1], q[0], kLow) | bytes(q[3], q[2], kHigh)) & 0x80808080u;
+  return even | odd << 4 | neg_even >> 4 | neg_odd;
 }
 
 // Eight codes of a block in a dword, element i in bits 4 i; r8: their random
@@ -119,12 +135,12 @@ template <int DT, bool SR>
 __device__ __forceinline__ uint32_t encode8(const uint32_t* q, uint32_t byte, const uint32_t* r8) {
   if constexpr (SR) {
     uint32_t out = 0;
+    if constexpr (DT == kBF16) {
+      out = encode8_sr(q, byte, r8);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float x;
-      if constexpr (DT == kBF16) x = __uint_as_float(i & 1 ? q[i / 2] & 0xffff0000u : q[i / 2] << 16);
-      else x = __uint_as_float(q[i]);
-      out |= code_sr<DT>(x, byte, (~r8[i / 4] >> (8 * (i & 3))) & 255u) << (4 * i);
+      for (int i = 0; i < 8; ++i)
+        out |= code_sr(__uint_as_float(q[i]), byte, (r8[i / 4] >> (8 * (i & 3))) & 255u) << (4 * i);
     }
     return byte == kMxNan ? 0u : out;
   } else if constexpr (DT == kBF16) {
