@@ -439,6 +439,11 @@ __global__ __launch_bounds__(64 * NW) void k_mx_rows(MxRowsArgs a) {
   for (int i = 0; i < R; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   constexpr int NQ = XDT == kBF16 ? 1 : 2;   // 16-byte loads of eight elements
   const int row = lane >> 4, ch = lane & 15;
+  // rows past x's last are read as the last one again: their sums are not stored
+  const X* const xrow = static_cast<const X*>(a.x);
+  int64_t xoff[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) xoff[h] = (4 * h + row < a.M ? 4 * h + row : a.M - 1) * a.ldx + ch * 8;
   struct Step {
     i32x4_t w[R];
     uint32_t ws;
@@ -451,25 +456,25 @@ __global__ __launch_bounds__(64 * NW) void k_mx_rows(MxRowsArgs a) {
       s.w[i] = *glb(reinterpret_cast<const i32x4_t*>(a.bc + (static_cast<int64_t>(k) * rt + t) * kMxTileBytes) + lane);
     }
     s.ws = *glb(reinterpret_cast<const uint32_t*>(a.bs + (static_cast<int64_t>(k) * st + (rt0 >> 2)) * kMxScaleBytes) + lane);
+    const X* p = xrow + k * kMxTileK;
+    if ((k + 1) * kMxTileK <= a.K) {
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) s.x[h][q] = load16b(p + xoff[h] + q * (8 / NQ));
+      return;
+    }
     const int c = k * kMxTileK + ch * 8;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
 #pragma unroll
       for (int q = 0; q < NQ; ++q) s.x[h][q] = u32x4_t{0, 0, 0, 0};
-      const int r = 4 * h + row;
-      if (4 * h >= a.M || r >= a.M) continue;
-      const X* p = static_cast<const X*>(a.x) + static_cast<int64_t>(r) * a.ldx + c;
-      if (c + 8 <= a.K) {
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) s.x[h][q] = load16b(p + q * (8 / NQ));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < a.K) {
-            if constexpr (XDT == kBF16) s.x[h][0][e / 2] |= static_cast<uint32_t>(*glb(p + e)) << (16 * (e & 1));
-            else s.x[h][e / 4][e & 3] = __float_as_uint(*glb(p + e));
-          }
-      }
+      for (int e = 0; e < 8; ++e)
+        if (c + e < a.K) {
+          if constexpr (XDT == kBF16) s.x[h][0][e / 2] |= static_cast<uint32_t>(*glb(p + xoff[h] + e)) << (16 * (e & 1));
+          else s.x[h][e / 4][e & 3] = __float_as_uint(*glb(p + xoff[h] + e));
+        }
     }
   };
   auto multiply = [&](const Step& s) {
