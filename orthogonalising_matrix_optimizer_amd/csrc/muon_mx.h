@@ -175,7 +175,8 @@ hipError_t launch_mx_quantize(const MxQuantArgs& a, int dt, bool rows, bool cols
                               int64_t blocks, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxDequantArgs& a, int dt, int64_t blocks, hipStream_t s);
 // tile_m: rows of the output tiles (256 or 128; always 128 columns)
-hipError_t launch_mx_gemm(const MxGemmArgs& a, int odt, int tile_m, hipStream_t s);
+// keep: the outputs go into the caches, not past them
+hipError_t launch_mx_gemm(const MxGemmArgs& a, int odt, int tile_m, bool keep, hipStream_t s);
 hipError_t launch_mx_reduce(const MxReduceArgs& a, int odt, int64_t blocks, hipStream_t s);
 hipError_t launch_mx_rows(const MxRowsArgs& a, int xdt, int odt, hipStream_t s);
 hipError_t launch_dropout(const MxDropArgs& a, int dt, int64_t blocks, hipStream_t s);

@@ -123,6 +123,17 @@ int drop_of(float p, uint64_t seed, const uint64_t* dev, MxDrop* d) {
 
 int64_t round_up(int64_t v, int64_t a) { return ceil_div(v, a) * a; }
 
+// Whether `bytes` of outputs are written past the caches.  The memory side's
+// cache holds 256 MiB.  Outputs of half of it and more, if they fit, push out
+// what the next call reads; smaller ones don't, and larger ones would be written
+// to memory in the call anyway.  A quantisation and a product after each other,
+// K = 2560, N = 10240, past the caches | into them: 4096 rows (80 MiB) 69 | 67
+// us, 8192 (160) 132 | 143, 12288 (240) 188 | 206, 16384 (320) 303 | 286; a
+// layer's step of 16384 rows (outputs of 320, 80 and 50 MiB) 952 | 897.
+bool past_caches(int64_t bytes) {
+  return bytes > int64_t(128) << 20 && bytes <= int64_t(256) << 20;
+}
+
 // How a list of products is run: the tile height, and the contraction length
 // (in code tiles) above which a product is split, 0 for none; per product the
 // workspace offset of its partial products.
@@ -417,17 +428,18 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
   // with a split contraction every product of the list writes fp32 partials, so
   // that one launch holds them all
   const bool split = plan.chunk != 0;
-  int64_t items = 0, blocks = 0;
+  int64_t items = 0, blocks = 0, written = 0;
   double stages = 0;
   g.c.accumulate = split ? 0 : red.c.accumulate;
   if (!split) g.c.drop = red.c.drop;
   auto flush = [&]() {
     share_out(g, items, stages);
-    if (g.n && launch_mx_gemm(g, split ? int(kF32) : out[0].dtype, plan.tile_m, s) != hipSuccess)
+    if (g.n && launch_mx_gemm(g, split ? int(kF32) : out[0].dtype, plan.tile_m,
+                              split || !past_caches(written), s) != hipSuccess)
       return MUON_E_HIP;
     if (red.n && launch_mx_reduce(red, out[0].dtype, blocks, s) != hipSuccess) return MUON_E_HIP;
     g.n = red.n = 0;
-    items = blocks = 0;
+    items = blocks = written = 0;
     stages = 0;
     return MUON_OK;
   };
@@ -475,6 +487,7 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
     g.base[g.n++] = uint32_t(items);
     items += tiles * splits;
     blocks += nb;
+    written += M * N * esize(out[i].dtype);
     stages += double(tiles) * kt;
   }
   return flush();

@@ -150,6 +150,7 @@ __device__ __forceinline__ void wait_stage(int ahead, bool extra) {
 // blocks of an XCD neighbouring ones) and the stages of its items form one
 // sequence, so an item's stores run beside the next item's loads.  PER_CU
 // blocks share a CU, and one multiplies while another waits at its barrier.
+// KEEP: the output goes into the caches, else past them.
 //
 // Measured on MI355X (random codes, 16384 x 2560 outputs, K = 10240): 256 x 128
 // tiles of four waves, two blocks a CU, 3.9-4.3 PF; 128 x 128, three blocks,
@@ -159,7 +160,7 @@ __device__ __forceinline__ void wait_stage(int ahead, bool extra) {
 // LDS loads of a stage need as long as its products (skipping parts at 16384 x
 // 4096 x 10240: all 312 us, without loads 228, without LDS reads 280, without
 // products 215, loads alone 215).
-template <class Args, int ODT, int TM, int TN, int WM, int WN, int NST, int PER_CU, bool DROP>
+template <class Args, int ODT, int TM, int TN, int WM, int WN, int NST, int PER_CU, bool DROP, bool KEEP>
 __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(Args args) {
   using T = typename std::conditional<ODT == kBF16, uint16_t, float>::type;
   constexpr int NW = WM * WN;
@@ -317,8 +318,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(
         if constexpr (DROP) drop8(v, c / 8, row, p.index, seed, args.c.drop);
         T* o = out + row * p.ld + c;
         if (whole) {
-          // partial products are read again at once
-          if (p.stride) store8(o, v);
+          if constexpr (KEEP) store8(o, v);
           else stream8(o, v);
         } else if (c + 8 <= p.N) {
           if (args.c.accumulate) {
@@ -340,14 +340,14 @@ __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(
 
 constexpr int kCUs = 256;
 
-template <class Args, int ODT, int TM, int TN, int NST, int PER_CU, bool DROP>
+template <class Args, int ODT, int TM, int TN, int NST, int PER_CU, bool DROP, bool KEEP>
 hipError_t launch_tile(const Args& a, hipStream_t s) {
   constexpr int WM = 2, WN = 2, NW = WM * WN;
   using OpN = Operand<TN, NW, 0>;
   using OpM = Operand<TM, NW, 1>;
   constexpr int lds = NST * (OpN::kBytes + OpM::kBytes + OpN::kScales + OpM::kScales);
   static_assert(lds * PER_CU <= 160 * 1024, "LDS");
-  auto* k = &k_mx_gemm<Args, ODT, TM, TN, WM, WN, NST, PER_CU, DROP>;
+  auto* k = &k_mx_gemm<Args, ODT, TM, TN, WM, WN, NST, PER_CU, DROP, KEEP>;
   // the LDS limit is raised once per device
   static std::atomic<uint64_t> raised{0};
   int dev = 0;
@@ -368,17 +368,22 @@ hipError_t launch_tile(const Args& a, hipStream_t s) {
 }
 
 template <class Args, int ODT, bool DROP>
-hipError_t launch_drop(const Args& a, int tile_m, hipStream_t s) {
-  return tile_m == 256 ? launch_tile<Args, ODT, 256, 128, 3, 2, DROP>(a, s)
-                       : launch_tile<Args, ODT, 128, 128, 3, 3, DROP>(a, s);
+hipError_t launch_keep(const Args& a, int tile_m, bool keep, hipStream_t s) {
+  if (tile_m == 256)
+    return keep ? launch_tile<Args, ODT, 256, 128, 3, 2, DROP, true>(a, s)
+                : launch_tile<Args, ODT, 256, 128, 3, 2, DROP, false>(a, s);
+  return keep ? launch_tile<Args, ODT, 128, 128, 3, 3, DROP, true>(a, s)
+              : launch_tile<Args, ODT, 128, 128, 3, 3, DROP, false>(a, s);
 }
 
 template <class Args>
-hipError_t launch_gemm_of(const Args& a, int odt, int tile_m, hipStream_t s) {
+hipError_t launch_gemm_of(const Args& a, int odt, int tile_m, bool keep, hipStream_t s) {
   const bool drop = a.c.drop.threshold != 0;
   if (odt == kBF16)
-    return drop ? launch_drop<Args, kBF16, true>(a, tile_m, s) : launch_drop<Args, kBF16, false>(a, tile_m, s);
-  return drop ? launch_drop<Args, kF32, true>(a, tile_m, s) : launch_drop<Args, kF32, false>(a, tile_m, s);
+    return drop ? launch_keep<Args, kBF16, true>(a, tile_m, keep, s)
+                : launch_keep<Args, kBF16, false>(a, tile_m, keep, s);
+  return drop ? launch_keep<Args, kF32, true>(a, tile_m, keep, s)
+              : launch_keep<Args, kF32, false>(a, tile_m, keep, s);
 }
 
 // Sum of the partial products of a split contraction, in the order of the
@@ -548,8 +553,9 @@ hipError_t launch_rows(const MxRowsArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_mx_gemm(const MxGemmArgs& a, int odt, int tile_m, hipStream_t s) {
-  return a.n == 1 ? launch_gemm_of(list_of_one(a), odt, tile_m, s) : launch_gemm_of(a, odt, tile_m, s);
+hipError_t launch_mx_gemm(const MxGemmArgs& a, int odt, int tile_m, bool keep, hipStream_t s) {
+  return a.n == 1 ? launch_gemm_of(list_of_one(a), odt, tile_m, keep, s)
+                  : launch_gemm_of(a, odt, tile_m, keep, s);
 }
 
 hipError_t launch_mx_rows(const MxRowsArgs& a, int xdt, int odt, hipStream_t s) {

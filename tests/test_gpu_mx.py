@@ -345,3 +345,20 @@ def test_linear_shapes_pairs_and_accumulation():
     y0, s0 = mo.mx_linear(x[:0], pair.w, save=True)
     dx0, dw0 = mo.mx_linear_grad(dy[:0], pair.w_t, s0)
     assert y0.shape == (0, 80) and dx0.shape == (0, 96) and not dw0.any()
+
+
+def test_matmul_output_past_the_caches():
+    """Outputs between half of the last cache and all of it take another kind of store."""
+    M, N, K = 8200, 8200, 130
+    announce(f"matmul {M}x{N}x{K} past the caches")
+    qa, qb = mo.mx_quantize(_rand(M, K, BF16, 1)), mo.mx_quantize(_rand(N, K, BF16, 2))
+    out = torch.full((M + 1, N + 3), 7.0, device="cuda", dtype=BF16)
+    mo.mx_matmul(qa, qb, out=out[:M, :N])
+    assert 128 << 20 < 2 * M * N <= 256 << 20
+    rows = torch.tensor([0, 1, 127, 128, 255, 4095, 4096, 8191, 8192, M - 1], device="cuda")
+    da, db = mo.mx_dequantize(qa, dtype=F32), mo.mx_dequantize(qb, dtype=F32)
+    exact = da[rows].double() @ db.double().t().contiguous()
+    size = da[rows].double().abs() @ db.double().abs().t().contiguous()
+    tol = K * 2.0 ** -23 * size + 2.0 ** -8 * (exact.abs() + K * 2.0 ** -23 * size)
+    assert bool(((out[rows, :N].double() - exact).abs() <= tol).all())
+    assert bool((out[M:] == 7.0).all()) and bool((out[:, N:] == 7.0).all())
