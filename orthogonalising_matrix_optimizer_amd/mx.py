@@ -10,6 +10,7 @@ packed as bytes (a call on a single token costs less than its launches).
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from struct import Struct
 from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
@@ -20,6 +21,7 @@ from . import _lib
 _DT = {torch.bfloat16: _lib.MUON_BF16, torch.float32: _lib.MUON_F32}
 _MAT, _MX = "Pqqqii", "PPqq"      # muon_mat, muon_mx
 _MAT1, _MX1 = Struct(_MAT), Struct(_MX)
+_structs = lru_cache(maxsize=256)(lambda fields, n: Struct(fields * n))
 _SPLIT = _lib.CODES["MUON_E_WORKSPACE"]
 
 Seed = Union[int, torch.Tensor]
@@ -94,13 +96,14 @@ def _new_mx(rows, cols, device):
         buf = torch.empty(k * (t + -(-r // 64) * 256), dtype=torch.uint8, device=device)
         p = buf.data_ptr()
         return [MX4(buf, 0, device, (p, p + k * t, r, c) if p else (0, 0, r, c))]
-    sizes = [(-(-r // 16) * 1024 + -(-r // 64) * 256) * -(-c // 128) for r, c in zip(rows, cols)]
-    buf = torch.empty(sum(sizes), dtype=torch.uint8, device=device)
+    codes = [(r + 15 >> 4) * (c + 127 >> 7) << 10 for r, c in zip(rows, cols)]
+    scales = [(r + 63 >> 6) * (c + 127 >> 7) << 8 for r, c in zip(rows, cols)]
+    buf = torch.empty(sum(codes) + sum(scales), dtype=torch.uint8, device=device)
     p, at, out = buf.data_ptr(), 0, []
-    for r, c, n in zip(rows, cols, sizes):
+    for r, c, n, m in zip(rows, cols, codes, scales):
         q = p + at
-        out.append(MX4(buf, at, device, (q, q + -(-r // 16) * -(-c // 128) * 1024, r, c) if n else (0, 0, r, c)))
-        at += n
+        out.append(MX4(buf, at, device, (q, q + n, r, c) if n else (0, 0, r, c)))
+        at += n + m
     return out
 
 
@@ -120,7 +123,8 @@ def _new_dense(rows, cols, dtype, device):
         for r in rows:
             flat += (p, r, width, width, d, 0)
             p += r * step
-        return list(buf.split(rows)), Struct(_MAT * n).pack(*flat)
+        # nothing else refers to buf, so the parts need not be tied to it as views
+        return list(torch.unsafe_split_with_sizes(buf, rows)), _structs(_MAT, n).pack(*flat)
     ts = [torch.empty(s, dtype=dtype, device=device) for s in zip(rows, cols)]
     return ts, _mats(ts, device)
 
@@ -160,29 +164,33 @@ def _mat(t: torch.Tensor, dev: torch.device):
 
 
 def _flat(ts, dev):
-    """The fields of the muon_mats of 2-D tensors, one after the other."""
-    flat, at = [], dev.index
+    """The fields of the muon_mats of tensors' rows, one after the other."""
+    flat, at, dt = [], dev.index, _DT
     for t in ts:
-        r, c = t.shape
-        s, one = t.stride()
-        d = _DT.get(t.dtype)
-        if d is not None and one == 1 and s >= c and t.get_device() == at:
-            flat += (t.data_ptr(), r, c, s, d, 0)
-        else:
-            flat += _mat(t, dev)
+        # the usual operand without a call; any other is looked at in full
+        if isinstance(t, torch.Tensor) and t.is_contiguous() and t.get_device() == at and t.dtype in dt:
+            s = t.shape
+            if len(s) == 2:
+                r, c = s
+                flat += (t.data_ptr(), r, c, c, dt[t.dtype], 0)
+                continue
+        flat += _mat(_rows_of(t), dev)
     return flat
 
 
 def _mats(ts, dev) -> bytes:
     if len(ts) == 1:
         return _MAT1.pack(*_mat(ts[0], dev))
-    return Struct(_MAT * len(ts)).pack(*_flat(ts, dev))
+    return _structs(_MAT, len(ts)).pack(*_flat(ts, dev))
 
 
 def _pack_mx(ms) -> bytes:
     if len(ms) == 1:
         return _MX1.pack(*ms[0].desc)
-    return Struct(_MX * len(ms)).pack(*[v for m in ms for v in m.desc])
+    flat = []
+    for m in ms:
+        flat += m.desc
+    return _structs(_MX, len(ms)).pack(*flat)
 
 
 def _mxs(ms, dev) -> bytes:
@@ -270,13 +278,13 @@ def mx_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], transpose: Union
     if transpose not in (False, True, "both"):
         raise ValueError(f"transpose is False, True or 'both', not {transpose!r}")
     single = isinstance(x, torch.Tensor)
-    xs = [_rows_of(x)] if single else [_rows_of(t) for t in x]
+    xs = [x] if single else list(x)
     n = len(xs)
     if not xs:
         return []
-    dev = _gpu(xs[0].device)
+    dev = _gpu(_rows_of(xs[0]).device)
     flat = _flat(xs, dev)
-    mats = _MAT1.pack(*flat) if n == 1 else Struct(_MAT * n).pack(*flat)
+    mats = _MAT1.pack(*flat) if n == 1 else _structs(_MAT, n).pack(*flat)
     both = transpose == "both"
     rows = cols = None
     if out is None:
