@@ -124,15 +124,12 @@ int drop_of(float p, uint64_t seed, const uint64_t* dev, MxDrop* d) {
 int64_t round_up(int64_t v, int64_t a) { return ceil_div(v, a) * a; }
 
 // Whether `bytes` of outputs are written past the caches.  The memory side's
-// cache holds 256 MiB.  Outputs of half of it and more, if they fit, push out
-// what the next call reads; smaller ones don't, and larger ones would be written
-// to memory in the call anyway.  A quantisation and a product after each other,
-// K = 2560, N = 10240, past the caches | into them: 4096 rows (80 MiB) 69 | 67
-// us, 8192 (160) 132 | 143, 12288 (240) 188 | 206, 16384 (320) 303 | 286; a
-// layer's step of 16384 rows (outputs of 320, 80 and 50 MiB) 952 | 897.
-bool past_caches(int64_t bytes) {
-  return bytes > int64_t(128) << 20 && bytes <= int64_t(256) << 20;
-}
+// cache holds 256 MiB: outputs of half of it and more push out what the next
+// call reads, smaller ones may be read from it.  A quantisation and a product
+// after each other, K = 2560, N = 10240, into the caches | past them: 4096 rows
+// (80 MiB) 71 | 72 us, 8192 (160) 139 | 122, 12288 (240) 204 | 182, 16384 (320)
+// 280 | 259; a layer's step of 8192 rows 462 | 453, of 16384 with dropout 882 | 877.
+bool past_caches(int64_t bytes) { return bytes > int64_t(128) << 20; }
 
 // How a list of products is run: the tile height, and the contraction length
 // (in code tiles) above which a product is split, 0 for none; per product the

@@ -51,7 +51,7 @@ struct Operand {
   static_assert(ROWS / kMxTileR % NW == 0 && kScaleLanes <= 64 && SW < NW, "load split");
   uint64_t codes, scales;  // the next stage's row panel
   uint64_t kcode, kscale;  // bytes from one stage to the next
-  uint32_t vcode[kPer];    // byte offset of the wave's tiles in a panel
+  uint32_t vcode[kPer];    // byte offsets of the lane's pieces in a panel
   uint32_t vscale;
 
   __device__ __forceinline__ void plan(const uint8_t* c, const uint8_t* s, int row0, int rows,
@@ -65,7 +65,7 @@ struct Operand {
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int j = wave + NW * u;
-      vcode[u] = (j < rt - t0 ? j : rt - t0 - 1) * kMxTileBytes;
+      vcode[u] = (j < rt - t0 ? j : rt - t0 - 1) * kMxTileBytes + lane * 16;
     }
     const int g = lane * 16 / kMxScaleBytes;
     vscale = (g < st - s0 ? g : st - s0 - 1) * kMxScaleBytes + lane * 16 % kMxScaleBytes;
@@ -74,8 +74,7 @@ struct Operand {
   __device__ __forceinline__ void load(int wave, int lane, uint32_t dst, uint32_t sdst) {
     const u32x4_t dc = make_desc(reinterpret_cast<const void*>(codes), kBytes);
 #pragma unroll
-    for (int u = 0; u < kPer; ++u)
-      dma16(dc, dst + (wave + NW * u) * kMxTileBytes, lane * 16, vcode[u]);
+    for (int u = 0; u < kPer; ++u) dma16(dc, dst + (wave + NW * u) * kMxTileBytes, vcode[u], 0);
     if (wave == SW) {
       const u32x4_t ds = make_desc(reinterpret_cast<const void*>(scales), kScales);
       if (lane < kScaleLanes) dma16(ds, sdst, vscale, 0);
@@ -300,27 +299,64 @@ __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(
     T* out = static_cast<T*>(p.out) + it.split * p.stride;
     const bool whole = !args.c.accumulate && it.m0 + TM <= p.M && it.n0 + TN <= p.N;
     covered = whole ? issued : 0;
+    // eight columns of a row, from column c = column(i)
+    auto column = [&](int i) { return it.n0 + (wn * FN + i) * 16 + 8 * (lane >> 4); };
+    auto result = [&](int i, int j, int row, float* v) {
+      const bool swap = lane >= 32;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = swap ? acc[i + 1][j][e] : acc[i][j][e];
+        v[4 + e] = swap ? acc[i][j][e] : acc[i + 1][j][e];
+      }
+      if constexpr (DROP) drop8(v, column(i) / 8, row, p.index, seed, args.c.drop);
+    };
+    // A lane has 16-byte pieces a and b of its row's 128 bytes; lanes r and r + 8
+    // swap one, so that a store writes eight whole lines.  (Sixteen half lines past
+    // the caches took 1.4 times the bytes to memory: 8192 x 10240, K = 2560, 132
+    // against 125 us, 16384 x 10240 283 against 257.)
+    const bool up = lane & 8;
+    auto put = [&](T* o, u32x4_t a, u32x4_t b, int apart) {
+      u32x4_t got;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        got[e] = __builtin_amdgcn_update_dpp(0, up ? a[e] : b[e], 0x128 /* row_ror:8 */, 0xf, 0xf, false);
+      o += up ? apart : 0;
+      if constexpr (KEEP) {
+        store16b(o, up ? got : a);
+        store16b(o + 8 * p.ld, up ? b : got);
+      } else {
+        stream16b(o, up ? got : a);
+        stream16b(o + 8 * p.ld, up ? b : got);
+      }
+    };
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-      const int row = it.m0 + (wm * FM + j) * 16 + (lane & 15);
+      const int row = it.m0 + (wm * FM + j) * 16 + r;
+      if (whole) {
+        T* o = out + (row - (up ? 8 : 0)) * p.ld;
+#pragma unroll
+        for (int i = 0; i < FN; i += ODT == kBF16 ? 4 : 2) {
+          float v[8];
+          result(i, j, row, v);
+          if constexpr (ODT == kBF16) {
+            float w[8];
+            result(i + 2, j, row, w);
+            put(o + column(i), narrow8(v), narrow8(w), 32);
+          } else {
+            put(o + column(i), bits4(v), bits4(v + 4), 4);
+          }
+        }
+        continue;
+      }
       if (row >= p.M) continue;
 #pragma unroll
       for (int i = 0; i < FN; i += 2) {
-        const int c = it.n0 + (wn * FN + i) * 16 + 8 * (lane >> 4);
+        const int c = column(i);
         if (c >= p.N) continue;
-        const bool swap = lane >= 32;
         float v[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = swap ? acc[i + 1][j][e] : acc[i][j][e];
-          v[4 + e] = swap ? acc[i][j][e] : acc[i + 1][j][e];
-        }
-        if constexpr (DROP) drop8(v, c / 8, row, p.index, seed, args.c.drop);
+        result(i, j, row, v);
         T* o = out + row * p.ld + c;
-        if (whole) {
-          if constexpr (KEEP) store8(o, v);
-          else stream8(o, v);
-        } else if (c + 8 <= p.N) {
+        if (c + 8 <= p.N) {
           if (args.c.accumulate) {
             float w[8];
             load8(o, w);

@@ -168,11 +168,11 @@ def _flat(ts, dev):
     flat, at, dt = [], dev.index, _DT
     for t in ts:
         # the usual operand without a call; any other is looked at in full
-        if isinstance(t, torch.Tensor) and t.is_contiguous() and t.get_device() == at and t.dtype in dt:
-            s = t.shape
-            if len(s) == 2:
+        if isinstance(t, torch.Tensor) and t.is_contiguous() and t.get_device() == at:
+            s, d = t.shape, dt.get(t.dtype)
+            if len(s) == 2 and d is not None:
                 r, c = s
-                flat += (t.data_ptr(), r, c, c, dt[t.dtype], 0)
+                flat += (t.data_ptr(), r, c, c, d, 0)
                 continue
         flat += _mat(_rows_of(t), dev)
     return flat
