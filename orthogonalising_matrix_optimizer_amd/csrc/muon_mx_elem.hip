@@ -152,13 +152,15 @@ __device__ __forceinline__ uint32_t encode8(const uint32_t* q, uint32_t byte, co
 
 // One 128 x 128 tile of the input per block of sixteen waves.  A lane reads 16
 // consecutive elements of one row, so a block of 32 is a pair of lanes; for the
-// transpose the tile passes through LDS and half of the lanes take 32 rows of a
-// column each.  Short work per lane keeps small matrices quick and costs large
-// ones nothing: with four waves of four times the work, both orientations of
-// bf16 on MI355X, us (4 | 16 waves): 1 x 2560 3.8 | 3.1; 1024 x 1024 4.1 | 3.4;
-// 8192 x 2560 14.8 | 14.5; 16384 x 10240 98.8 | 96.5 (5.3 TB/s, as a copy).
-// Stochastically 1001 x 777 of fp32 17.0 | 9.8; 16384 x 10240 of bf16 151 | 157:
-// there the generator's products and the roundings are the bound.
+// transpose the tile passes through LDS and a pair of lanes takes 32 rows of a
+// column.  Short work per lane keeps small matrices quick and costs large ones
+// nothing: with four waves of four times the work, both orientations of bf16 on
+// MI355X, us (4 | 16 waves): 1 x 2560 3.8 | 3.1; 1024 x 1024 4.1 | 3.4; 8192 x
+// 2560 14.8 | 14.5; 16384 x 10240 98.8 | 96.5 (5.3 TB/s, as a copy).  To nearest
+// memory is the bound.  Stochastically it is the instruction count: the
+// generator's products and the roundings keep the vector units busy 96 % of the
+// time at 2.4 GHz, 16384 x 10240 of bf16 both ways 138 us (161 before the
+// byte selects of encode8_sr).
 template <class Args, int DT, bool ROWS, bool COLS, bool SR>
 __global__ __launch_bounds__(kQuantThreads) void k_mx_quantize(Args args) {
   constexpr int T = kMxQuantTile, PD = Elem<DT>::kPerDword, ND = 16 / PD;   // dwords of 16 elements

@@ -154,11 +154,12 @@ __device__ __forceinline__ void wait_stage(int ahead, bool extra) {
 // Measured on MI355X (random codes, 16384 x 2560 outputs, K = 10240): 256 x 128
 // tiles of four waves, two blocks a CU, 3.9-4.3 PF; 128 x 128, three blocks,
 // 3.5-3.8; 256 x 256 of eight waves 3.6-3.9 (with the two waves of a SIMD
-// alternating between reads and products 2.9).  The instruction alone sustains
-// 9.5 PF on zeros and 7.1 on random codes (power).  What bounds the loop: the
-// LDS loads of a stage need as long as its products (skipping parts at 16384 x
-// 4096 x 10240: all 312 us, without loads 228, without LDS reads 280, without
-// products 215, loads alone 215).
+// alternating between reads and products 2.9).  What bounds it: power and the
+// loads into LDS.  The instruction alone sustains 9.5 PF on zeros and 7.1 on
+// random codes; 16384 x 4096 x 10240 takes 304 us on zeros and 424 on random
+// codes (quantised normal numbers lie between), with every stage in L2 278 and
+// 360, the loads alone 194, and 156 from L2 (28 TB/s).  The matrix units are busy
+// 36-46 % of the time at 2.2-2.3 GHz in the products of a 2560 x 10240 layer.
 template <class Args, int ODT, int TM, int TN, int WM, int WN, int NST, int PER_CU, bool DROP, bool KEEP>
 __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(Args args) {
   using T = typename std::conditional<ODT == kBF16, uint16_t, float>::type;
