@@ -277,6 +277,9 @@ def mx_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], transpose: Union
     an earlier call of the same shapes and overwrites them."""
     if transpose not in (False, True, "both"):
         raise ValueError(f"transpose is False, True or 'both', not {transpose!r}")
+    both = transpose == "both"
+    if not both:
+        transpose = bool(transpose)      # 0, 1 and numpy's booleans pass the check above
     single = isinstance(x, torch.Tensor)
     xs = [x] if single else list(x)
     n = len(xs)
@@ -285,7 +288,6 @@ def mx_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], transpose: Union
     dev = _gpu(_rows_of(xs[0]).device)
     flat = _flat(xs, dev)
     mats = _MAT1.pack(*flat) if n == 1 else _structs(_MAT, n).pack(*flat)
-    both = transpose == "both"
     rows = cols = None
     if out is None:
         r, c = flat[1::6], flat[2::6]
@@ -456,5 +458,5 @@ def dropout(x: torch.Tensor, p: float, seed: Seed, out: Optional[torch.Tensor] =
         _set_seed(opt, "seed", seed, dev)
         _call("muon_dropout", dev, xm, om, p, 0, opt.seed_dev)
     else:
-        _call("muon_dropout", dev, xm, om, p, seed & 0xFFFFFFFFFFFFFFFF, None)
+        _call("muon_dropout", dev, xm, om, p, int(seed) & 0xFFFFFFFFFFFFFFFF, None)
     return res

@@ -194,8 +194,9 @@ class Muon:
         for again in self._mx_calls:
             again()
 
-    def _products(self, grads):
-        """`grads` with the gradients given as 4-bit factors multiplied out."""
+    def _products(self, grads, run: bool = True):
+        """`grads` with the buffers of the products where 4-bit factors were
+        given; `run` multiplies them."""
         at = [i for i, g in enumerate(grads) if not isinstance(g, torch.Tensor)]
         if not at:
             return grads
@@ -208,8 +209,9 @@ class Muon:
             if i not in self._pgrads:
                 self._pgrads[i] = torch.empty(self.params[i].shape, dtype=torch.float32,
                                               device=self.params[i].device)
-        _mx.mx_matmul([grads[i][0] for i in at], [grads[i][1] for i in at],
-                      out=[self._pgrads[i] for i in at])
+        if run:
+            _mx.mx_matmul([grads[i][0] for i in at], [grads[i][1] for i in at],
+                          out=[self._pgrads[i] for i in at])
         for i in at:
             grads[i] = self._pgrads[i]
         return grads
@@ -224,7 +226,8 @@ class Muon:
     def step_prepare(self, grads: List[torch.Tensor]) -> None:
         """Make the device descriptor table for these gradient buffers resident
         (no launch, counters unchanged), so a step with them can be captured."""
-        code = self.lib.muon_step_prepare(self._pmats, self._grad_mats(self._products(grads)),
+        code = self.lib.muon_step_prepare(self._pmats,
+                                          self._grad_mats(self._products(grads, run=False)),
                                           self.state, _stream())
         _lib.check(code, "muon_step_prepare")
 

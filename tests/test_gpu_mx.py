@@ -362,3 +362,16 @@ def test_matmul_output_past_the_caches():
     tol = K * 2.0 ** -23 * size + 2.0 ** -8 * (exact.abs() + K * 2.0 ** -23 * size)
     assert bool(((out[rows, :N].double() - exact).abs() <= tol).all())
     assert bool((out[M:] == 7.0).all()) and bool((out[:, N:] == 7.0).all())
+
+
+def test_numpy_arguments():
+    """numpy's booleans and integers do what Python's do."""
+    announce("numpy arguments")
+    x = _rand(40, 70, BF16, 4)
+    for yes in (1, np.True_):
+        assert torch.equal(mo.mx_quantize(x, yes).dequantize(F32), mo.mx_quantize(x, True).dequantize(F32))
+    for no in (0, np.False_):
+        assert torch.equal(mo.mx_quantize(x, no).dequantize(F32), mo.mx_quantize(x).dequantize(F32))
+    for seed in (np.int64(-5), np.uint64(2 ** 64 - 5)):
+        assert torch.equal(mo.dropout(x, 0.3, seed), mo.dropout(x, 0.3, -5))
+        assert torch.equal(mo.mx_quantize(x, seed=seed).dequantize(F32), mo.mx_quantize(x, seed=-5).dequantize(F32))

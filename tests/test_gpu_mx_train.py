@@ -304,3 +304,16 @@ def test_matrices_past_32_bit_offsets():
     b = np.concatenate([tail.T, a[2:]])
     want, s = b[:, :300].T @ b, np.abs(b[:, :300]).T @ np.abs(b)
     assert np.all(np.abs(host(z[:300]) - want) <= (len(marks) * 2.0 ** -23 + 2.0 ** -24) * s)
+
+
+def test_preparing_a_step_launches_no_product():
+    announce("step_prepare with factors")
+    ps = _params(SHAPES, 9)
+    opt = mo.Muon(ps, mx=True)
+    pairs = _pairs(opt, _batch(64, 1), 3)
+    opt.step(pairs)
+    for g in opt._pgrads.values():
+        g.fill_(7.0)
+    opt.step_prepare(pairs)
+    torch.cuda.synchronize()
+    assert all(bool((g == 7.0).all()) for g in opt._pgrads.values())
