@@ -375,3 +375,21 @@ def test_numpy_arguments():
     for seed in (np.int64(-5), np.uint64(2 ** 64 - 5)):
         assert torch.equal(mo.dropout(x, 0.3, seed), mo.dropout(x, 0.3, -5))
         assert torch.equal(mo.mx_quantize(x, seed=seed).dequantize(F32), mo.mx_quantize(x, seed=-5).dequantize(F32))
+
+
+@pytest.mark.parametrize("M,N,K", [(256, 128, 64), (300, 264, 200), (513, 385, 130), (128, 128, 9000), (40, 70, 33)])
+def test_matmul_with_dropout_is_dropout_of_matmul(M, N, K):
+    """Whole tiles, edges and split contractions drop the elements that dropout()
+    drops from the fp32 product, and scale them before the only rounding."""
+    announce(f"matmul with dropout {M}x{N}x{K}")
+    a, b = mo.mx_quantize(_rand(M, K, BF16, 31)), mo.mx_quantize(_rand(N, K, BF16, 32))
+    want = mo.dropout(mo.mx_matmul(a, b, dtype=F32), 0.3, 99)
+    assert torch.equal(mo.mx_matmul(a, b, dtype=F32, dropout=0.3, dropout_seed=99), want)
+    assert torch.equal(mo.mx_matmul(a, b, dropout=0.3, dropout_seed=99), want.to(BF16))
+    for dt in (F32, BF16):
+        out = torch.full((M, N + 5), 3.0, device="cuda", dtype=dt)
+        base = _rand(M, N, dt, 33)
+        out[:, :N] = base
+        mo.mx_matmul(a, b, out=out[:, :N], accumulate=True, dropout=0.3, dropout_seed=99)
+        assert torch.equal(out[:, :N], (base.float() + want).to(dt))
+        assert bool((out[:, N:] == 3.0).all())
