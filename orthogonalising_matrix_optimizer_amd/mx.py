@@ -88,12 +88,15 @@ def _mx_bytes(rows: int, cols: int) -> int:
     return (-(-rows // 16) * 1024 + -(-rows // 64) * 256) * -(-cols // 128)
 
 
+_empty = torch.empty_strided      # 0.4 us less than torch.empty on the host
+
+
 def _new_mx(rows, cols, device):
     """MX4 matrices of rows[i] x cols[i], in one allocation."""
     if len(rows) == 1:
         r, c = rows[0], cols[0]
         k, t = -(-c // 128), -(-r // 16) * 1024
-        buf = torch.empty(k * (t + -(-r // 64) * 256), dtype=torch.uint8, device=device)
+        buf = _empty((k * (t + -(-r // 64) * 256),), (1,), dtype=torch.uint8, device=device)
         p = buf.data_ptr()
         return [MX4(buf, 0, device, (p, p + k * t, r, c) if p else (0, 0, r, c))]
     codes = [(r + 15 >> 4) * (c + 127 >> 7) << 10 for r, c in zip(rows, cols)]
@@ -107,16 +110,25 @@ def _new_mx(rows, cols, device):
     return out
 
 
-def _new_dense(rows, cols, dtype, device):
-    """Dense rows[i] x cols[i] tensors and their packed muon_mat array; equally
-    wide ones share an allocation."""
+def _new_one(rows, cols, dtype, device):
+    """A dense rows x cols tensor and its packed muon_mat."""
     d = _DT.get(dtype)
     if d is None:
         raise ValueError(f"unsupported dtype {dtype}")
+    t = _empty((rows, cols), (cols or 1, 1), dtype=dtype, device=device)
+    return t, _MAT1.pack(t.data_ptr(), rows, cols, cols, d, 0)
+
+
+def _new_dense(rows, cols, dtype, device):
+    """Dense rows[i] x cols[i] tensors and their packed muon_mat array; equally
+    wide ones share an allocation."""
     n, width = len(rows), cols[0]
     if n == 1:
-        t = torch.empty((rows[0], width), dtype=dtype, device=device)
-        return [t], _MAT1.pack(t.data_ptr(), rows[0], width, width, d, 0)
+        t, mat = _new_one(rows[0], width, dtype, device)
+        return [t], mat
+    d = _DT.get(dtype)
+    if d is None:
+        raise ValueError(f"unsupported dtype {dtype}")
     if cols.count(width) == n:
         buf = torch.empty((sum(rows), width), dtype=dtype, device=device)
         p, step, flat = buf.data_ptr(), width * dtype.itemsize, []
@@ -209,7 +221,7 @@ def _device_of(m) -> torch.device:
 
 
 def _gpu(dev: torch.device) -> torch.device:
-    if dev.type != "cuda":
+    if dev.index is None:        # a tensor on a GPU names which
         raise ValueError("tensors must be on a GPU")
     return dev
 
@@ -395,12 +407,13 @@ def mx_linear(x: torch.Tensor, w: MX4, save: bool = False, dropout: float = 0.0,
     being what mx_linear_grad needs: the input's transpose in 4 bits."""
     x2 = _rows_of(x)
     rows, cols = x2.shape
-    if cols != w.cols:
+    _device_of(w)
+    if cols != w.desc[3]:
         raise ValueError(f"x has {cols} features, the layer takes {w.cols}")
     if not save and not dropout and rows <= _lib.MX_FEW_ROWS:
         dev = _gpu(x.device)
-        xm = _mats([x2], dev)
-        (y,), ym = _new_dense([rows], [w.rows], x.dtype, dev)
+        xm = _MAT1.pack(*_mat(x2, dev))
+        y, ym = _new_one(rows, w.desc[2], x.dtype, dev)
         _call("muon_mx_matmul_rows", dev, xm, _mxs([w], dev), ym)
         saved = None
     else:
@@ -446,7 +459,7 @@ def dropout(x: torch.Tensor, p: float, seed: Seed, out: Optional[torch.Tensor] =
     dev = _gpu(x.device)
     xm = _MAT1.pack(*_mat(x2, dev))
     if out is None:
-        (res,), om = _new_dense([x2.shape[0]], [x2.shape[1]], x.dtype, dev)
+        res, om = _new_one(*x2.shape, x.dtype, dev)
         if x.dim() != 2:
             res = res.view(x.shape)
     else:
