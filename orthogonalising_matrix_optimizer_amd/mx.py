@@ -6,7 +6,7 @@ function of a seed and is never stored.  The number format and the random
 numbers are stated in include/muon.h.  As in the rest of the package all
 computation runs in the HIP library; this module allocates outputs and passes
 pointers with the current stream of the tensors' device.  Descriptors are
-packed as bytes (a call on a single token costs less than its launches).
+packed as bytes: on a single token a call's cost is the host's.
 """
 from __future__ import annotations
 
