@@ -330,13 +330,15 @@ def mx_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], transpose: Union
 
 def quantize_again(xs: Sequence[torch.Tensor], pairs: Sequence[MXPair]):
     """The call mx_quantize(xs, "both", out=pairs) with its descriptors packed
-    once, for a list that is quantised again and again in the same memory."""
+    once, for a list that is quantised again and again in the same memory,
+    which the returned function keeps alive."""
     dev = xs[0].device
+    keep = list(xs), list(pairs)
     mats = _mats(xs, dev)
     rows, cols = _mxs([p.w for p in pairs], dev), _mxs([p.w_t for p in pairs], dev)
 
     def again() -> None:
-        _call("muon_mx_quantize", dev, mats, rows, cols, len(xs), None)
+        _call("muon_mx_quantize", dev, mats, rows, cols, len(keep[0]), None)
     return again
 
 
