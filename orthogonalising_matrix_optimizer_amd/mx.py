@@ -395,7 +395,8 @@ def mx_matmul(a: Union[MX4, Sequence[MX4]], b: Union[MX4, Sequence[MX4]],
     if code == _SPLIT:   # the list's contraction is split: give it room for the partial products
         ws = torch.empty(int(_lib.load().muon_mx_matmul_workspace_bytes(ca, cb, n)), dtype=torch.uint8,
                          device=dev)
-        _call("muon_mx_matmul", dev, ca, cb, co, n, opt, ws.data_ptr(), ws.numel())
+        _lib.check(_call("muon_mx_matmul", dev, ca, cb, co, n, opt, ws.data_ptr(), ws.numel()),
+                   "muon_mx_matmul")
     if out is not None:
         return out
     return outs[0] if single else outs

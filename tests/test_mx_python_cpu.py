@@ -32,3 +32,26 @@ def test_a_repeated_quantisation_keeps_the_memory_it_writes(monkeypatch):
     del again
     gc.collect()
     assert all(m() is None for m in memory)
+
+
+def test_a_refused_workspace_is_an_error(monkeypatch):
+    """A product whose second call, with a workspace, is refused too has no
+    result to return."""
+    seen = []
+
+    def refused(*args):
+        seen.append(args[-2])       # workspace bytes
+        return _lib.CODES["MUON_E_WORKSPACE"]
+
+    class Library:
+        @staticmethod
+        def muon_mx_matmul_workspace_bytes(*args):
+            return 0                # as after a failed allocation on the host
+
+    monkeypatch.setitem(mx._functions, "muon_mx_matmul", refused)
+    monkeypatch.setattr(mx, "_current_device", lambda: None)
+    monkeypatch.setattr(mx, "_current_stream", lambda i: None)
+    monkeypatch.setattr(_lib, "load", lambda: Library)
+    with pytest.raises(_lib.MuonError):
+        mo.mx_matmul(_held(8, 40), _held(5, 40))
+    assert seen == [0, 0]
