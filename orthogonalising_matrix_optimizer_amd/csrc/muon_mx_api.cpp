@@ -148,6 +148,9 @@ int64_t even_chunk(int64_t kt, int64_t chunk) {
   return kt ? ceil_div(kt, ceil_div(kt, chunk)) : 1;
 }
 
+// Blocks that sum the parts of a split M x N product.
+int64_t reduce_blocks(int64_t M, int64_t N) { return ceil_div(M * (round_up(N, 8) / 8), 256); }
+
 // Microseconds a stage (128 columns) of a work item takes with 1, 2, 3 blocks
 // on its CU, measured on MI355X: 256 x 128 tiles (two blocks a CU) and 128 x
 // 128 (three).  Of the two the cheaper is taken, e.g. K = 2560, N = 2560: M =
@@ -188,12 +191,16 @@ ProductPlan plan_products(const muon_mx* a, const muon_mx* b, int n) {
   // 81 | 88 and 512 x 2048 x 4096 19 | 20.
   for (int64_t c = kMinChunk; c < longest; c += c / 2) {
     double items = 0, bytes = 0, part = 0;
+    bool fits = true;   // every product's items and sum in a launch of their own
     for (int i = 0; i < n; ++i) {
       const int64_t kt = ceil_div(a[i].cols, kMxTileK), splits = std::max<int64_t>(1, ceil_div(kt, c));
+      const double own = double(splits) * ceil_div(a[i].rows, 128) * ceil_div(b[i].rows, kTileN);
+      fits = fits && own <= kMaxBlocks && reduce_blocks(a[i].rows, b[i].rows) <= kMaxBlocks;
       part = std::max(part, double(even_chunk(kt, c)));
-      items += double(splits) * ceil_div(a[i].rows, 128) * ceil_div(b[i].rows, kTileN);
+      items += own;
       bytes += 8.0 * splits * a[i].rows * b[i].rows;
     }
+    if (!fits) continue;
     const double t = list_us(kStage128, 3, items, w128, part) + bytes / 8e6 + 5;
     if (t < 0.9 * best) {
       best = t / 0.9;
@@ -446,7 +453,7 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
     if (tiles == 0) continue;
     const int64_t chunk = split ? even_chunk(kt, plan.chunk) : std::max<int64_t>(kt, 1);
     const int64_t splits = std::max<int64_t>(1, ceil_div(kt, chunk));
-    const int64_t nb = split ? ceil_div(M * (round_up(N, 8) / 8), 256) : 0;
+    const int64_t nb = split ? reduce_blocks(M, N) : 0;
     if (g.n == kMxMaxList || items + tiles * splits > kMaxBlocks || blocks + nb > kMaxBlocks)
       if ((rc = int(flush())) != MUON_OK) return rc;
     MxProduct& p = g.m[g.n];
