@@ -473,8 +473,11 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
 
 /* out = x b^T for at most MUON_MX_FEW_ROWS rows of x that are not in 4 bits yet
  * (the layer of single tokens): x is quantised to nearest in the same launch,
- * with the codes of muon_mx_quantize.  out has any element type. */
+ * with the codes of muon_mx_quantize.  out has any element type.  b has at most
+ * MUON_MX_FEW_ROWS_MAX_N rows (MUON_E_SHAPE): 512 threads for every 64 of them
+ * and fewer than 2^32 in a launch. */
 #define MUON_MX_FEW_ROWS 16
+#define MUON_MX_FEW_ROWS_MAX_N 536870848
 int muon_mx_matmul_rows(const muon_mat* x, const muon_mx* b, const muon_mat* out, void* stream);
 
 /* out = in with each element kept with probability 1 - p and multiplied by

@@ -24,6 +24,7 @@ PHASES = {"prepare": 0, "gram": 1, "poly": 2, "apply": 3, "finish": 4, "adamw": 
 MAX_STEPS = 16
 NOALLOC_SCRATCH_BYTES = 64 << 20
 MX_FEW_ROWS = 16
+MX_FEW_ROWS_MAX_N = (1 << 29) - 64
 
 
 class MuonMat(ctypes.Structure):

@@ -508,6 +508,7 @@ int muon_mx_matmul_rows(const muon_mat* x, const muon_mx* b, const muon_mat* out
     return rc;
   if (x->rows > MUON_MX_FEW_ROWS || x->cols != b->cols || out->rows != x->rows || out->cols != b->rows)
     return MUON_E_SHAPE;
+  if (b->rows > MUON_MX_FEW_ROWS_MAX_N) return MUON_E_SHAPE;
   std::vector<Span> spans;
   add_span(spans, *x, false);
   add_span(spans, *b, false);

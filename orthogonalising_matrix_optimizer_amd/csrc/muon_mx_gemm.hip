@@ -600,6 +600,7 @@ void launch_rows_of(const MxRowsArgs& a, hipStream_t s) {
 //   1 x 10240 x 2560: 10.0 | 6.2 | 8.9;  13 rows 14.4 | 10.6 | 13.2
 //   1 x 768 x 768: 2.5 | 2.1 | 2.0;  16 x 768 x 2304: 3.6 | 3.2 | 3.1
 // Many rows of b amortise x; a long contraction with few of them needs the waves.
+// b with at most MUON_MX_FEW_ROWS_MAX_N rows keeps the grid below 2^32 threads.
 template <int XDT, int ODT>
 hipError_t launch_rows(const MxRowsArgs& a, hipStream_t s) {
   if (a.N >= 8192) launch_rows_of<XDT, ODT, 8, 4, 1>(a, s);

@@ -413,7 +413,7 @@ def mx_linear(x: torch.Tensor, w: MX4, save: bool = False, dropout: float = 0.0,
     _device_of(w)
     if cols != w.desc[3]:
         raise ValueError(f"x has {cols} features, the layer takes {w.cols}")
-    if not save and not dropout and rows <= _lib.MX_FEW_ROWS:
+    if not save and not dropout and rows <= _lib.MX_FEW_ROWS and w.desc[2] <= _lib.MX_FEW_ROWS_MAX_N:
         dev = _gpu(x.device)
         xm = _MAT1.pack(*_mat(x2, dev))
         y, ym = _new_one(rows, w.desc[2], x.dtype, dev)

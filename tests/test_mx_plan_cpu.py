@@ -40,3 +40,19 @@ def test_split_lists_stay_inside_the_grids(lib):
         assert lib.muon_mx_matmul_workspace_bytes(*_operands([(m, n, 128), long])) == 0
     below = (1 << 17, 1 << 17, 128)
     assert lib.muon_mx_matmul_workspace_bytes(*_operands([below, long])) > 0
+
+
+def test_the_product_of_few_rows_refuses_what_its_grid_cannot_hold(lib):
+    """512 threads for every 64 rows of b, below 2^32 threads a launch."""
+    for rows in ((1 << 29) - 63, 1 << 29, 1 << 30):
+        assert -(-rows // 64) * 512 >= 1 << 32
+        x = _lib.MuonMat(BASE, 1, 96, 96, BF16, 0)
+        b = _lib.MuonMX(BASE + (1 << 20), BASE + (1 << 40), rows, 96)
+        out = _lib.MuonMat(BASE + (1 << 42), 1, rows, rows, BF16, 0)
+        assert lib.muon_mx_matmul_rows(_arr([x]), _arr([b]), _arr([out]), None) == E["MUON_E_SHAPE"]
+
+
+def test_limits_match_the_header():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "muon.h")).read()
+    assert f"#define MUON_MX_FEW_ROWS_MAX_N {_lib.MX_FEW_ROWS_MAX_N}\n" in text

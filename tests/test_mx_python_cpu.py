@@ -55,3 +55,18 @@ def test_a_refused_workspace_is_an_error(monkeypatch):
     with pytest.raises(_lib.MuonError):
         mo.mx_matmul(_held(8, 40), _held(5, 40))
     assert seen == [0, 0]
+
+
+@pytest.mark.parametrize("rows,few", [((1 << 29) - 64, True), ((1 << 29) - 63, False)])
+def test_a_layer_past_the_few_rows_grid_takes_the_general_product(monkeypatch, rows, few):
+    w = mx.MX4(torch.empty(0, dtype=torch.uint8), 0, CPU, (0, 0, rows, 32))
+    calls = []
+
+    def record(name, dev, *args):
+        calls.append(name)
+        return 0
+    monkeypatch.setattr(mx, "_call", record)
+    monkeypatch.setattr(mx, "_gpu", lambda dev: dev)
+    monkeypatch.setattr(mx, "_new_one", lambda r, c, dt, dev: (torch.empty(0), b""))
+    mo.mx_linear(torch.zeros(2, 32), w)
+    assert calls == (["muon_mx_matmul_rows"] if few else ["muon_mx_quantize", "muon_mx_matmul"])
