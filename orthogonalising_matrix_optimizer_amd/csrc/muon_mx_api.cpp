@@ -13,6 +13,7 @@
 #include "../../include/muon.h"
 #include "muon_common.h"
 #include "muon_mx.h"
+#include "muon_span.h"
 
 using namespace muon;
 
@@ -52,14 +53,6 @@ int check_mx(const muon_mx& m) {
   return MUON_OK;
 }
 
-// Memory that a call reads or writes: `width` bytes in every `pitch` from lo
-// on, up to hi.
-struct Span {
-  uintptr_t lo, hi;
-  size_t pitch, width;
-  bool write;
-};
-
 void add_span(std::vector<Span>& v, const void* p, size_t bytes, bool write) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
   if (p && bytes) v.push_back({a, a + bytes, bytes, bytes, write});
@@ -77,36 +70,6 @@ void add_span(std::vector<Span>& v, const muon_mx& m, bool write) {
   if (m.rows == 0 || m.cols == 0) return;
   add_span(v, m.codes, muon_mx_codes_bytes(m.rows, m.cols), write);
   add_span(v, m.scales, muon_mx_scales_bytes(m.rows, m.cols), write);
-}
-
-// Whether two spans share a byte; column slices of one buffer do not.
-bool share(const Span& a, const Span& b) {
-  if (b.lo >= a.hi || a.lo >= b.hi) return false;
-  if (a.pitch != b.pitch) return true;
-  const size_t d = (a.lo < b.lo ? b.lo - a.lo : a.lo - b.lo) % a.pitch;
-  const size_t first = a.lo < b.lo ? a.width : b.width, second = a.lo < b.lo ? b.width : a.width;
-  return d < first || d + second > a.pitch;
-}
-
-// Whether something written is also read or written through another argument.
-bool conflict(std::vector<Span>& v) {
-  std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
-  // the spans still open at the next one's start: only they can share bytes with it
-  std::vector<Span> open;
-  for (const Span& s : v) {
-    size_t kept = 0;
-    for (const Span& o : open)
-      if (o.hi > s.lo) {
-        if ((o.write || s.write) && share(o, s)) return true;
-        open[kept++] = o;
-      }
-    open.resize(kept);
-    // equal spans that are only read count once
-    if (!(kept && !s.write && open[kept - 1].lo == s.lo && open[kept - 1].hi == s.hi &&
-          !open[kept - 1].write))
-      open.push_back(s);
-  }
-  return false;
 }
 
 // Dropout probability -> threshold in steps of 2^-16 and the kept elements' factor.
