@@ -57,9 +57,10 @@ inline bool conflict(std::vector<Span>& v) {
       }
     open.resize(kept);
     // equal spans that are only read count once
-    if (!(kept && !s.write && open[kept - 1].lo == s.lo && open[kept - 1].hi == s.hi &&
-          !open[kept - 1].write))
-      open.push_back(s);
+    auto same = [&](const Span& o) {
+      return o.lo == s.lo && o.hi == s.hi && o.pitch == s.pitch && o.width == s.width;
+    };
+    if (!(kept && !s.write && same(open[kept - 1]) && !open[kept - 1].write)) open.push_back(s);
   }
   return false;
 }

@@ -28,27 +28,55 @@ int main() {
 }
 """
 
+# three spans a line -> conflict
+PROGRAM3 = r"""
+#include <stdio.h>
+#include "muon_span.h"
+using namespace muon;
+int main() {
+  long s[5];
+  std::vector<Span> v;
+  while (scanf("%ld %ld %ld %ld %ld", s, s + 1, s + 2, s + 3, s + 4) == 5) {
+    v.push_back({uintptr_t(s[0]), uintptr_t(s[0] + (s[1] - 1) * s[2] + s[3]), size_t(s[2]), size_t(s[3]), s[4] != 0});
+    if (v.size() == 3) {
+      printf("%d\n", conflict(v));
+      v.clear();
+    }
+  }
+  return 0;
+}
+"""
+
 
 def _bytes(s):
     start, rows, pitch, width, _ = s
     return {start + i * pitch + j for i in range(rows) for j in range(width)}
 
 
-@pytest.fixture(scope="module")
-def answers(tmp_path_factory):
+def _program(d, source):
     if shutil.which("g++") is None:
         pytest.skip("needs g++")
-    d = tmp_path_factory.mktemp("span")
-    (d / "span.cpp").write_text(PROGRAM)
+    (d / "span.cpp").write_text(source)
     subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", CSRC, str(d / "span.cpp"), "-o", str(d / "span")], check=True)
 
-    def ask(pairs):
-        text = "\n".join(" ".join(map(str, (*a, *b))) for a, b in pairs)
+    def ask(groups):
+        text = "\n".join(" ".join(str(v) for span in g for v in span) for g in groups)
         out = subprocess.run([str(d / "span")], input=text, capture_output=True, text=True, check=True).stdout
         got = [tuple(map(int, line.split())) for line in out.splitlines()]
-        assert len(got) == len(pairs)
+        assert len(got) == len(groups)
         return got
     return ask
+
+
+@pytest.fixture(scope="module")
+def answers(tmp_path_factory):
+    return _program(tmp_path_factory.mktemp("span"), PROGRAM)
+
+
+@pytest.fixture(scope="module")
+def answers3(tmp_path_factory):
+    ask = _program(tmp_path_factory.mktemp("span3"), PROGRAM3)
+    return lambda groups: [c for c, in ask(groups)]
 
 
 def _check(pairs, got, exact):
@@ -103,3 +131,10 @@ def test_no_shared_byte_is_missed(answers):
                 for p in (rng.randint(1, 14), rng.randint(1, 14)))
         pairs.append((a, b))
     _check(pairs, answers(pairs), exact=False)
+
+
+def test_two_operands_that_begin_and_end_alike(answers3):
+    """Of two inputs with the same first and last byte one may have gaps that
+    the other has not: an output in such a gap overlaps the other."""
+    strided, whole, gap = (1000, 3, 100, 50, 0), (1000, 1, 250, 250, 0), (1060, 1, 10, 10, 1)
+    assert answers3([(strided, whole, gap), (whole, strided, gap), (strided, strided, gap)]) == [1, 1, 0]
