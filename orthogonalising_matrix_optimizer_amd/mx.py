@@ -11,6 +11,7 @@ packed as bytes: on a single token a call's cost is the host's.
 from __future__ import annotations
 
 from functools import lru_cache
+from math import prod
 from struct import Struct
 from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
@@ -152,7 +153,7 @@ def _rows_of(t: torch.Tensor) -> torch.Tensor:
         raise ValueError("tensors must have at least one dimension")
     c = t.shape[-1]
     try:
-        return t.view(t.numel() // c if c else 0, c)
+        return t.view(prod(t.shape[:-1]), c)
     except RuntimeError:
         raise ValueError("the leading dimensions must be one run of evenly spaced rows") from None
 

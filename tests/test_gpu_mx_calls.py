@@ -44,3 +44,28 @@ def test_outputs_that_are_slices_of_one_buffer():
     wide[:, :60] = x
     mo.dropout(wide[4:5, :60], 0.3, 9, out=wide[4:5, 60:])
     assert torch.equal(wide[4:5, 60:], mo.dropout(x[4:5], 0.3, 9)) and torch.equal(wide[:, :60], x)
+
+
+@pytest.mark.parametrize("lead", [(), (6,), (2, 3), (2, 10), (0, 3)])
+def test_layers_without_features(lead):
+    """No inputs give zeros, no outputs give no gradient; leading dimensions stay."""
+    announce(f"layers without features {lead}")
+    n = int(np.prod(lead, dtype=np.int64))
+    none, some = torch.zeros(5, 0, device="cuda", dtype=BF16), torch.zeros(0, 5, device="cuda", dtype=BF16)
+    x = torch.zeros(*lead, 0, device="cuda", dtype=BF16)
+    pair = mo.mx_quantize(none, "both")
+    y = mo.mx_linear(x, pair.w)
+    assert tuple(y.shape) == (*lead, 5) and not y.any()
+    y, saved = mo.mx_linear(x, pair.w, save=True)
+    assert tuple(y.shape) == (*lead, 5) and not y.any()
+    dx, dw = mo.mx_linear_grad(torch.ones_like(y), pair.w_t, saved)
+    assert tuple(dx.shape) == (*lead, 0) and tuple(dw.shape) == (5, 0)
+    assert tuple(mo.dropout(x, 0.5, 3).shape) == (*lead, 0)
+    # and a layer without outputs
+    x = torch.ones(*lead, 5, device="cuda", dtype=BF16)
+    pair = mo.mx_quantize(some, "both")
+    y, saved = mo.mx_linear(x, pair.w, save=True)
+    assert tuple(y.shape) == (*lead, 0)
+    dx, dw = mo.mx_linear_grad(y, pair.w_t, saved)
+    assert tuple(dx.shape) == (*lead, 5) and not dx.any() and tuple(dw.shape) == (0, 5)
+    assert saved.x_t.cols == (n if lead else 1)

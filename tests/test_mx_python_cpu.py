@@ -70,3 +70,9 @@ def test_a_layer_past_the_few_rows_grid_takes_the_general_product(monkeypatch, r
     monkeypatch.setattr(mx, "_new_one", lambda r, c, dt, dev: (torch.empty(0), b""))
     mo.mx_linear(torch.zeros(2, 32), w)
     assert calls == (["muon_mx_matmul_rows"] if few else ["muon_mx_quantize", "muon_mx_matmul"])
+
+
+@pytest.mark.parametrize("shape,rows", [((2, 3, 0), 6), ((0, 3, 4), 0), ((2, 0, 0), 0), ((0,), 1), ((7,), 1),
+                                        ((2, 3, 4), 6)])
+def test_rows_of_tensors_without_features(shape, rows):
+    assert tuple(mx._rows_of(torch.zeros(shape)).shape) == (rows, shape[-1])
