@@ -436,7 +436,10 @@ def mx_linear_grad(dy: torch.Tensor, w_t: Optional[MX4], saved: MXSaved, seed: O
     and W^T in 4 bits (None: no dx).  dy is quantised once for both products,
     stochastically with a `seed`.  dw = dy^T x goes to a new tensor of
     grad_dtype or to `out` (added to it with `accumulate`); with `pair` its
-    two 4-bit factors are returned instead, for Muon.step to multiply."""
+    two 4-bit factors are returned instead, for Muon.step to multiply (then
+    without out, accumulate and grad_dtype)."""
+    if pair and (out is not None or accumulate or grad_dtype is not torch.float32):
+        raise ValueError("pair=True returns factors: out, accumulate and grad_dtype have no use")
     dy2 = _rows_of(dy)
     if dy2.shape[0] != saved.x_t.cols:
         raise ValueError(f"dy has {dy2.shape[0]} rows, the layer saw {saved.x_t.cols}")

@@ -76,3 +76,12 @@ def test_a_layer_past_the_few_rows_grid_takes_the_general_product(monkeypatch, r
                                         ((2, 3, 4), 6)])
 def test_rows_of_tensors_without_features(shape, rows):
     assert tuple(mx._rows_of(torch.zeros(shape)).shape) == (rows, shape[-1])
+
+
+@pytest.mark.parametrize("kw", [dict(out=torch.zeros(4, 40)), dict(accumulate=True), dict(grad_dtype=torch.bfloat16),
+                                dict(out=torch.zeros(4, 40), accumulate=True)])
+def test_factors_are_not_accumulated(kw):
+    """With pair=True nothing is multiplied, so there is nothing to write or add."""
+    saved = mx.MXSaved(_held(40, 8), 0.0, None)
+    with pytest.raises(ValueError, match="pair"):
+        mo.mx_linear_grad(torch.zeros(8, 4), None, saved, pair=True, **kw)
