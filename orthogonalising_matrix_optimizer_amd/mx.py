@@ -77,7 +77,8 @@ class MXPair(NamedTuple):
 
 class MXSaved(NamedTuple):
     """What mx_linear keeps for mx_linear_grad: the input's transpose in 4 bits
-    (after dropout) and how to make the dropout mask again."""
+    (after dropout) and how to make the dropout mask again (of a seed tensor
+    the value that the forward pass used)."""
     x_t: MX4
     dropout: float
     dropout_seed: Optional[Seed]
@@ -421,6 +422,9 @@ def mx_linear(x: torch.Tensor, w: MX4, save: bool = False, dropout: float = 0.0,
         _call("muon_mx_matmul_rows", dev, xm, _mxs([w], dev), ym)
         saved = None
     else:
+        if save and dropout and isinstance(dropout_seed, torch.Tensor):
+            # the backward pass needs this pass's value (a kernel also under capture)
+            dropout_seed = dropout_seed + 0
         q = mx_quantize(x2, "both" if save else False, dropout=dropout, dropout_seed=dropout_seed)
         y = mx_matmul(q[0] if save else q, w, dtype=x.dtype)
         saved = MXSaved(q[1], float(dropout), dropout_seed) if save else None

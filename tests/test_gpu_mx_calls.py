@@ -69,3 +69,37 @@ def test_layers_without_features(lead):
     dx, dw = mo.mx_linear_grad(y, pair.w_t, saved)
     assert tuple(dx.shape) == (*lead, 5) and not dx.any() and tuple(dw.shape) == (0, 5)
     assert saved.x_t.cols == (n if lead else 1)
+
+
+@pytest.mark.parametrize("shape", [(), (1,)])
+def test_a_seed_advanced_between_forward_and_backward(shape):
+    """The gradient has the forward pass's mask, eagerly and in a replayed graph."""
+    announce(f"advanced seed {shape}")
+    w, x, dy = _rand(40, 64, BF16, 1), _rand(33, 64, BF16, 2), _rand(33, 40, BF16, 3)
+    pair = mo.mx_quantize(w, "both")
+
+    def step(seed, advance=False):
+        y, saved = mo.mx_linear(x, pair.w, save=True, dropout=0.4, dropout_seed=seed)
+        if advance:
+            seed += 1
+        return (y, *mo.mx_linear_grad(dy, pair.w_t, saved, seed=11))
+    seed = torch.full(shape, 5, dtype=torch.int64, device="cuda")
+    assert all(torch.equal(a, b) for a, b in zip(step(seed, True), step(5)))
+    assert int(seed) == 6
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(seed, True)
+    for t in (6, 7, 8, -3):
+        if t < 0:
+            seed.fill_(t)
+        g.replay()
+        got = [o.clone() for o in out]
+        (torch.randn(512, 512, device="cuda") @ torch.randn(512, 512, device="cuda")).sum()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, step(t))), t
+        assert int(seed) == t + 1
+    for bad in (torch.zeros(1, dtype=torch.int64), torch.zeros(1, device="cuda"),
+                torch.zeros(2, dtype=torch.int64, device="cuda")):
+        with pytest.raises(ValueError):
+            step(bad)

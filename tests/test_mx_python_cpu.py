@@ -85,3 +85,22 @@ def test_factors_are_not_accumulated(kw):
     saved = mx.MXSaved(_held(40, 8), 0.0, None)
     with pytest.raises(ValueError, match="pair"):
         mo.mx_linear_grad(torch.zeros(8, 4), None, saved, pair=True, **kw)
+
+
+def test_the_forward_pass_keeps_the_seed_that_it_used(monkeypatch):
+    """A program may advance its seed tensor between a layer's forward and
+    backward pass: the gradient needs the mask of the forward pass."""
+    used = []
+
+    def quantize(x, transpose, dropout, dropout_seed):
+        used.append(dropout_seed)
+        return mx.MXPair(_held(8, 40), _held(40, 8))
+    monkeypatch.setattr(mx, "mx_quantize", quantize)
+    monkeypatch.setattr(mx, "mx_matmul", lambda a, b, dtype: torch.zeros(8, 4))
+    seed = torch.tensor([5])
+    _, saved = mo.mx_linear(torch.zeros(8, 40), _held(4, 40), save=True, dropout=0.5, dropout_seed=seed)
+    seed += 1
+    assert int(saved.dropout_seed) == 5 and used[0] is saved.dropout_seed
+    for given in (7, None):
+        _, saved = mo.mx_linear(torch.zeros(8, 40), _held(4, 40), save=True, dropout=0.0, dropout_seed=given)
+        assert saved.dropout_seed is given
