@@ -7,6 +7,12 @@ numbers are stated in include/muon.h.  As in the rest of the package all
 computation runs in the HIP library; this module allocates outputs and passes
 pointers with the current stream of the tensors' device.  Descriptors are
 packed as bytes: on a single token a call's cost is the host's.
+
+Nothing here is recorded by autograd.  The gradients are calls of their own
+(mx_linear_grad, dropout on the gradient), made by hand or by the two halves of
+a torch.autograd.Function; mx_linear, mx_linear_grad and dropout refuse a tensor
+that requires a gradient where autograd records.  mx_quantize takes weights
+that require one.
 """
 from __future__ import annotations
 
@@ -157,6 +163,13 @@ def _rows_of(t: torch.Tensor) -> torch.Tensor:
         return t.view(prod(t.shape[:-1]), c)
     except RuntimeError:
         raise ValueError("the leading dimensions must be one run of evenly spaced rows") from None
+
+
+def _not_recorded(t: torch.Tensor) -> None:
+    """Refuses a tensor whose gradient autograd would look for in the result."""
+    if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("the 4-bit operators and dropout record nothing for autograd: call them under "
+                         "torch.no_grad() or in an autograd.Function, or give t.detach()")
 
 
 def _mat(t: torch.Tensor, dev: torch.device):
@@ -410,6 +423,7 @@ def mx_linear(x: torch.Tensor, w: MX4, save: bool = False, dropout: float = 0.0,
     result [..., out] has x's type.  With `dropout` the layer's input is
     dropout(x, dropout, dropout_seed).  With `save` returns (y, saved), saved
     being what mx_linear_grad needs: the input's transpose in 4 bits."""
+    _not_recorded(x)
     x2 = _rows_of(x)
     rows, cols = x2.shape
     _device_of(w)
@@ -444,6 +458,7 @@ def mx_linear_grad(dy: torch.Tensor, w_t: Optional[MX4], saved: MXSaved, seed: O
     without out, accumulate and grad_dtype)."""
     if pair and (out is not None or accumulate or grad_dtype is not torch.float32):
         raise ValueError("pair=True returns factors: out, accumulate and grad_dtype have no use")
+    _not_recorded(dy)
     dy2 = _rows_of(dy)
     if dy2.shape[0] != saved.x_t.cols:
         raise ValueError(f"dy has {dy2.shape[0]} rows, the layer saw {saved.x_t.cols}")
@@ -466,6 +481,7 @@ def dropout(x: torch.Tensor, p: float, seed: Seed, out: Optional[torch.Tensor] =
     """x with each element kept with probability 1 - p and scaled by
     1 / (1 - p), or zeroed; the same call on a gradient is the backward pass.
     `out` may be x itself."""
+    _not_recorded(x)
     x2 = _rows_of(x)
     dev = _gpu(x.device)
     xm = _MAT1.pack(*_mat(x2, dev))

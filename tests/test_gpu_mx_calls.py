@@ -103,3 +103,34 @@ def test_a_seed_advanced_between_forward_and_backward(shape):
                 torch.zeros(2, dtype=torch.int64, device="cuda")):
         with pytest.raises(ValueError):
             step(bad)
+
+
+def test_layers_in_an_autograd_function():
+    """The two passes as the halves of an autograd.Function, beside torch's own operations."""
+    announce("autograd.Function")
+    w = _rand(40, 64, BF16, 1)
+    pair = mo.mx_quantize(w, "both")
+
+    class Layer(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight):
+            y, ctx.saved = mo.mx_linear(x, pair.w, save=True, dropout=0.2, dropout_seed=4)
+            return y
+
+        @staticmethod
+        def backward(ctx, dy):
+            return mo.mx_linear_grad(dy.contiguous(), pair.w_t, ctx.saved, seed=5)
+    x = _rand(33, 64, F32, 2).requires_grad_()
+    weight = w.float().requires_grad_()
+    y = Layer.apply(x, weight)
+    (y * y).sum().backward()
+    with torch.no_grad():
+        want, saved = mo.mx_linear(x, pair.w, save=True, dropout=0.2, dropout_seed=4)
+        dx, dw = mo.mx_linear_grad(2 * want, pair.w_t, saved, seed=5)
+    assert torch.equal(y, want) and torch.equal(x.grad, dx) and torch.equal(weight.grad, dw)
+    for f in (lambda: mo.mx_linear(x, pair.w), lambda: mo.dropout(x, 0.1, 1),
+              lambda: mo.mx_linear_grad(y, None, saved)):
+        with pytest.raises(ValueError, match="autograd"):
+            f()
+    assert mo.mx_quantize(weight).shape == (40, 64)
+    assert len(mo.Muon([torch.nn.Parameter(w.clone())], mx=True).mx) == 1

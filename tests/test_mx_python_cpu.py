@@ -104,3 +104,23 @@ def test_the_forward_pass_keeps_the_seed_that_it_used(monkeypatch):
     for given in (7, None):
         _, saved = mo.mx_linear(torch.zeros(8, 40), _held(4, 40), save=True, dropout=0.0, dropout_seed=given)
         assert saved.dropout_seed is given
+
+
+def test_a_result_that_autograd_would_lose_is_refused(monkeypatch):
+    """The operators record no graph: a tensor that requires a gradient is taken
+    only where autograd does not record."""
+    x = torch.zeros(2, 40, requires_grad=True)
+    w, saved = _held(4, 40), mx.MXSaved(_held(40, 8), 0.0, None)
+    dy = torch.zeros(8, 4, requires_grad=True)
+    calls = (lambda: mo.mx_linear(x, w), lambda: mo.mx_linear(x, w, save=True), lambda: mo.dropout(x, 0.5, 1),
+             lambda: mo.mx_linear_grad(dy, None, saved), lambda: mo.dropout(x[0], 0.5, 1))
+    for f in calls:
+        with pytest.raises(ValueError, match="autograd"):
+            f()
+    # where nothing is recorded the next refusal is that of host memory, and
+    # weights are quantised whether they require gradients or not
+    for f in calls:
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+            f()
+    with pytest.raises(ValueError, match="GPU"):
+        mo.mx_quantize(x)
