@@ -172,6 +172,11 @@ def _not_recorded(t: torch.Tensor) -> None:
                          "torch.no_grad() or in an autograd.Function, or give t.detach()")
 
 
+def _written(ts) -> None:
+    """Tells autograd that the library wrote tensors, as torch's own in-place operations do."""
+    torch.autograd.graph.increment_version([t for t in ts if not t.is_inference()])
+
+
 def _mat(t: torch.Tensor, dev: torch.device):
     """muon_mat of a 2-D tensor whose rows are contiguous."""
     d = _DT.get(t.dtype)
@@ -375,6 +380,7 @@ def mx_dequantize(m: Union[MX4, Sequence[MX4]], dtype: torch.dtype = torch.bfloa
         mats = _mats(outs, dev)
     _call("muon_mx_dequantize", dev, mxs, mats, len(ms))
     if out is not None:
+        _written(outs)
         return out
     return outs[0] if single else outs
 
@@ -413,6 +419,7 @@ def mx_matmul(a: Union[MX4, Sequence[MX4]], b: Union[MX4, Sequence[MX4]],
         _lib.check(_call("muon_mx_matmul", dev, ca, cb, co, n, opt, ws.data_ptr(), ws.numel()),
                    "muon_mx_matmul")
     if out is not None:
+        _written(outs)
         return out
     return outs[0] if single else outs
 
@@ -499,4 +506,6 @@ def dropout(x: torch.Tensor, p: float, seed: Seed, out: Optional[torch.Tensor] =
         _call("muon_dropout", dev, xm, om, p, 0, opt.seed_dev)
     else:
         _call("muon_dropout", dev, xm, om, p, int(seed) & 0xFFFFFFFFFFFFFFFF, None)
+    if out is not None:
+        _written((out,))
     return res

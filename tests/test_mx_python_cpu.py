@@ -124,3 +124,34 @@ def test_a_result_that_autograd_would_lose_is_refused(monkeypatch):
             f()
     with pytest.raises(ValueError, match="GPU"):
         mo.mx_quantize(x)
+
+
+def test_results_written_into_given_tensors_count_as_changes(monkeypatch):
+    """autograd refuses to use a saved tensor that was overwritten: it learns of
+    that by the tensor's version."""
+    monkeypatch.setattr(mx, "_call", lambda *a: 0)
+    monkeypatch.setattr(mx, "_gpu", lambda dev: dev)
+    big, q, w = torch.zeros(9, 60), _held(8, 40), _held(5, 40)
+    saved = mx.MXSaved(_held(40, 8), 0.0, None)
+    views = [big[:8, :5], big[:8, 10:15]]
+    for write, t in ((lambda: mo.mx_matmul(q, w, out=big[:8, :5]), big),
+                     (lambda: mo.mx_matmul([q, q], [w, w], out=views, accumulate=True), big),
+                     (lambda: mo.mx_dequantize(q, out=big[:8, :40]), big),
+                     (lambda: mo.mx_dequantize([q, q], out=[big[:8, :40], torch.zeros(8, 40)]), big),
+                     (lambda: mo.dropout(big, 0.5, 1, out=big), big),
+                     (lambda: mo.mx_linear_grad(torch.zeros(8, 5), None, saved, out=big[:5, :40]), big)):
+        before = t._version
+        write()
+        assert t._version > before
+    # the error that this gives
+    p = torch.ones(8, 40, requires_grad=True)
+    kept = p.detach().clone()
+    loss = (p * kept).sum()
+    mo.dropout(kept, 0.5, 1, out=kept)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    # tensors of inference mode have no version
+    with torch.inference_mode():
+        t = torch.zeros(8, 5)
+        mo.mx_matmul(q, w, out=t)
+    mo.mx_matmul([q, q], [w, w], out=[t, big[:8, :5]])
