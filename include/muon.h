@@ -471,6 +471,18 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
                    const muon_mx_options* opt, void* workspace, size_t workspace_bytes,
                    void* stream);
 
+/* How muon_mx_matmul would run a list, without running it (host only; the
+ * operands' and outputs' memory may be NULL): the height of its output tiles
+ * (256 or 128 rows, by 128 columns), the parts of each product's contraction
+ * (n entries; 0 for an empty output), and of its first launch whether the
+ * outputs go past the caches and the XCDs' ranges of work items (nine entries:
+ * XCD x has the items from xcd_items[x] to xcd_items[x + 1] - 1; a product's
+ * items are the tiles of its first part, then of the next).  Each result may be
+ * NULL. */
+int muon_mx_plan_info(const muon_mx* a, const muon_mx* b, const muon_mat* out, int32_t n,
+                      int32_t* tile_rows, int32_t* parts, int32_t* past_caches,
+                      int32_t* xcd_items);
+
 /* out = x b^T for at most MUON_MX_FEW_ROWS rows of x that are not in 4 bits yet
  * (the layer of single tokens): x is quantised to nearest in the same launch,
  * with the codes of muon_mx_quantize.  out has any element type.  b has at most

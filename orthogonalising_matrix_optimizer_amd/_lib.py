@@ -147,6 +147,8 @@ def load() -> ctypes.CDLL:
     lib.muon_mx_matmul_workspace_bytes.restype = c_size_t
     lib.muon_mx_matmul.argtypes = [V, V, V, c_int32, P(MXOptions), V, c_size_t, V]
     lib.muon_mx_matmul.restype = c_int32
+    lib.muon_mx_plan_info.argtypes = [V, V, V, c_int32, P(c_int32), P(c_int32), P(c_int32), P(c_int32)]
+    lib.muon_mx_plan_info.restype = c_int32
     lib.muon_mx_matmul_rows.argtypes = [V, V, V, V]
     lib.muon_mx_matmul_rows.restype = c_int32
     lib.muon_dropout.argtypes = [V, V, c_float, c_uint64, V, V]

@@ -206,6 +206,90 @@ void share_out(MxGemmArgs& g, int64_t items, double stages) {
   while (x < 8) g.c.xcd[++x] = int32_t(items);
 }
 
+// Shapes and types of one product of a list.
+int check_product(const muon_mx& a, const muon_mx& b, const muon_mat& out, const muon_mat& first) {
+  if (out.dtype != first.dtype) return MUON_E_DTYPE;
+  if (a.cols != b.cols || out.rows != a.rows || out.cols != b.rows) return MUON_E_SHAPE;
+  if (ceil_div(a.rows, 128) * ceil_div(b.rows, kTileN) > kMaxBlocks) return MUON_E_SHAPE;
+  return MUON_OK;
+}
+
+// Arguments of a launch of products and of the launch that sums their parts.
+struct ProductLaunch {
+  MxGemmArgs g;
+  MxReduceArgs red;
+  int64_t items, blocks, written;   // work items, blocks of the sum, bytes of output
+  double stages;
+  ProductLaunch() { std::memset(this, 0, sizeof(*this)); }
+};
+
+// Fills l with the list's products and calls run() for each launch.  With a
+// split contraction every product of the list writes fp32 partials, so that one
+// launch holds them all.
+template <class Run>
+int build_launches(const muon_mx* a, const muon_mx* b, const muon_mat* out, int32_t n,
+                   const ProductPlan& plan, char* workspace, ProductLaunch& l, Run run) {
+  const bool split = plan.chunk != 0;
+  int rc;
+  auto flush = [&]() {
+    if (l.g.n == 0) return int(MUON_OK);
+    share_out(l.g, l.items, l.stages);
+    const int code = run();
+    l.g.n = l.red.n = 0;
+    l.items = l.blocks = l.written = 0;
+    l.stages = 0;
+    return code;
+  };
+  for (int i = 0; i < n; ++i) {
+    const int64_t M = a[i].rows, N = b[i].rows, kt = ceil_div(a[i].cols, kMxTileK);
+    const int64_t tiles = ceil_div(M, plan.tile_m) * ceil_div(N, kTileN);
+    if (tiles == 0) continue;
+    const int64_t chunk = split ? even_chunk(kt, plan.chunk) : std::max<int64_t>(kt, 1);
+    const int64_t splits = std::max<int64_t>(1, ceil_div(kt, chunk));
+    const int64_t nb = split ? reduce_blocks(M, N) : 0;
+    if (l.g.n == kMxMaxList || l.items + tiles * splits > kMaxBlocks || l.blocks + nb > kMaxBlocks)
+      if ((rc = flush()) != MUON_OK) return rc;
+    MxProduct& p = l.g.m[l.g.n];
+    p.ac = static_cast<const uint8_t*>(a[i].codes);
+    p.as = static_cast<const uint8_t*>(a[i].scales);
+    p.bc = static_cast<const uint8_t*>(b[i].codes);
+    p.bs = static_cast<const uint8_t*>(b[i].scales);
+    p.out = out[i].ptr;
+    p.ld = out[i].ld;
+    p.stride = 0;
+    p.M = int32_t(M);
+    p.N = int32_t(N);
+    p.kt = int32_t(kt);
+    p.chunk = int32_t(chunk);
+    p.tiles = int32_t(tiles);
+    p.index = i;
+    if (split) {
+      MxReduce& r = l.red.m[l.g.n];
+      std::memset(&r, 0, sizeof(r));
+      r.ldp = int32_t(round_up(N, 8));
+      r.stride = M * r.ldp;
+      r.in = workspace ? reinterpret_cast<const float*>(workspace + plan.offset[i]) : nullptr;
+      r.out = out[i].ptr;
+      r.ld = out[i].ld;
+      r.M = p.M;
+      r.N = p.N;
+      r.splits = int32_t(splits);
+      r.index = i;
+      l.red.base[l.g.n] = uint32_t(l.blocks);
+      l.red.n = l.g.n + 1;
+      p.out = const_cast<float*>(r.in);
+      p.ld = r.ldp;
+      p.stride = r.stride;
+    }
+    l.g.base[l.g.n++] = uint32_t(l.items);
+    l.items += tiles * splits;
+    l.blocks += nb;
+    l.written += M * N * esize(out[i].dtype);
+    l.stages += double(tiles) * kt;
+  }
+  return flush();
+}
+
 }  // namespace
 
 extern "C" {
@@ -362,22 +446,17 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
   muon_mx_options o;
   muon_mx_default_options(&o);
   if (opt) o = *opt;
-  MxGemmArgs g;
-  std::memset(&g, 0, sizeof(g));
-  MxReduceArgs red;
-  std::memset(&red, 0, sizeof(red));
+  MxReduceCommon red_common;
+  std::memset(&red_common, 0, sizeof(red_common));
   int rc;
-  if ((rc = drop_of(o.dropout, o.dropout_seed, o.dropout_seed_dev, &red.c.drop)) != MUON_OK) return rc;
-  red.c.accumulate = o.accumulate != 0;
+  if ((rc = drop_of(o.dropout, o.dropout_seed, o.dropout_seed_dev, &red_common.drop)) != MUON_OK) return rc;
+  red_common.accumulate = o.accumulate != 0;
   std::vector<Span> spans;
   for (int i = 0; i < n; ++i) {
     if ((rc = check_mx(a[i])) != MUON_OK || (rc = check_mx(b[i])) != MUON_OK ||
         (rc = check_dense(out[i])) != MUON_OK)
       return rc;
-    if (out[i].dtype != out[0].dtype) return MUON_E_DTYPE;
-    if (a[i].cols != b[i].cols || out[i].rows != a[i].rows || out[i].cols != b[i].rows)
-      return MUON_E_SHAPE;
-    if (ceil_div(a[i].rows, 128) * ceil_div(b[i].rows, kTileN) > kMaxBlocks) return MUON_E_SHAPE;
+    if ((rc = check_product(a[i], b[i], out[i], out[0])) != MUON_OK) return rc;
     add_span(spans, a[i], false);
     add_span(spans, b[i], false);
     add_span(spans, out[i], true);
@@ -388,76 +467,53 @@ int muon_mx_matmul(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
     if (reinterpret_cast<uintptr_t>(workspace) % 16) return MUON_E_ALIGN;
     add_span(spans, workspace, plan.bytes, true);
   }
-  add_span(spans, red.c.drop.seed.dev, sizeof(uint64_t), false);
+  add_span(spans, red_common.drop.seed.dev, sizeof(uint64_t), false);
   if (conflict(spans)) return MUON_E_ALIAS;
   hipStream_t s = static_cast<hipStream_t>(stream);
 
-  // with a split contraction every product of the list writes fp32 partials, so
-  // that one launch holds them all
-  const bool split = plan.chunk != 0;
-  int64_t items = 0, blocks = 0, written = 0;
-  double stages = 0;
-  g.c.accumulate = split ? 0 : red.c.accumulate;
-  if (!split) g.c.drop = red.c.drop;
-  auto flush = [&]() {
-    share_out(g, items, stages);
-    if (g.n && launch_mx_gemm(g, split ? int(kF32) : out[0].dtype, plan.tile_m,
-                              split || !past_caches(written), s) != hipSuccess)
+  ProductLaunch l;
+  l.red.c = red_common;
+  l.g.c.accumulate = plan.chunk ? 0 : red_common.accumulate;
+  if (!plan.chunk) l.g.c.drop = red_common.drop;
+  return build_launches(a, b, out, n, plan, static_cast<char*>(workspace), l, [&]() {
+    if (launch_mx_gemm(l.g, plan.chunk ? int(kF32) : out[0].dtype, plan.tile_m,
+                       plan.chunk || !past_caches(l.written), s) != hipSuccess)
       return MUON_E_HIP;
-    if (red.n && launch_mx_reduce(red, out[0].dtype, blocks, s) != hipSuccess) return MUON_E_HIP;
-    g.n = red.n = 0;
-    items = blocks = written = 0;
-    stages = 0;
+    if (l.red.n && launch_mx_reduce(l.red, out[0].dtype, l.blocks, s) != hipSuccess)
+      return MUON_E_HIP;
     return MUON_OK;
-  };
+  });
+} catch (...) {   // an allocation of the host's failed
+  return MUON_E_HIP;
+}
+
+int muon_mx_plan_info(const muon_mx* a, const muon_mx* b, const muon_mat* out, int32_t n,
+                      int32_t* tile_rows, int32_t* parts, int32_t* past, int32_t* xcd_items) try {
+  if (n <= 0) return MUON_E_SHAPE;
+  if (!a || !b || !out) return MUON_E_NULL;
+  int rc;
   for (int i = 0; i < n; ++i) {
-    const int64_t M = a[i].rows, N = b[i].rows, kt = ceil_div(a[i].cols, kMxTileK);
-    const int64_t tiles = ceil_div(M, plan.tile_m) * ceil_div(N, kTileN);
-    if (tiles == 0) continue;
-    const int64_t chunk = split ? even_chunk(kt, plan.chunk) : std::max<int64_t>(kt, 1);
-    const int64_t splits = std::max<int64_t>(1, ceil_div(kt, chunk));
-    const int64_t nb = split ? reduce_blocks(M, N) : 0;
-    if (g.n == kMxMaxList || items + tiles * splits > kMaxBlocks || blocks + nb > kMaxBlocks)
-      if ((rc = int(flush())) != MUON_OK) return rc;
-    MxProduct& p = g.m[g.n];
-    p.ac = static_cast<const uint8_t*>(a[i].codes);
-    p.as = static_cast<const uint8_t*>(a[i].scales);
-    p.bc = static_cast<const uint8_t*>(b[i].codes);
-    p.bs = static_cast<const uint8_t*>(b[i].scales);
-    p.out = out[i].ptr;
-    p.ld = out[i].ld;
-    p.stride = 0;
-    p.M = int32_t(M);
-    p.N = int32_t(N);
-    p.kt = int32_t(kt);
-    p.chunk = int32_t(chunk);
-    p.tiles = int32_t(tiles);
-    p.index = i;
-    if (split) {
-      MxReduce& r = red.m[g.n];
-      std::memset(&r, 0, sizeof(r));
-      r.ldp = int32_t(round_up(N, 8));
-      r.stride = M * r.ldp;
-      r.in = reinterpret_cast<const float*>(static_cast<char*>(workspace) + plan.offset[i]);
-      r.out = out[i].ptr;
-      r.ld = out[i].ld;
-      r.M = p.M;
-      r.N = p.N;
-      r.splits = int32_t(splits);
-      r.index = i;
-      red.base[g.n] = uint32_t(blocks);
-      red.n = g.n + 1;
-      p.out = const_cast<float*>(r.in);
-      p.ld = r.ldp;
-      p.stride = r.stride;
-    }
-    g.base[g.n++] = uint32_t(items);
-    items += tiles * splits;
-    blocks += nb;
-    written += M * N * esize(out[i].dtype);
-    stages += double(tiles) * kt;
+    if (out[i].dtype != MUON_BF16 && out[i].dtype != MUON_F32) return MUON_E_DTYPE;
+    if (!shape_ok(a[i].rows, a[i].cols) || !shape_ok(b[i].rows, b[i].cols)) return MUON_E_SHAPE;
+    if ((rc = check_product(a[i], b[i], out[i], out[0])) != MUON_OK) return rc;
   }
-  return flush();
+  const ProductPlan plan = plan_products(a, b, n);
+  if (tile_rows) *tile_rows = plan.tile_m;
+  if (past) *past = 0;
+  if (xcd_items) std::fill(xcd_items, xcd_items + 9, 0);
+  if (parts) std::fill(parts, parts + n, 0);
+  ProductLaunch l;
+  bool first = true;
+  return build_launches(a, b, out, n, plan, nullptr, l, [&]() {
+    for (int j = 0; j < l.g.n && parts; ++j)
+      parts[l.g.m[j].index] = std::max(1, int(ceil_div(l.g.m[j].kt, l.g.m[j].chunk)));
+    if (first) {
+      if (past) *past = !plan.chunk && past_caches(l.written);
+      if (xcd_items) std::copy(l.g.c.xcd, l.g.c.xcd + 9, xcd_items);
+    }
+    first = false;
+    return MUON_OK;
+  });
 } catch (...) {   // an allocation of the host's failed
   return MUON_E_HIP;
 }

@@ -16,6 +16,7 @@ that require one.
 """
 from __future__ import annotations
 
+from ctypes import byref, c_int32
 from functools import lru_cache
 from math import prod
 from struct import Struct
@@ -422,6 +423,22 @@ def mx_matmul(a: Union[MX4, Sequence[MX4]], b: Union[MX4, Sequence[MX4]],
         _written(outs)
         return out
     return outs[0] if single else outs
+
+
+def mx_plan_info(shapes: Sequence[Tuple[int, int, int]], dtype: torch.dtype = torch.bfloat16) -> dict:
+    """How mx_matmul runs a list of M x N x K products (muon_mx_plan_info):
+    the output tiles' height, the parts of each contraction, and of the first
+    launch whether the outputs go past the caches and the XCDs' first items."""
+    n = len(shapes)
+    tile, past = c_int32(0), c_int32(0)
+    parts, items = (c_int32 * n)(), (c_int32 * 9)()
+    a, b, out = (_structs(fields, n).pack(*(v for s in shapes for v in f(*s))) for fields, f in (
+        (_MX, lambda m, n, k: (0, 0, m, k)), (_MX, lambda m, n, k: (0, 0, n, k)),
+        (_MAT, lambda m, n, k: (0, m, n, n, _DT[dtype], 0))))
+    _lib.check(_lib.load().muon_mx_plan_info(a, b, out, n, byref(tile), parts, byref(past), items),
+               "muon_mx_plan_info")
+    return {"tile_rows": tile.value, "parts": list(parts), "past_caches": bool(past.value),
+            "xcd_items": list(items)}
 
 
 def mx_linear(x: torch.Tensor, w: MX4, save: bool = False, dropout: float = 0.0,

@@ -3,7 +3,9 @@ their launches."""
 import os
 
 import pytest
+import torch
 
+import orthogonalising_matrix_optimizer_amd as mo
 from orthogonalising_matrix_optimizer_amd import _lib
 
 BASE = 0x7f0000000000   # fake device addresses: validation fails before any use
@@ -56,3 +58,35 @@ def test_limits_match_the_header():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     text = open(os.path.join(root, "include", "muon.h")).read()
     assert f"#define MUON_MX_FEW_ROWS_MAX_N {_lib.MX_FEW_ROWS_MAX_N}\n" in text
+
+
+def test_plan_info(lib):
+    """The tile heights, parts and ranges that the measurements chose; the tests of
+    each kind of tile rely on these."""
+    assert mo.mx_plan_info([(16384, 10240, 2560)]) == dict(
+        tile_rows=256, parts=[1], past_caches=True, xcd_items=[640 * i for i in range(9)])
+    info = mo.mx_plan_info([(2048, 2560, 2560)], torch.float32)
+    assert (info["tile_rows"], info["parts"], info["past_caches"]) == (128, [1], False)
+    info = mo.mx_plan_info([(768, 768, 8192), (0, 768, 8192), (768, 768, 0)], torch.float32)
+    assert info["tile_rows"] == 128 and info["parts"][0] > 1 and info["parts"][1:] == [0, 1]
+    # a list of more than one launch: the ranges are the first one's
+    info = mo.mx_plan_info([(256, 128, 128)] * 80)
+    assert info["parts"] == [1] * 80 and info["xcd_items"][-1] == 36 * (256 // info["tile_rows"])
+    assert mo.mx_plan_info([(0, 5, 7)])["xcd_items"] == [0] * 9
+
+
+def test_plan_info_refusals(lib):
+    def call(m=64, n=32, k=96, out=None, dt=F32, count=1):
+        a, b, _ = _operands([(m, n, k)])
+        o = _arr([_lib.MuonMat(None, *(out or (m, n)), n, dt, 0)])
+        return lib.muon_mx_plan_info(a, b, o, count, None, None, None, None)
+    assert call() == 0
+    assert call(count=0) == E["MUON_E_SHAPE"] and call(m=-1) == E["MUON_E_SHAPE"]
+    assert call(out=(64, 33)) == E["MUON_E_SHAPE"] and call(k=(1 << 24) + 1) == E["MUON_E_SHAPE"]
+    assert call(dt=9) == E["MUON_E_DTYPE"]
+    a, b, _ = _operands([(1, 1, 1)])
+    assert lib.muon_mx_plan_info(a, b, None, 1, None, None, None, None) == E["MUON_E_NULL"]
+    with pytest.raises(_lib.MuonError):
+        mo.mx_plan_info([])
+    with pytest.raises(_lib.MuonError):
+        mo.mx_plan_info([(-1, 5, 7)])
