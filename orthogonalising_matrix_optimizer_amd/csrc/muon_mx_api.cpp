@@ -187,21 +187,23 @@ ProductPlan plan_products(const muon_mx* a, const muon_mx* b, int n) {
 // Deals a launch's work items to the eight XCDs: contiguous ranges (items that
 // follow each other share operands) with an eighth of the stages each.  An empty
 // item counts as one stage.
-void share_out(MxGemmArgs& g, int64_t items, double stages) {
+void share_out(MxGemmArgs& g, int64_t items) {
+  auto own = [&](int i) { return (i + 1 < g.n ? g.base[i + 1] : items) - int64_t(g.base[i]); };
+  auto per_item = [&](int i) { return std::max(1.0, double(g.m[i].tiles) * g.m[i].kt / own(i)); };
+  double stages = 0;
+  for (int i = 0; i < g.n; ++i) stages += own(i) * per_item(i);
   int64_t at = 0;
   double before = 0;
   int x = 0;
   g.c.xcd[0] = 0;
   for (int i = 0; i < g.n && x < 7; ++i) {
-    const MxProduct& p = g.m[i];
-    const int64_t own = (i + 1 < g.n ? g.base[i + 1] : items) - at;
-    const double per = std::max(1.0, double(p.tiles) * p.kt / own);
-    while (x < 7 && before + own * per >= stages * (x + 1) / 8) {
+    const double per = per_item(i), part = own(i) * per;
+    while (x < 7 && before + part >= stages * (x + 1) / 8) {
       const double want = (stages * (x + 1) / 8 - before) / per;
-      g.c.xcd[++x] = int32_t(at + std::min<int64_t>(own, std::max<int64_t>(0, int64_t(want + 0.5))));
+      g.c.xcd[++x] = int32_t(at + std::min<int64_t>(own(i), std::max<int64_t>(0, int64_t(want + 0.5))));
     }
-    at += own;
-    before += own * per;
+    at += own(i);
+    before += part;
   }
   while (x < 8) g.c.xcd[++x] = int32_t(items);
 }
@@ -219,7 +221,6 @@ struct ProductLaunch {
   MxGemmArgs g;
   MxReduceArgs red;
   int64_t items, blocks, written;   // work items, blocks of the sum, bytes of output
-  double stages;
   ProductLaunch() { std::memset(this, 0, sizeof(*this)); }
 };
 
@@ -233,11 +234,10 @@ int build_launches(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
   int rc;
   auto flush = [&]() {
     if (l.g.n == 0) return int(MUON_OK);
-    share_out(l.g, l.items, l.stages);
+    share_out(l.g, l.items);
     const int code = run();
     l.g.n = l.red.n = 0;
     l.items = l.blocks = l.written = 0;
-    l.stages = 0;
     return code;
   };
   for (int i = 0; i < n; ++i) {
@@ -285,7 +285,6 @@ int build_launches(const muon_mx* a, const muon_mx* b, const muon_mat* out, int3
     l.items += tiles * splits;
     l.blocks += nb;
     l.written += M * N * esize(out[i].dtype);
-    l.stages += double(tiles) * kt;
   }
   return flush();
 }

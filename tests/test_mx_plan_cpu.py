@@ -90,3 +90,42 @@ def test_plan_info_refusals(lib):
         mo.mx_plan_info([])
     with pytest.raises(_lib.MuonError):
         mo.mx_plan_info([(-1, 5, 7)])
+
+
+def _stages_by_xcd(shapes, info):
+    """Steps of 128 columns that each XCD's items have, an empty item counting as one."""
+    items = []
+    for (m, n, k), parts in zip(shapes, info["parts"]):
+        tiles, kt = -(-m // info["tile_rows"]) * -(-n // 128), -(-k // 128)
+        chunk = -(-kt // parts) if parts else 0
+        for p in range(parts):
+            items += [max(1, min(chunk, kt - p * chunk))] * tiles
+    edges = info["xcd_items"]
+    assert edges[0] == 0 and edges[-1] == len(items) and edges == sorted(edges)
+    return [sum(items[a:b]) for a, b in zip(edges, edges[1:])]
+
+
+@pytest.mark.parametrize("shapes", [
+    [(2048, 1408, 256 * (i % 2)) for i in range(36)],               # every second expert without tokens
+    [(2048, 1408, 0)] * 5,                                          # none with any
+    [(2048, 1408, 0)] * 18 + [(2048, 1408, 256)] * 18,
+    [(2048, 1408, 256)] * 18 + [(2048, 1408, 0)] * 18,
+    [(768, 768, 2000 * i) for i in range(12)],                      # split, the first one empty
+    [(768, 768, 200 * (i % 3)) for i in range(30)] + [(768, 768, 30000)],
+    [(1000 + 100 * i, 1408, 2048) for i in range(36)],
+    [(16384, 10240, 2560)],
+])
+def test_work_is_dealt_evenly_to_the_xcds(lib, shapes):
+    """An eighth of the steps each, within the longest item at either end.  A split
+    product's items count with their mean length, and its last part is shorter:
+    up to there its tiles have done as many steps more as that part lacks."""
+    info = mo.mx_plan_info(shapes, torch.float32)
+    stages = _stages_by_xcd(shapes, info)
+    longest = short = 0
+    for (m, n, k), parts in zip(shapes, info["parts"]):
+        kt = -(-k // 128)
+        chunk = -(-kt // max(1, parts))
+        longest = max(longest, chunk, 1)
+        if kt:
+            short = max(short, -(-m // info["tile_rows"]) * -(-n // 128) * (chunk * parts - kt))
+    assert max(abs(s - sum(stages) / 8) for s in stages) <= 2 * longest + short, (stages, info)
