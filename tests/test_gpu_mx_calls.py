@@ -134,3 +134,31 @@ def test_layers_in_an_autograd_function():
             f()
     assert mo.mx_quantize(weight).shape == (40, 64)
     assert len(mo.Muon([torch.nn.Parameter(w.clone())], mx=True).mx) == 1
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 33), (17, 129), (65, 200), (130, 257), (300, 5)])
+def test_blocks_past_the_last_column_are_zeros_with_an_ordinary_scale(rows, cols):
+    """What a product reads there adds nothing to a row, whatever the row holds."""
+    announce(f"padding {rows}x{cols}")
+    for dtype in (BF16, F32):
+        x = _rand(rows, cols, dtype, 7)
+        x[0, -1] = float("nan")
+        x[-1, 0] = float("inf")
+        for kw in (dict(), dict(seed=3), dict(dropout=0.4, dropout_seed=2), dict(seed=3, dropout=0.4, dropout_seed=2)):
+            q, qt = mo.mx_quantize(x, "both", **kw)
+            for m in (q, qt, mo.mx_quantize(x, False, **kw), mo.mx_quantize(x, True, **kw)):
+                kt, rt, st = -(-m.cols // 128), -(-m.rows // 16), -(-m.rows // 64)
+                raw = m.data.cpu().numpy()
+                n = kt * rt * 1024
+                # [k tile, row tile, block in k tile, row in tile, bytes]
+                codes = raw[:n].reshape(kt, rt, 4, 16, 16)
+                scales = raw[n:].reshape(kt, st, 4, 16, 4)
+                for b in range(-(-m.cols // 32), 4 * kt):
+                    for r in range(m.rows):
+                        assert not codes[b // 4, r // 16, b % 4, r % 16].any()
+                        assert scales[b // 4, r // 64, b % 4, r % 16, r % 64 // 16] != 255
+                # and the elements past it in its own block
+                last = -(-m.cols // 32) - 1
+                for e in range(m.cols - 32 * last, 32):
+                    byte = codes[last // 4, :, last % 4].reshape(rt * 16, 16)[:m.rows, e // 2]
+                    assert not (byte >> (4 * (e & 1)) & 15).any()
