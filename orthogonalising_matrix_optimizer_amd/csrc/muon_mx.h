@@ -23,7 +23,6 @@
 
 namespace muon {
 
-constexpr int kMxBlock = 32;       // elements that share a scale
 constexpr int kMxTileR = 16;       // rows of a code tile
 constexpr int kMxTileK = 128;      // columns of a code tile
 constexpr int kMxTileBytes = 1024;

@@ -20,7 +20,8 @@ using namespace muon;
 namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;
-// the products address a panel of 256 rows with 32-bit offsets
+// where an fp32 sum of equal terms stops growing; it also keeps the parts of a
+// split contraction (kMinChunk code tiles at least) to 2^13
 constexpr int64_t kMaxCols = int64_t(1) << 24;
 // a grid has fewer than 2^32 threads: blocks of 256, and of the quantiser's 1024
 constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;

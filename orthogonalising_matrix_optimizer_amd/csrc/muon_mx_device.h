@@ -67,7 +67,6 @@ __device__ __forceinline__ int find_in_list(const L& l, uint32_t b) {
 
 // 16 bytes at any element's address: the hardware needs no more alignment.
 typedef u32x4_t u32x4_any __attribute__((aligned(2)));
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 template <class T>
 __device__ __forceinline__ u32x4_t load16b(const T* p) {
   return *reinterpret_cast<const GAS u32x4_any*>(glb(p));
@@ -109,11 +108,6 @@ __device__ __forceinline__ void store8(uint16_t* p, const float* v) { store16b(p
 __device__ __forceinline__ void store8(float* p, const float* v) {
   store16b(p, bits4(v));
   store16b(p + 4, bits4(v + 4));
-}
-__device__ __forceinline__ void stream8(uint16_t* p, const float* v) { stream16b(p, narrow8(v)); }
-__device__ __forceinline__ void stream8(float* p, const float* v) {
-  stream16b(p, bits4(v));
-  stream16b(p + 4, bits4(v + 4));
 }
 __device__ __forceinline__ float load1(const uint16_t* p) {
   return __uint_as_float(static_cast<uint32_t>(*glb(p)) << 16);
