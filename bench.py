@@ -56,9 +56,13 @@ def traffic_file(workload: str) -> str:
     return os.path.join(ROOT, "profiles", f"traffic_apply_{workload}.json")
 
 
+# the source of the GEMM kernels
+GEMM_SOURCES = ("muon_gemm.hip", "muon_common.h", "muon_device.h")
+
+
 def _src_hash() -> str:
     h = hashlib.sha256()
-    for f in ("muon_gemm.hip", "muon_common.h"):
+    for f in GEMM_SOURCES:
         with open(os.path.join(ROOT, "orthogonalising_matrix_optimizer_amd", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
