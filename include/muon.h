@@ -403,7 +403,10 @@ int muon_adamw_step(const muon_vec* params, const muon_vec* grads, muon_adamw_st
  * Words serve elements from the first word's low bits upwards.
  * A seed is given by value or, where the *_dev pointer is not NULL, by the
  * device address of one (8-byte aligned), read when the kernel runs: a
- * replayed graph repeats its numbers unless that memory changes.
+ * replayed graph repeats its numbers unless that memory changes.  Nothing else
+ * enters: calls with one seed have the same numbers at the same places, so a
+ * program gives each layer and each step a seed of its own (for instance step *
+ * layers + layer), or all layers of a shape drop and round alike.
  *
  * All matrices of one call may have different shapes, zero rows or columns
  * included, and share one element type.  The matrices here need only the

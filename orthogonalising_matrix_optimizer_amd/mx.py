@@ -8,6 +8,10 @@ computation runs in the HIP library; this module allocates outputs and passes
 pointers with the current stream of the tensors' device.  Descriptors are
 packed as bytes: on a single token a call's cost is the host's.
 
+A seed fixes the numbers of a call whatever layer it is for: give each layer
+and each step its own (step * layers + layer), or all layers of a shape drop
+the same elements.  Within a list each matrix has its own numbers.
+
 Nothing here is recorded by autograd.  The gradients are calls of their own
 (mx_linear_grad, dropout on the gradient), made by hand or by the two halves of
 a torch.autograd.Function; mx_linear, mx_linear_grad and dropout refuse a tensor
@@ -305,7 +309,8 @@ def mx_quantize(x: Union[torch.Tensor, Sequence[torch.Tensor]], transpose: Union
     transpose=True one of the transpose, with transpose="both" an MXPair of
     the two from one read.  Rounds to nearest, or stochastically with a
     `seed` (an int, or a one-element int64 tensor read when the kernel runs).
-    `dropout` quantises what dropout(x, dropout, dropout_seed) would store.
+    `dropout` quantises what dropout(x, dropout, dropout_seed) would store (in
+    a list, of its first matrix: each has the numbers of its place).
     A list is quantised in one call and gives a list; `out` takes results of
     an earlier call of the same shapes and overwrites them."""
     if transpose not in (False, True, "both"):
@@ -445,8 +450,9 @@ def mx_linear(x: torch.Tensor, w: MX4, save: bool = False, dropout: float = 0.0,
               dropout_seed: Optional[Seed] = None):
     """x W^T for W in 4 bits and x [..., in] quantised here to nearest; the
     result [..., out] has x's type.  With `dropout` the layer's input is
-    dropout(x, dropout, dropout_seed).  With `save` returns (y, saved), saved
-    being what mx_linear_grad needs: the input's transpose in 4 bits."""
+    dropout(x, dropout, dropout_seed), with a seed that no other layer or step
+    has.  With `save` returns (y, saved), saved being what mx_linear_grad
+    needs: the input's transpose in 4 bits."""
     _not_recorded(x)
     x2 = _rows_of(x)
     rows, cols = x2.shape

@@ -281,7 +281,8 @@ class StepGraph:
     same buffers (parameters, the gradient tensors given at capture, state,
     workspace) with the captured lr, wd, beta, coefficients and weight-average
     flags.  Write new gradients into the captured gradient tensors before a
-    replay.  Host counters advance per replay as for an eager step (through
+    replay (of a gradient given as 4-bit factors, into both factors' `data`).
+    Host counters advance per replay as for an eager step (through
     the library's muon_state_advance).  Eager steps, orthogonalisations and
     blends on the same optimizer between replays are allowed; capturing
     another graph on it replaces the table this one replays with.  Capture is

@@ -162,3 +162,28 @@ def test_blocks_past_the_last_column_are_zeros_with_an_ordinary_scale(rows, cols
                 for e in range(m.cols - 32 * last, 32):
                     byte = codes[last // 4, :, last % 4].reshape(rt * 16, 16)[:m.rows, e // 2]
                     assert not (byte >> (4 * (e & 1)) & 15).any()
+
+
+def test_layers_of_a_shape_with_seeds_of_their_own():
+    """The documented loop: seeds step * layers + layer give layers and steps
+    masks and roundings of their own; one seed gives the same ones."""
+    announce("seeds by layer")
+    mats = [_rand(64, 96, BF16, 1), _rand(64, 96, BF16, 2)]
+    opt = mo.Muon(mats, lr=0.02, mx=True)
+    x, dy = torch.ones(50, 96, dtype=BF16, device="cuda"), _rand(50, 64, BF16, 4)
+    masks, rounded = [], []
+    for step in range(2):
+        pairs = []
+        for i in range(len(mats)):
+            seed = step * len(mats) + i
+            y, saved = mo.mx_linear(x, opt.mx[i].w, save=True, dropout=0.5, dropout_seed=seed)
+            dx, pair = mo.mx_linear_grad(dy, opt.mx[i].w_t, saved, seed=seed, pair=True)
+            masks.append(saved.x_t.dequantize(F32) != 0)
+            rounded.append(pair[0].dequantize(F32))
+            pairs.append(pair)
+        opt.step(pairs)
+    for a in range(4):
+        for b in range(a):
+            assert not torch.equal(masks[a], masks[b]) and not torch.equal(rounded[a], rounded[b])
+    again = mo.mx_linear(x, opt.mx[0].w, save=True, dropout=0.5, dropout_seed=3)[1]
+    assert torch.equal(again.x_t.dequantize(F32) != 0, masks[3])
