@@ -412,7 +412,8 @@ int muon_adamw_step(const muon_vec* params, const muon_vec* grads, muon_adamw_st
  * included, and share one element type.  The matrices here need only the
  * alignment of their elements (16-byte aligned rows are faster).  Nothing a
  * call writes may overlap anything else that it reads or writes
- * (MUON_E_ALIAS); column slices of one buffer do not overlap.  Calls keep no
+ * (MUON_E_ALIAS); slices of one buffer (columns, single rows, every n-th row)
+ * that share no byte do not overlap.  Calls keep no
  * state and may run under stream capture and from several host threads at
  * once; only muon_mx_matmul takes a workspace. */
 

@@ -154,12 +154,13 @@ __device__ __forceinline__ void wait_stage(int ahead, bool extra) {
 // Measured on MI355X (random codes, 16384 x 2560 outputs, K = 10240): 256 x 128
 // tiles of four waves, two blocks a CU, 3.9-4.3 PF; 128 x 128, three blocks,
 // 3.5-3.8; 256 x 256 of eight waves 3.6-3.9 (with the two waves of a SIMD
-// alternating between reads and products 2.9).  What bounds it: power and the
-// loads into LDS.  The instruction alone sustains 9.5 PF on zeros and 7.1 on
-// random codes; 16384 x 4096 x 10240 takes 304 us on zeros and 424 on random
-// codes (quantised normal numbers lie between), with every stage in L2 278 and
-// 360, the loads alone 194, and 156 from L2 (28 TB/s).  The matrix units are busy
-// 36-46 % of the time at 2.2-2.3 GHz in the products of a 2560 x 10240 layer.
+// alternating between reads and products 2.9).  What bounds it: loads into LDS
+// and products hardly overlap.  The instruction alone sustains 9.5 PF on zeros and
+// 7.1 on random codes, so 16384 x 4096 x 10240 would take 145 and 194 us; the
+// loads alone take 194, and 156 from L2 (28 TB/s); together they take 304 us on
+// zeros and 424 on random codes, with every stage in L2 278 and 360.  In the
+// products of a 2560 x 10240 layer the matrix units are busy 34-43 % of the time at
+// 2.1-2.2 GHz, LDS reads 15-19 %, and waves wait for LDS 5-7 % of theirs.
 template <class Args, int ODT, int TM, int TN, int WM, int WN, int NST, int PER_CU, bool DROP, bool KEEP>
 __global__ __launch_bounds__(64 * WM * WN, PER_CU * WM * WN / 4) void k_mx_gemm(Args args) {
   using T = typename std::conditional<ODT == kBF16, uint16_t, float>::type;
@@ -600,6 +601,14 @@ void launch_rows_of(const MxRowsArgs& a, hipStream_t s) {
 //   1 x 10240 x 2560: 10.0 | 6.2 | 8.9;  13 rows 14.4 | 10.6 | 13.2
 //   1 x 768 x 768: 2.5 | 2.1 | 2.0;  16 x 768 x 2304: 3.6 | 3.2 | 3.1
 // Many rows of b amortise x; a long contraction with few of them needs the waves.
+// In between (bf16, graph of launches, 1 x row | 16 rows of x):
+//   4096 x 4096: 5.7 | 4.3 | 5.0 and 7.5 | 6.3 | 6.7;  2560 x 4096: 3.8 | 3.4 | 3.5 and 4.8 | 4.4 | 4.4
+//   6144 x 6144: 8.4 | 7.3 | 7.9 and 10.5 | 13.3 | 11.9;  2560 x 6144: 4.9 | 4.3 | 4.6 and 6.1 | 7.8 | 6.7
+//   6144 x 8192: 9.1 | 8.4 | 8.6 and 11.3 | 14.5 | 12.5;  768 x 8192: 3.2 | 3.0 | 3.0 and 3.8 | 4.8 | 3.7
+//   10240 x 10240: 13.1 | 14.6 | 13.8 and 18.5 | 29.2 | 26.2
+// So one row would take the sixteen waves up to about 9000 rows of b, sixteen rows
+// the four tiles from about 5000 on; between those and 8192 the rule is up to 1.3
+// times slower for sixteen rows, and up to 1.1 times at 8192 for one.
 // b with at most MUON_MX_FEW_ROWS_MAX_N rows keeps the grid below 2^32 threads.
 template <int XDT, int ODT>
 hipError_t launch_rows(const MxRowsArgs& a, hipStream_t s) {
