@@ -28,9 +28,8 @@ inline bool meets(const Span& s, uintptr_t lo, uintptr_t hi) {
   return next < s.hi && next < hi;
 }
 
-// Whether two spans share a byte: slices of one buffer do not, a single row
-// (which callers describe by its width alone) or every n-th row among them.
-// Spans of other pitches may be taken to share one that they do not.
+// Whether two spans share a byte.  A single row is described by its width alone,
+// every n-th row of a buffer by n pitches.
 inline bool share(const Span& a, const Span& b) {
   if (b.lo >= a.hi || a.lo >= b.hi) return false;
   auto run = [](const Span& s) { return s.hi - s.lo == s.width || s.pitch == s.width; };
@@ -40,7 +39,14 @@ inline bool share(const Span& a, const Span& b) {
   const size_t pitch = std::gcd(a.pitch, b.pitch);
   const Span &first = a.lo < b.lo ? a : b, &second = a.lo < b.lo ? b : a;
   const size_t d = (second.lo - first.lo) % pitch;
-  return d < first.width || d + second.width > pitch;
+  if (d >= first.width && d + second.width <= pitch) return false;
+  // else the rows themselves, of the span with fewer of them, where the other is
+  const Span &few = a.pitch > b.pitch ? a : b, &many = a.pitch > b.pitch ? b : a;
+  uintptr_t row = few.lo;
+  if (many.lo > row) row += (many.lo - row) / few.pitch * few.pitch;
+  for (; row < few.hi && row < many.hi; row += few.pitch)
+    if (meets(many, row, row + few.width)) return true;
+  return false;
 }
 
 // Whether something written is also read or written through another argument.

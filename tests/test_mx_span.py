@@ -79,13 +79,11 @@ def answers3(tmp_path_factory):
     return lambda groups: [c for c, in ask(groups)]
 
 
-def _check(pairs, got, exact):
+def _check(pairs, got):
     for (a, b), (share, conflict) in zip(pairs, got):
         real = bool(_bytes(a) & _bytes(b))
-        assert share >= real, (a, b)
+        assert share == real, (a, b)
         assert conflict == (share and (a[4] or b[4])), (a, b)
-        if exact:
-            assert share == real, (a, b)
 
 
 def _slice(rng, pitch, rows):
@@ -106,10 +104,8 @@ def test_column_slices_of_one_buffer(answers):
     while len(pairs) < 20000:
         pitch, rows = rng.randint(1, 12), rng.randint(1, 9)
         a, b = _slice(rng, pitch, rows), _slice(rng, pitch, rows)
-        # every second row against every third is looked at below
-        if a[1] == 1 or b[1] == 1 or a[2] == b[2]:
-            pairs.append((a, b))
-    _check(pairs, answers(pairs), exact=True)
+        pairs.append((a, b))
+    _check(pairs, answers(pairs))
 
 
 def test_strided_rows_beside_a_column_slice(answers):
@@ -120,17 +116,17 @@ def test_strided_rows_beside_a_column_slice(answers):
              ((1100, 1, 31, 31, 1), (1030, 17, 100, 30, 1)),
              ((1100, 1, 30, 30, 0), (1100, 1, 30, 30, 0))]
     assert [s for s, _ in answers(pairs)] == [0, 1, 0, 0, 1, 1]
-    _check(pairs, answers(pairs), exact=True)
+    _check(pairs, answers(pairs))
 
 
-def test_no_shared_byte_is_missed(answers):
+def test_spans_of_any_pitch(answers):
     rng = random.Random(2)
     pairs = []
     for _ in range(40000):
         a, b = ((1000 + rng.randrange(60), rng.randint(1, 6), p, rng.randint(1, p), rng.randrange(2))
                 for p in (rng.randint(1, 14), rng.randint(1, 14)))
         pairs.append((a, b))
-    _check(pairs, answers(pairs), exact=False)
+    _check(pairs, answers(pairs))
 
 
 def test_two_operands_that_begin_and_end_alike(answers3):
