@@ -503,6 +503,125 @@ int muon_mx_matmul_rows(const muon_mat* x, const muon_mx* b, const muon_mat* out
 int muon_dropout(const muon_mat* in, const muon_mat* out, float p, uint64_t seed,
                  const uint64_t* seed_dev, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A token model's sparse parts: the embedding table (which AdamW steps) and
+ * layers of experts (whose matrices the Muon step takes), each with its
+ * gradient.  Calls keep no state and may run under stream capture and from
+ * several host threads at once; matrices need only the alignment of their
+ * elements (16-byte aligned rows are faster).  Nothing a call writes may
+ * overlap anything else that it reads or writes (MUON_E_ALIAS).  Device
+ * indexes outside their range are never followed: what they stand for counts
+ * as absent.  Workspaces are the caller's, 16-byte aligned, used by the call's
+ * work on the stream alone and need no initialisation.
+ *
+ * Slots.  Each of n_tokens tokens has k slots (t, j), numbered t * k + j, each
+ * with an expert.  Sorted by expert, by number among equals, they are the rows
+ * of the experts' products: expert e has the rows offsets[e] to offsets[e+1]-1.
+ * A slot whose expert is outside 0 .. experts-1 (-1, say: a token of padding) is
+ * dropped: it has no row and takes no part.  Rows from offsets[experts] on
+ * belong to no slot; products read and write none of them. */
+
+#define MUON_MAX_EXPERTS 512
+#define MUON_MAX_K 64
+#define MUON_MAX_SLOTS 16777216   /* slots of a plan, tokens of an embedding's gradient */
+
+/* The sorted slots, on the device. */
+typedef struct {
+  int32_t* offsets;   /* experts + 1 entries                                   */
+  int32_t* tokens;    /* n_tokens * k entries: the token of each row, -1 behind
+                         the last expert's rows                               */
+  int32_t* place;     /* n_tokens * k entries: the row of each slot, -1 if it
+                         was dropped                                           */
+  int64_t  n_tokens;
+  int32_t  k;
+  int32_t  experts;
+} muon_slots;
+
+/* `count` row-major rows x cols matrices: element (i, j) of matrix e at
+ * ptr[e*stride + i*ld + j].  stride >= (rows-1)*ld + cols. */
+typedef struct {
+  void*   ptr;
+  int64_t count, rows, cols, ld, stride;
+  int32_t dtype;
+  int32_t _pad;
+} muon_stack;
+
+/* Contiguous integers on the device, of 4 or 8 bytes. */
+typedef struct {
+  const void* ptr;
+  int64_t     n;
+  int32_t     bytes;
+  int32_t     _pad;
+} muon_ids;
+
+/* Sorts the slots of a choice of experts (n_tokens * k integers) into `slots`. */
+size_t muon_expert_plan_workspace_bytes(int64_t n_tokens, int32_t k, int32_t experts);
+int muon_expert_plan(const muon_ids* choice, const muon_slots* slots, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* The k experts of each token with the largest of its logits (n_tokens x
+ * experts), in falling order, ties to the lowest expert, and their sorted slots.
+ * An expert whose logit is -inf is not chosen: slots for which none is left
+ * have expert -1 and gate 0.  gates (n_tokens x k, dense) are the softmax over
+ * all experts, or with `normalize` over the chosen ones.  A token with a NaN or
+ * +inf among its logits has NaN gates (NaN goes before all numbers).
+ * Workspace as for muon_expert_plan. */
+int muon_route(const muon_mat* logits, int32_t normalize, float* gates, int32_t* chosen,
+               const muon_slots* slots, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of the gates with respect to the logits: with p the softmax over all
+ * experts, dlogits_i = p_i ([i chosen] dgate_i - sum_j dgate_j gate_j); with
+ * `normalize` gate_i (dgate_i - sum) for the chosen and 0 for the others.
+ * dgates of dropped slots count as 0; a token without any expert gets zeros. */
+int muon_route_grad(const float* dgates, const muon_mat* logits, const float* gates,
+                    const int32_t* chosen, int32_t k, int32_t normalize,
+                    const muon_mat* dlogits, void* stream);
+
+/* Products of the slots' rows with their experts' matrices w (experts x out x
+ * in), all operands of one element type, sums in fp32, rounded once to the type
+ * of what is written.  x has a row for each slot in the sorted order, or with
+ * `gather` one for each token (of less than 0xf0000000 bytes in all: MUON_E_SHAPE, and
+ * muon_expert_gather makes sorted rows).  fp32 operands are multiplied as sums of
+ * three bf16 terms each (all of their 24 bits; products' terms below 2^-24 are
+ * left out); one that is not finite makes the sums it enters NaN.
+ *   linear:    out[r] = x[r] w[e(r)]^T                 (slots x out)
+ *   linear_dx: dx[r]  = dy[r] w[e(r)]                  (slots x in)
+ *   linear_dw: dw[e]  = sum over e's rows dy[r]^T x[r] (out x in; zeros without
+ *              rows), added to dw with `accumulate`.
+ * Rows behind the last expert's are left as they were. */
+int muon_expert_linear(const muon_mat* x, const muon_stack* w, const muon_slots* slots,
+                       int32_t gather, const muon_mat* out, void* stream);
+int muon_expert_linear_dx(const muon_mat* dy, const muon_stack* w, const muon_slots* slots,
+                          const muon_mat* dx, void* stream);
+size_t muon_expert_linear_dw_workspace_bytes(int64_t slots, const muon_stack* dw);
+int muon_expert_linear_dw(const muon_mat* dy, const muon_mat* x, const muon_slots* slots,
+                          int32_t gather, int32_t accumulate, const muon_stack* dw,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* out[r] = x[token of row r]: the tokens' rows in the sorted order. */
+int muon_expert_gather(const muon_mat* x, const muon_slots* slots, const muon_mat* out,
+                       void* stream);
+
+/* out[t] = sum_j gates[t,j] y[row of slot (t,j)] in fp32, in the order of j, and
+ * its gradients: dy[row of (t,j)] = gates[t,j] dout[t], dgates[t,j] = the
+ * product of dout[t] and that row of y (0 where dropped).  gates may be NULL
+ * for ones (the gradient of a gathered x); dy or dgates may be NULL. */
+int muon_expert_combine(const muon_mat* y, const float* gates, const muon_slots* slots,
+                        const muon_mat* out, void* stream);
+int muon_expert_combine_grad(const muon_mat* dout, const muon_mat* y, const float* gates,
+                             const muon_slots* slots, const muon_mat* dy, float* dgates,
+                             void* stream);
+
+/* out[t] = scale * w[ids[t]] (a row of zeros for an id outside w's rows: padding),
+ * and the gradient dw[v] = scale * sum of dy[t] over the tokens with ids[t] = v, in
+ * fp32 in an order that depends on nothing but the ids; rows without tokens are
+ * zeroed, or with `accumulate`, which adds to dw, left as they are. */
+int muon_embedding(const muon_ids* ids, const muon_mat* w, float scale, const muon_mat* out,
+                   void* stream);
+size_t muon_embedding_grad_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols);
+int muon_embedding_grad(const muon_mat* dy, const muon_ids* ids, float scale, int32_t accumulate,
+                        const muon_mat* dw, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,6 +25,8 @@ MAX_STEPS = 16
 NOALLOC_SCRATCH_BYTES = 64 << 20
 MX_FEW_ROWS = 16
 MX_FEW_ROWS_MAX_N = (1 << 29) - 64
+MAX_EXPERTS, MAX_K, MAX_SLOTS = 512, 64, 1 << 24
+GATHER_BYTES = 0xf0000000   # a product gathers from less than this
 
 
 class MuonMat(ctypes.Structure):
@@ -71,6 +73,20 @@ class MXOptions(ctypes.Structure):
     _fields_ = [("stochastic", c_int32), ("accumulate", c_int32), ("dropout", c_float),
                 ("_pad", c_int32), ("seed", c_uint64), ("dropout_seed", c_uint64),
                 ("seed_dev", c_void_p), ("dropout_seed_dev", c_void_p)]
+
+
+class MuonSlots(ctypes.Structure):
+    _fields_ = [("offsets", c_void_p), ("tokens", c_void_p), ("place", c_void_p),
+                ("n_tokens", c_int64), ("k", c_int32), ("experts", c_int32)]
+
+
+class MuonStack(ctypes.Structure):
+    _fields_ = [("ptr", c_void_p), ("count", c_int64), ("rows", c_int64), ("cols", c_int64),
+                ("ld", c_int64), ("stride", c_int64), ("dtype", c_int32), ("_pad", c_int32)]
+
+
+class MuonIds(ctypes.Structure):
+    _fields_ = [("ptr", c_void_p), ("n", c_int64), ("bytes", c_int32), ("_pad", c_int32)]
 
 
 class MuonError(RuntimeError):
@@ -153,6 +169,26 @@ def load() -> ctypes.CDLL:
     lib.muon_mx_matmul_rows.restype = c_int32
     lib.muon_dropout.argtypes = [V, V, c_float, c_uint64, V, V]
     lib.muon_dropout.restype = c_int32
+    # so are those of the embedding table and the expert layers
+    I, L, Z = c_int32, c_int64, c_size_t
+    for name, args in (("muon_expert_plan", [V, V, V, Z, V]),
+                       ("muon_route", [V, I, V, V, V, V, Z, V]),
+                       ("muon_route_grad", [V, V, V, V, I, I, V, V]),
+                       ("muon_expert_linear", [V, V, V, I, V, V]),
+                       ("muon_expert_linear_dx", [V, V, V, V, V]),
+                       ("muon_expert_linear_dw", [V, V, V, I, I, V, V, Z, V]),
+                       ("muon_expert_gather", [V, V, V, V]),
+                       ("muon_expert_combine", [V, V, V, V, V]),
+                       ("muon_expert_combine_grad", [V, V, V, V, V, V, V]),
+                       ("muon_embedding", [V, V, c_float, V, V]),
+                       ("muon_embedding_grad", [V, V, c_float, I, V, V, Z, V])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = c_int32
+    for name, args in (("muon_expert_plan_workspace_bytes", [L, I, I]),
+                       ("muon_expert_linear_dw_workspace_bytes", [L, V]),
+                       ("muon_embedding_grad_workspace_bytes", [L, L, L])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = c_size_t
     _LIB = lib
     return lib
 

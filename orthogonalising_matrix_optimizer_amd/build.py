@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmuon_mi355x.so")
 SOURCES = ["muon_elem.hip", "muon_gemm.hip", "muon_noalloc.hip", "muon_mx_elem.hip", "muon_mx_gemm.hip",
-           "muon_api.cpp", "muon_mx_api.cpp"]
+           "muon_route.hip", "muon_rows.hip", "muon_experts.hip",
+           "muon_api.cpp", "muon_mx_api.cpp", "muon_sparse_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -19,7 +19,7 @@ from . import build as _build
 
 OUT_DIR = os.path.join(_build.BUILD, "sanitized")
 LIB = os.path.join(OUT_DIR, "libmuon_mi355x_sanitized.so")
-HOST_SOURCES = ["muon_api.cpp", "muon_mx_api.cpp"]
+HOST_SOURCES = ["muon_api.cpp", "muon_mx_api.cpp", "muon_sparse_api.cpp"]
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 SANITIZE = ["-fsanitize=address,undefined", "-fno-sanitize-recover=undefined",
             "-fno-omit-frame-pointer"]

@@ -1,0 +1,534 @@
+// Products of ragged groups of rows with their experts' matrices on gfx950 MFMA.
+//
+// The rows of expert e are the sorted slots offsets[e] .. offsets[e+1]-1, which
+// only the device knows.  Three products, C = R C^T in the general form, where
+// the operand of the output's rows and that of its columns hold the contraction
+// either along their rows in memory ("along") or across them ("across"):
+//   fwd: out rows = slots, columns = out features; x along, w along
+//   dx:  out rows = slots, columns = in features;  dy along, w across
+//   dw:  out rows = out features, columns = in features, contraction over the
+//        expert's slots; dy across, x across
+// A block computes one tile; it finds its expert by a wave's sum over the
+// experts' tile counts.  Blocks are dealt to XCDs so that each works on a
+// contiguous range of tiles, which share operand panels in its L2.
+//
+// LDS holds stages of BK contraction elements.  An operand along the
+// contraction is kept as rows of 16-byte chunks, XOR-swizzled by row, read by
+// 16-byte reads; one across it as contraction rows, from which the transposing
+// read builds operands.  Contraction elements past the end are zeros in both
+// operands, so that nothing of a neighbour (a NaN, say) enters a sum.
+//
+// bf16 operands whose rows start at 16 bytes and hold whole 16-byte pieces go
+// straight to LDS (LDS-DMA), which zeroes what a lane points past the buffer's
+// end.  All others are loaded into registers and checked there.  fp32 operands
+// are split there into three bf16 terms h + m + l, each the rounding of what the
+// terms before leave (24 bits in all), and six of the nine products of terms
+// are summed, the largest left out being m l with 2^-26 of h h: an fp32 product
+// in six bf16 matrix instructions, which together run at 2.7 times the rate of
+// the fp32 matrix instruction.
+//
+// The four results that the matrix instruction leaves in consecutive registers
+// are rows of its first operand, which is that of the output's columns.  Its 32
+// rows are taken in an order that leaves a lane 16 consecutive columns of
+// one output row.
+#include <atomic>
+#include <type_traits>
+
+#include "muon_common.h"
+#include "muon_device.h"
+#include "muon_mx_device.h"
+#include "muon_sparse.h"
+
+namespace muon {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+
+constexpr uint32_t kPast = kExpertSpan;    // an offset past every buffer: reads as zeros
+constexpr int kBatch = 64;                // experts looked at at once
+
+// ---- the tile of a block
+struct Tile {
+  int e;        // expert
+  int lo, hi;   // its rows
+  int r0, c0;   // first row (fwd, dx: from lo; dw: of the matrix) and column
+  bool any;
+};
+
+__device__ __forceinline__ int clamp_to(int v, int most) { return v < 0 ? 0 : v < most ? v : most; }
+
+// An expert's rows, whatever the offsets hold.
+__device__ __forceinline__ void rows_of(const ExpertArgs& a, int e, int& lo, int& hi) {
+  lo = clamp_to(a.offsets[e], a.slots);
+  hi = clamp_to(a.offsets[e + 1], a.slots);
+  if (hi < lo) hi = lo;
+}
+
+// Sum over the lanes below and including this one.
+__device__ __forceinline__ int sum_below(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// fwd, dx: tiles of TM rows, expert by expert, all columns of a row tile after
+// each other; XCD x (blocks x, x + 8, ..) has the x-th eighth.
+template <int TM, int TN>
+__device__ __forceinline__ Tile row_tile(const ExpertArgs& a, int lane) {
+  const int across = (a.cols + TN - 1) / TN;
+  auto tiles_of = [&](int e) {
+    int lo = 0, hi = 0;
+    if (e < a.experts) rows_of(a, e, lo, hi);
+    return (hi - lo + TM - 1) / TM;
+  };
+  int all = 0;
+  for (int e0 = 0; e0 < a.experts; e0 += kBatch) all += __shfl(sum_below(tiles_of(e0 + lane), lane), 63, 64);
+  const int64_t items = static_cast<int64_t>(all) * across;
+  const int x = blockIdx.x & 7;
+  const int64_t item = items * x / 8 + (blockIdx.x >> 3);
+  Tile t{0, 0, 0, 0, 0, false};
+  if (item >= items * (x + 1) / 8) return t;
+  int want = static_cast<int>(item / across);
+  t.c0 = static_cast<int>(item % across) * TN;
+  for (int e0 = 0; e0 < a.experts; e0 += kBatch) {
+    const int own = tiles_of(e0 + lane), upto = sum_below(own, lane);
+    const uint64_t past = __ballot(upto > want);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      t.e = e0 + l;
+      t.r0 = (want - __shfl(upto - own, l, 64)) * TM;
+      t.any = true;
+      break;
+    }
+    want -= __shfl(upto, 63, 64);
+  }
+  t.e = __builtin_amdgcn_readfirstlane(t.e);
+  t.r0 = __builtin_amdgcn_readfirstlane(t.r0);
+  t.c0 = __builtin_amdgcn_readfirstlane(t.c0);
+  rows_of(a, t.e, t.lo, t.hi);
+  t.lo = __builtin_amdgcn_readfirstlane(t.lo);
+  t.hi = __builtin_amdgcn_readfirstlane(t.hi);
+  return t;
+}
+
+// dw: an eighth of each expert's tiles to an XCD, in turn from another one, so
+// that unequal experts load them alike.
+template <int TM, int TN>
+__device__ __forceinline__ Tile matrix_tile(const ExpertArgs& a) {
+  const int across = (a.cols + TN - 1) / TN, tiles = (a.rows + TM - 1) / TM * across;
+  const int share = (tiles + 7) / 8;
+  const int i = blockIdx.x >> 3, e = i / share;
+  const int at = ((blockIdx.x + e) & 7) * share + i % share;
+  Tile t{e, 0, 0, at / across * TM, at % across * TN, e < a.experts && at < tiles};
+  if (t.any) {
+    rows_of(a, e, t.lo, t.hi);
+    t.lo = __builtin_amdgcn_readfirstlane(t.lo);
+    t.hi = __builtin_amdgcn_readfirstlane(t.hi);
+  }
+  return t;
+}
+
+// ---- operands
+//
+// LDS layout of a plane of one operand's stage.  Along the contraction: row r,
+// chunk c of BK / 8; 256 bytes (all banks) hold two rows (BK 64) or four (BK
+// 32), and the chunk index is XOR-ed so that the 16 rows that 16 lanes read
+// together fall into different 16-byte slots: rows 0-15 of the rows' operand,
+// and 0-7 and 16-23 of the columns' operand, in whose order the lanes take them.
+template <int BK, bool COLS>
+__device__ __forceinline__ int swizzle(int r) {
+  if constexpr (BK == 64) return COLS ? ((r >> 1) & 3) | (r >> 2 & 4) : (r >> 1) & 7;
+  else return COLS ? (r >> 2 & 1) | (r >> 3 & 2) : (r >> 2) & 3;
+}
+template <int BK, bool COLS>
+__device__ __forceinline__ int along_off(int r, int c) {
+  return r * (BK * 2) + ((c ^ swizzle<BK, COLS>(r)) << 4);
+}
+// Across: contraction row k, element p; the chunk index XOR-ed with 4 (k & 3),
+// so that four rows' 64 bytes fall into different quarters of the banks.
+template <int R>
+__device__ __forceinline__ int across_off(int k, int p) {
+  return k * (R * 2) + (((p >> 3) ^ (4 * (k & 3))) << 4) + (p & 7) * 2;
+}
+
+// fp32 -> three bf16 terms of eight elements.
+__device__ __forceinline__ void split8(const float* v, u32x4_t& h, u32x4_t& m, u32x4_t& l) {
+  h = narrow8(v);
+  float w[8], r[8];
+  widen8(h, w);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = v[e] - w[e];
+  m = narrow8(r);
+  widen8(m, w);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] -= w[e];
+  l = narrow8(r);
+}
+
+// What a block takes of one operand.
+struct Panel {
+  const uint8_t* base;   // along: the tile's first row (gathered: the matrix); across: the expert's first row
+  int64_t pitch;         // bytes from row to row
+  const int32_t* tokens; // gathered: of the expert's (across) or the tile's (along) rows
+  int src;               // gathered: rows of the matrix
+  int rows;              // along: rows of the tile; across: the contraction length
+  int cols;              // along: the contraction length; across: columns of the matrix
+  int c0;                // across: the tile's first column
+};
+
+// Loads of one operand: ROWS of the output (or columns, COLS) by BK, by NW waves.
+template <int ROWS, int NW, int BK, bool ACROSS, bool COLS, int DT, bool DMA>
+struct Side {
+  static constexpr int kES = DT == kBF16 ? 2 : 4;
+  static constexpr int kPlane = ROWS * BK * 2;                // bytes of a plane of a stage
+  static constexpr int kPlanes = DT == kBF16 ? 1 : 3;
+  static constexpr int kBytes = kPlane * kPlanes;
+  static constexpr int kPer = kPlane / 1024 / NW;             // 1 KiB pieces of a wave
+  static_assert(kPer * NW * 1024 == kPlane && !(DMA && DT != kBF16), "load split");
+  Panel p;
+  int row[kPer];          // along: the lane's row of the tile (of the matrix when gathered), or -1
+  int next[kPer];         // across, gathered: the matrix's rows of the next stage to be loaded
+  u32x4_t q[DMA ? 1 : kPer][DT == kBF16 ? 1 : 2];
+
+  // Place of the lane's piece u: row of the stage and 16-byte chunk in it.
+  static __device__ __forceinline__ void place(int u, int wave, int lane, int& r, int& c) {
+    constexpr int CPR = (ACROSS ? ROWS : BK) / 8;
+    const int slot = (wave + NW * u) * 64 + lane;
+    r = slot / CPR;
+    c = slot % CPR;
+    if constexpr (ACROSS) c ^= (4 * (r & 3)) & (CPR - 1);
+    else c ^= swizzle<BK, COLS>(r);
+  }
+  __device__ __forceinline__ int source(int r) const {   // the matrix's row of a gathered row
+    const int t = r < p.rows ? p.tokens[r] : -1;
+    return t < p.src ? t : -1;
+  }
+  __device__ __forceinline__ void plan(const Panel& panel, int wave, int lane) {
+    p = panel;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      int r, c;
+      place(u, wave, lane, r, c);
+      if constexpr (!ACROSS) row[u] = p.tokens ? source(r) : r < p.rows ? r : -1;
+    }
+    look(0, wave, lane);
+  }
+  // Across, gathered: finds the rows of the stage from contraction row k on.
+  __device__ __forceinline__ void look(int k, int wave, int lane) {
+    if constexpr (ACROSS) {
+      if (p.tokens) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          int r, c;
+          place(u, wave, lane, r, c);
+          next[u] = source(k + r);
+        }
+      }
+    }
+  }
+  // Starts the loads of the stage from contraction element k on.
+  __device__ __forceinline__ void load(int k, int wave, int lane, uint32_t lds) {
+    if constexpr (DMA) {
+      const bool gathered = p.tokens != nullptr;
+      const uint32_t pitch = static_cast<uint32_t>(p.pitch);
+      const uint8_t* base = p.base;
+      uint32_t bytes, soff = 0;
+      if (gathered) {
+        bytes = static_cast<uint32_t>((p.src - 1) * p.pitch) + static_cast<uint32_t>(p.cols) * 2;
+        if (!ACROSS) soff = static_cast<uint32_t>(k) * 2;
+      } else if (ACROSS) {
+        const int n = p.rows - k < BK ? p.rows - k : BK;
+        base += k * p.pitch + p.c0 * 2;
+        bytes = static_cast<uint32_t>(n - 1) * pitch + static_cast<uint32_t>(p.cols - p.c0) * 2;
+      } else {
+        const int n = p.rows < ROWS ? p.rows : ROWS;
+        bytes = static_cast<uint32_t>(n - 1) * pitch + static_cast<uint32_t>(p.cols) * 2;
+        soff = static_cast<uint32_t>(k) * 2;
+      }
+      const u32x4_t d = make_desc(base, bytes);
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        int r, c;
+        place(u, wave, lane, r, c);
+        uint32_t v;
+        if constexpr (ACROSS) {
+          if (gathered)
+            v = next[u] >= 0 && p.c0 + c * 8 < p.cols ? static_cast<uint32_t>(next[u]) * pitch + (p.c0 + c * 8) * 2 : kPast;
+          else
+            v = static_cast<uint32_t>(r) * pitch + c * 16;
+        } else {
+          v = row[u] >= 0 && k + c * 8 < p.cols ? static_cast<uint32_t>(row[u]) * pitch + c * 16 : kPast;
+        }
+        dma16(d, lds + (wave + NW * u) * 1024, v, soff);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        int r, c;
+        place(u, wave, lane, r, c);
+        int64_t at;
+        int n;                                   // elements of the chunk that are there
+        if constexpr (ACROSS) {
+          at = p.tokens ? next[u] : k + r < p.rows ? k + r : -1;
+          c = p.c0 + c * 8;
+        } else {
+          at = row[u];
+          c = k + c * 8;
+        }
+        n = at >= 0 ? p.cols - c : 0;
+        const uint8_t* from = p.base + (n > 0 ? at * p.pitch + static_cast<int64_t>(c) * kES : 0);
+#pragma unroll
+        for (int i = 0; i < (DT == kBF16 ? 1 : 2); ++i) q[u][i] = u32x4_t{0, 0, 0, 0};
+        if constexpr (DT == kBF16) {
+          const uint16_t* s = reinterpret_cast<const uint16_t*>(from);
+          if (n >= 8) {
+            q[u][0] = load16b(s);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < n) q[u][0][i / 2] |= static_cast<uint32_t>(glb(s)[i]) << (16 * (i & 1));
+          }
+        } else {
+          const uint32_t* s = reinterpret_cast<const uint32_t*>(from);
+          if (n >= 8) {
+            q[u][0] = load16b(s);
+            q[u][1] = load16b(s + 4);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < n) q[u][i / 4][i % 4] = glb(s)[i];
+          }
+        }
+      }
+    }
+  }
+  // Writes what load() brought into registers to the stage.
+  __device__ __forceinline__ void put(int wave, int lane, uint8_t* stage) {
+    if constexpr (!DMA) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        uint8_t* to = stage + (wave + NW * u) * 1024 + lane * 16;
+        if constexpr (DT == kBF16) {
+          *reinterpret_cast<u32x4_t*>(to) = q[u][0];
+        } else {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(q[u][i / 4][i % 4]);
+          u32x4_t h, m, l;
+          split8(v, h, m, l);
+          *reinterpret_cast<u32x4_t*>(to) = h;
+          *reinterpret_cast<u32x4_t*>(to + kPlane) = m;
+          *reinterpret_cast<u32x4_t*>(to + 2 * kPlane) = l;
+        }
+      }
+    }
+  }
+  // The matrix instruction's operand of 32 rows from row0 on, contraction
+  // elements 16 kk .. 16 kk + 15, from a plane.
+  static __device__ __forceinline__ bf16x8_t frag(const uint8_t* plane, int row0, int kk, int lane) {
+    if constexpr (ACROSS) {
+      const int g = lane >> 4, i = lane & 15, q = i & 3;
+      const int k = 16 * kk + 8 * (g >> 1) + (i >> 2);
+      const int col = row0 + (COLS ? 16 * (q & 1) + 8 * (g & 1) + 4 * (q >> 1) : 16 * (g & 1) + 4 * q);
+      const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(plane + across_off<ROWS>(k, col)));
+      const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(plane + across_off<ROWS>(k + 4, col)));
+      return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const int l = lane & 31;
+      const int r = row0 + (COLS ? 16 * (l >> 2 & 1) + 4 * (l >> 3) + (l & 3) : l);
+      return *reinterpret_cast<const bf16x8_t*>(plane + along_off<BK, COLS>(r, 2 * kk + (lane >> 5)));
+    }
+  }
+};
+
+// ---- output: 16 consecutive columns of a row
+template <class T>
+__device__ __forceinline__ void put16(T* o, const float* v, int n, bool accumulate) {
+  if (n >= 16) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = v[8 * h + i];
+      if (accumulate) {
+        float old[8];
+        load8(o + 8 * h, old);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] += old[i];
+      }
+      store8(o + 8 * h, w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) store1(o + i, accumulate ? load1(o + i) + v[i] : v[i]);
+  }
+}
+
+// TM x TN tiles by WM x WN waves, two stages of BK.
+template <int OP, int DT, bool DMA, class T, int TM, int TN, int WM, int WN, int BK>
+__global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
+  constexpr int NW = WM * WN;
+  using Rows = Side<TM, NW, BK, OP == kExpertDw, false, DT, DMA>;
+  using Cols = Side<TN, NW, BK, OP != kExpertFwd, true, DT, DMA>;
+  constexpr int kStage = Rows::kBytes + Cols::kBytes, PL = Rows::kPlanes;
+  constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  const uint32_t lds = lds_addr(smem);
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  Tile tile;
+  if constexpr (OP == kExpertDw) tile = matrix_tile<TM, TN>(a);
+  else tile = row_tile<TM, TN>(a, lane);
+  if (!tile.any) return;
+  const int depth = OP == kExpertDw ? tile.hi - tile.lo : a.depth;
+  const int64_t es = DT == kBF16 ? 2 : 4;
+  const uint8_t* rbase = static_cast<const uint8_t*>(a.r);
+  const uint8_t* cbase = static_cast<const uint8_t*>(a.c);
+  Rows rows;
+  Cols cols;
+  if constexpr (OP == kExpertDw) {
+    rows.plan({rbase + tile.lo * a.ldr * es, a.ldr * es, nullptr, 0, depth, a.rows, tile.r0}, wave, lane);
+    cols.plan({a.tokens ? cbase : cbase + tile.lo * a.ldc * es, a.ldc * es,
+               a.tokens ? a.tokens + tile.lo : nullptr, a.src, depth, a.cols, tile.c0}, wave, lane);
+  } else {
+    const int first = tile.lo + tile.r0;
+    rows.plan({a.tokens ? rbase : rbase + first * a.ldr * es, a.ldr * es,
+               a.tokens ? a.tokens + first : nullptr, a.src, tile.hi - first, depth, 0}, wave, lane);
+    const uint8_t* w = cbase + tile.e * a.wstride * es;
+    if constexpr (OP == kExpertFwd)
+      cols.plan({w + tile.c0 * a.ldc * es, a.ldc * es, nullptr, 0, a.cols - tile.c0, depth, 0}, wave, lane);
+    else
+      cols.plan({w, a.ldc * es, nullptr, 0, depth, a.cols, tile.c0}, wave, lane);
+  }
+
+  f32x16_t acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = f32x16_t{};
+
+  const int stages = (depth + BK - 1) / BK;
+  auto start = [&](int k, int slot) {
+    rows.load(k * BK, wave, lane, lds + slot * kStage);
+    cols.load(k * BK, wave, lane, lds + slot * kStage + Rows::kBytes);
+    if (k + 1 < stages) {
+      rows.look((k + 1) * BK, wave, lane);
+      cols.look((k + 1) * BK, wave, lane);
+    }
+  };
+  auto land = [&](int slot) {
+    if constexpr (!DMA) {
+      rows.put(wave, lane, smem + slot * kStage);
+      cols.put(wave, lane, smem + slot * kStage + Rows::kBytes);
+    }
+  };
+  if (stages) {
+    start(0, 0);
+    land(0);
+  }
+  for (int k = 0; k < stages; ++k) {
+    if constexpr (DMA) wait_vm<0>();
+    lds_barrier();
+    const bool more = k + 1 < stages;
+    if (more) start(k + 1, (k + 1) & 1);
+    const uint8_t* sr = smem + (k & 1) * kStage;
+    const uint8_t* sc = sr + Rows::kBytes;
+#pragma unroll
+    for (int kk = 0; kk < BK / 16; ++kk) {
+      bf16x8_t fc[PL][FN], fr[PL][FM];
+#pragma unroll
+      for (int p = 0; p < PL; ++p) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+          fc[p][i] = Cols::frag(sc + p * Cols::kPlane, (wn * FN + i) * 32, kk, lane);
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+          fr[p][j] = Rows::frag(sr + p * Rows::kPlane, (wm * FM + j) * 32, kk, lane);
+      }
+      // the terms' products, the smallest first
+#pragma unroll
+      for (int sum = PL == 1 ? 0 : 2; sum >= 0; --sum)
+#pragma unroll
+        for (int p = 0; p < PL; ++p) {
+          const int o = sum - p;
+          if (o < 0 || o >= PL) continue;
+#pragma unroll
+          for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[p][i], fr[o][j], acc[i][j], 0, 0, 0);
+        }
+    }
+    if (more) land((k + 1) & 1);
+  }
+
+  const int most = OP == kExpertDw ? a.rows : tile.hi - tile.lo;
+  T* out = static_cast<T*>(a.out) + (OP == kExpertDw ? tile.e * a.ostride : tile.lo * a.ldo);
+  if (OP == kExpertDw && a.accumulate && depth == 0) return;
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int r = tile.r0 + (wm * FM + j) * 32 + (lane & 31);
+    if (r >= most) continue;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      const int c = tile.c0 + (wn * FN + i) * 32 + 16 * (lane >> 5);
+      float v[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) v[q] = acc[i][j][q];
+      if (c < a.cols) put16(out + r * a.ldo + c, v, a.cols - c, OP == kExpertDw && a.accumulate);
+    }
+  }
+}
+
+template <int OP, int DT, bool DMA, class T, int TM, int TN, int WM, int WN, int BK>
+hipError_t launch_tiles(const ExpertArgs& a, hipStream_t s) {
+  constexpr int NW = WM * WN;
+  using Rows = Side<TM, NW, BK, OP == kExpertDw, false, DT, DMA>;
+  using Cols = Side<TN, NW, BK, OP != kExpertFwd, true, DT, DMA>;
+  constexpr int lds = 2 * (Rows::kBytes + Cols::kBytes);
+  static_assert(lds <= 160 * 1024, "LDS");
+  auto* k = &k_experts<OP, DT, DMA, T, TM, TN, WM, WN, BK>;
+  // the LDS limit is raised once per device
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(raised.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
+  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(expert_blocks(a, OP, TM, TN))), dim3(64 * NW), lds, s, a);
+  return hipGetLastError();
+}
+
+template <int OP, class T>
+hipError_t launch_op(const ExpertArgs& a, int dt, bool aligned, hipStream_t s) {
+  if (dt == kF32) return launch_tiles<OP, kF32, false, T, 128, 128, 2, 2, 32>(a, s);
+  if (!aligned) return launch_tiles<OP, kBF16, false, T, 128, 128, 2, 2, 64>(a, s);
+  return launch_tiles<OP, kBF16, true, T, 256, 256, 2, 4, 64>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_experts(const ExpertArgs& a, int op, int dt, int odt, bool aligned, hipStream_t s) {
+  auto with = [&](auto z) {
+    using T = decltype(z);
+    if (op == kExpertFwd) return launch_op<kExpertFwd, T>(a, dt, aligned, s);
+    if (op == kExpertDx) return launch_op<kExpertDx, T>(a, dt, aligned, s);
+    return launch_op<kExpertDw, T>(a, dt, aligned, s);
+  };
+  return odt == kBF16 ? with(uint16_t{}) : with(float{});
+}
+
+}  // namespace muon

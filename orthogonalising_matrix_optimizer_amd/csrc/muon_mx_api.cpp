@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/muon.h"
+#include "muon_check.h"
 #include "muon_common.h"
 #include "muon_mx.h"
 #include "muon_span.h"
@@ -19,7 +20,6 @@ using namespace muon;
 
 namespace {
 
-constexpr int64_t kMaxRows = int64_t(1) << 30;
 // where an fp32 sum of equal terms stops growing; it also keeps the parts of a
 // split contraction (kMinChunk code tiles at least) to 2^13
 constexpr int64_t kMaxCols = int64_t(1) << 24;
@@ -27,22 +27,8 @@ constexpr int64_t kMaxCols = int64_t(1) << 24;
 constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;
 constexpr int64_t kMaxQuantBlocks = (int64_t(1) << 22) - 1;
 
-int esize(int dt) { return dt == MUON_BF16 ? 2 : 4; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 bool shape_ok(int64_t rows, int64_t cols) {
   return rows >= 0 && cols >= 0 && rows <= kMaxRows && cols <= kMaxCols;
-}
-
-// A matrix of any size, zero included; rows need only element alignment.
-int check_dense(const muon_mat& m) {
-  if (m.dtype != MUON_BF16 && m.dtype != MUON_F32) return MUON_E_DTYPE;
-  if (m.rows < 0 || m.cols < 0 || m.rows > kMaxRows || m.cols > kMaxRows) return MUON_E_SHAPE;
-  if (m.rows == 0 || m.cols == 0) return MUON_OK;
-  if (m.ld < m.cols || m.ld > (int64_t(1) << 40)) return MUON_E_SHAPE;
-  if (!m.ptr) return MUON_E_NULL;
-  if (reinterpret_cast<uintptr_t>(m.ptr) % esize(m.dtype)) return MUON_E_ALIGN;
-  return MUON_OK;
 }
 
 int check_mx(const muon_mx& m) {
@@ -52,19 +38,6 @@ int check_mx(const muon_mx& m) {
   if (reinterpret_cast<uintptr_t>(m.codes) % 16 || reinterpret_cast<uintptr_t>(m.scales) % 16)
     return MUON_E_ALIGN;
   return MUON_OK;
-}
-
-void add_span(std::vector<Span>& v, const void* p, size_t bytes, bool write) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  if (p && bytes) v.push_back({a, a + bytes, bytes, bytes, write});
-}
-
-void add_span(std::vector<Span>& v, const muon_mat& m, bool write) {
-  if (m.rows == 0 || m.cols == 0) return;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(m.ptr);
-  const size_t es = esize(m.dtype);
-  v.push_back({a, a + (size_t(m.rows - 1) * m.ld + m.cols) * es, size_t(m.ld) * es,
-               size_t(m.cols) * es, write});
 }
 
 void add_span(std::vector<Span>& v, const muon_mx& m, bool write) {

@@ -1,0 +1,148 @@
+// Kernel arguments and launchers of the embedding table and the expert layers
+// (see include/muon.h for the operators).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "muon_common.h"
+
+namespace muon {
+
+// ---- stable counting sort (muon_sort.hip)
+//
+// Sorts positions 0 .. n-1 by an integer key, by position among equal keys, in
+// passes of kSortBits (or kSortWide) bits, the lowest first.
+constexpr int kSortThreads = 1024;
+constexpr int kSortBits = 8, kSortWide = 10;
+// blocks up to which each counts all keys itself (one launch a pass)
+constexpr int kSortSelf = 32;
+
+// Bits of the keys 0 .. limit, and how they are sorted.
+inline int key_bits(int64_t limit) {
+  int b = 1;
+  while (limit >> b) ++b;
+  return b;
+}
+inline int sort_bits(int bits) {
+  return bits <= kSortBits || (bits > kSortWide && bits <= 2 * kSortBits) ? kSortBits : kSortWide;
+}
+// positions a thread takes: more where the blocks' counts would be many
+inline int sort_each(int64_t n) { return n <= (int64_t(1) << 20) ? 1 : 4; }
+
+struct SortArgs {
+  const void* ids;      // n integers of id_bytes (of the first pass)
+  int32_t id_bytes;
+  int32_t n;
+  int32_t limit;        // keys are 0 .. limit: ids outside 0 .. limit-1 have key `limit`
+  int32_t passes;
+  int32_t* key[2];      // keys and positions between passes; the last pass writes
+  int32_t* pos[2];      // into key[passes & 1 ^ 1] and pos[...] where they are not null
+  int32_t* counts;      // blocks x bins, for more than kSortSelf blocks
+  // where the sorted positions are a plan's slots (one pass): its arrays, or null
+  int32_t* offsets;
+  int32_t* tokens;
+  int32_t* place;
+  int32_t k;
+};
+hipError_t launch_sort(const SortArgs& a, hipStream_t s);
+
+// ---- routing (muon_route.hip)
+struct RouteArgs {
+  const void* logits;
+  int64_t ld;
+  float* gates;
+  int32_t* chosen;
+  int32_t tokens, experts, k, normalize;
+};
+// sort: of the slots of a.chosen
+hipError_t launch_route(const RouteArgs& a, const SortArgs& sort, int dt, hipStream_t s);
+
+struct RouteGradArgs {
+  const float* dgates;
+  const void* logits;
+  const float* gates;
+  const int32_t* chosen;
+  void* dlogits;
+  int64_t ld, ldd;
+  int32_t tokens, experts, k, normalize;
+};
+hipError_t launch_route_grad(const RouteGradArgs& a, int dt, int ddt, hipStream_t s);
+
+// ---- rows moved by index (muon_rows.hip)
+struct CombineArgs {
+  const void* y;          // slots' rows
+  const void* dout;       // tokens' rows (gradient)
+  const float* gates;     // or null: ones
+  const int32_t* place;
+  void* out;              // forward: tokens' rows; gradient: slots' rows, or null
+  float* dgates;          // or null
+  int64_t ldy, ldd, ldo;
+  int32_t tokens, k, slots, cols;
+};
+hipError_t launch_combine(const CombineArgs& a, int dt, int odt, hipStream_t s);
+hipError_t launch_combine_grad(const CombineArgs& a, int dt, hipStream_t s);
+
+struct EmbedArgs {
+  const void* ids;
+  const void* w;
+  void* out;
+  int64_t ldw, ldo, rows;   // rows of w
+  float scale;
+  int32_t id_bytes, tokens, cols;
+};
+hipError_t launch_embedding(const EmbedArgs& a, int dt, hipStream_t s);
+
+// Sums of dy's rows over runs of equal sorted keys.  A block takes kEmbedRun
+// consecutive sorted positions; a run inside it is written at once, a run that
+// crosses its edges goes to `part` (two rows a block) and is joined by a second launch.
+constexpr int kEmbedZeroRows = 64;   // rows of dw that a block looks over for zeroing
+struct EmbedGradArgs {
+  const void* dy;
+  const int32_t* key;     // sorted ids (the last ones `rows`: no gradient)
+  const int32_t* pos;     // their tokens
+  void* dw;
+  float* part;            // chunks x 2 x cols
+  int64_t ldy, ldw;
+  float scale;
+  int32_t tokens, rows, cols, accumulate;
+  int32_t chunk, chunks;  // sorted positions a block sums, blocks that sum
+};
+hipError_t launch_embedding_grad(const EmbedGradArgs& a, int dt, int odt, hipStream_t s);
+
+// ---- experts' products (muon_experts.hip)
+enum ExpertOp : int32_t { kExpertFwd = 0, kExpertDx = 1, kExpertDw = 2 };
+struct ExpertArgs {
+  const void* r;            // operand of the output's rows: x, dy, dy
+  const void* c;            // operand of the output's columns: w, w, x
+  void* out;
+  const int32_t* offsets;
+  const int32_t* tokens;    // gathered x: the rows' tokens, else null
+  int64_t ldr, ldc, ldo;    // elements
+  int64_t wstride, ostride; // elements between experts' matrices: of c, of out (dw)
+  int32_t experts, slots;
+  int32_t rows, cols;       // dw: rows of a matrix; columns of the output
+  int32_t depth;            // contraction length (fwd, dx)
+  int32_t src;              // rows of x when gathered
+  int32_t accumulate;       // dw
+};
+// Blocks of a launch with tm x tn tiles.  The rows' tiles are known to the device
+// alone: a full tile for every tm slots and a part of one an expert at most.
+inline int64_t expert_blocks(const ExpertArgs& a, int op, int tm, int tn) {
+  const int64_t across = (int64_t(a.cols) + tn - 1) / tn;
+  if (op == kExpertDw) {
+    const int64_t tiles = (int64_t(a.rows) + tm - 1) / tm * across;
+    return 8 * a.experts * ((tiles + 7) / 8);
+  }
+  const int64_t tiles = a.slots / tm + (a.experts < a.slots ? a.experts : a.slots);
+  return 8 * ((tiles * across + 7) / 8);
+}
+// Bytes that a buffer's descriptor spans at most: an offset from here on reads as
+// zeros and, with the offset along a row added, stays below 2^32.
+constexpr uint32_t kExpertSpan = 0xf0000000u;
+// Longest rows (elements) that are loaded straight to LDS: 256 of them are in a span.
+constexpr int64_t kExpertPitch = int64_t(1) << 22;
+// aligned: every row of the operands starts at 16 bytes (and holds whole ones along
+// the contraction), so that loads go straight to LDS
+hipError_t launch_experts(const ExpertArgs& a, int op, int dt, int odt, bool aligned, hipStream_t s);
+
+}  // namespace muon
