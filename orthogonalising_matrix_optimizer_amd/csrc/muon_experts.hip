@@ -182,19 +182,24 @@ struct Panel {
   int c0;                // across: the tile's first column
 };
 
-// Loads of one operand: ROWS of the output (or columns, COLS) by BK, by NW waves.
+// One operand of a block's stages: ROWS rows of the output (or columns, COLS) by BK
+// contraction elements, loaded by NW waves.  A wave's share is kPer pieces of 1
+// KiB, in which a lane has 16 bytes of LDS: eight elements.
 template <int ROWS, int NW, int BK, bool ACROSS, bool COLS, int DT, bool DMA>
 struct Side {
   static constexpr int kES = DT == kBF16 ? 2 : 4;
   static constexpr int kPlane = ROWS * BK * 2;                // bytes of a plane of a stage
   static constexpr int kPlanes = DT == kBF16 ? 1 : 3;
   static constexpr int kBytes = kPlane * kPlanes;
-  static constexpr int kPer = kPlane / 1024 / NW;             // 1 KiB pieces of a wave
+  static constexpr int kPer = kPlane / 1024 / NW;
+  static constexpr int kReads = ACROSS ? 2 : 1;               // LDS reads of an operand
   static_assert(kPer * NW * 1024 == kPlane && !(DMA && DT != kBF16), "load split");
   Panel p;
-  int row[kPer];          // along: the lane's row of the tile (of the matrix when gathered), or -1
-  int next[kPer];         // across, gathered: the matrix's rows of the next stage to be loaded
-  u32x4_t q[DMA ? 1 : kPer][DT == kBF16 ? 1 : 2];
+  // Along: the lane's rows of the tile (of the matrix when gathered), or -1; for
+  // LDS-DMA their offsets.  Across, gathered: the matrix's rows of the next stage.
+  int row[kPer];
+  u32x4_t q[DMA ? 1 : kPer][DT == kBF16 ? 1 : 2];             // loaded, not yet in LDS
+  u32x4_t desc;                                               // LDS-DMA, along and gathered: the buffer
 
   // Place of the lane's piece u: row of the stage and 16-byte chunk in it.
   static __device__ __forceinline__ void place(int u, int wave, int lane, int& r, int& c) {
@@ -211,61 +216,60 @@ struct Side {
   }
   __device__ __forceinline__ void plan(const Panel& panel, int wave, int lane) {
     p = panel;
+    if constexpr (DMA) {
+      const int n = p.tokens ? p.src : p.rows < ROWS ? p.rows : ROWS;
+      const int64_t bytes = (n - 1) * p.pitch + int64_t(p.cols) * 2;
+      desc = make_desc(p.base, static_cast<uint32_t>(bytes));
+    }
+    if constexpr (!ACROSS) {
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      int r, c;
-      place(u, wave, lane, r, c);
-      if constexpr (!ACROSS) row[u] = p.tokens ? source(r) : r < p.rows ? r : -1;
+      for (int u = 0; u < kPer; ++u) {
+        int r, c;
+        place(u, wave, lane, r, c);
+        row[u] = p.tokens ? source(r) : r < p.rows ? r : -1;
+        if constexpr (DMA)
+          row[u] = static_cast<int>(row[u] < 0 ? kPast : static_cast<uint32_t>(row[u]) * static_cast<uint32_t>(p.pitch) + c * 16);
+      }
     }
     look(0, wave, lane);
   }
   // Across, gathered: finds the rows of the stage from contraction row k on.
   __device__ __forceinline__ void look(int k, int wave, int lane) {
     if constexpr (ACROSS) {
-      if (p.tokens) {
+      if (p.tokens && k < p.rows) {
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
           int r, c;
           place(u, wave, lane, r, c);
-          next[u] = source(k + r);
+          row[u] = source(k + r);
         }
       }
     }
   }
-  // Starts the loads of the stage from contraction element k on.
+  // Starts the loads of the stage from contraction element k on; with LDS-DMA to
+  // `lds`, else into registers.
   __device__ __forceinline__ void load(int k, int wave, int lane, uint32_t lds) {
     if constexpr (DMA) {
-      const bool gathered = p.tokens != nullptr;
       const uint32_t pitch = static_cast<uint32_t>(p.pitch);
-      const uint8_t* base = p.base;
-      uint32_t bytes, soff = 0;
-      if (gathered) {
-        bytes = static_cast<uint32_t>((p.src - 1) * p.pitch) + static_cast<uint32_t>(p.cols) * 2;
-        if (!ACROSS) soff = static_cast<uint32_t>(k) * 2;
-      } else if (ACROSS) {
-        const int n = p.rows - k < BK ? p.rows - k : BK;
-        base += k * p.pitch + p.c0 * 2;
-        bytes = static_cast<uint32_t>(n - 1) * pitch + static_cast<uint32_t>(p.cols - p.c0) * 2;
-      } else {
-        const int n = p.rows < ROWS ? p.rows : ROWS;
-        bytes = static_cast<uint32_t>(n - 1) * pitch + static_cast<uint32_t>(p.cols) * 2;
-        soff = static_cast<uint32_t>(k) * 2;
-      }
-      const u32x4_t d = make_desc(base, bytes);
+      auto issue = [&](const u32x4_t& d, uint32_t soff, auto&& offset) {
 #pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        int r, c;
-        place(u, wave, lane, r, c);
-        uint32_t v;
-        if constexpr (ACROSS) {
-          if (gathered)
-            v = next[u] >= 0 && p.c0 + c * 8 < p.cols ? static_cast<uint32_t>(next[u]) * pitch + (p.c0 + c * 8) * 2 : kPast;
-          else
-            v = static_cast<uint32_t>(r) * pitch + c * 16;
-        } else {
-          v = row[u] >= 0 && k + c * 8 < p.cols ? static_cast<uint32_t>(row[u]) * pitch + c * 16 : kPast;
+        for (int u = 0; u < kPer; ++u) {
+          int r, c;
+          place(u, wave, lane, r, c);
+          dma16(d, lds + (wave + NW * u) * 1024, offset(u, r, c), soff);
         }
-        dma16(d, lds + (wave + NW * u) * 1024, v, soff);
+      };
+      if constexpr (!ACROSS) {
+        const int left = p.cols - k;
+        issue(desc, static_cast<uint32_t>(k) * 2, [&](int u, int, int c) { return c * 8 < left ? static_cast<uint32_t>(row[u]) : kPast; });
+      } else if (p.tokens) {
+        issue(desc, 0, [&](int u, int, int c) {
+          return row[u] >= 0 && p.c0 + c * 8 < p.cols ? static_cast<uint32_t>(row[u]) * pitch + (p.c0 + c * 8) * 2 : kPast;
+        });
+      } else {
+        const int n = p.rows - k < BK ? p.rows - k : BK;
+        issue(make_desc(p.base + k * p.pitch + p.c0 * 2, static_cast<uint32_t>(n - 1) * pitch + static_cast<uint32_t>(p.cols - p.c0) * 2),
+              0, [&](int, int r, int c) { return static_cast<uint32_t>(r) * pitch + c * 16; });
       }
     } else {
 #pragma unroll
@@ -273,15 +277,14 @@ struct Side {
         int r, c;
         place(u, wave, lane, r, c);
         int64_t at;
-        int n;                                   // elements of the chunk that are there
         if constexpr (ACROSS) {
-          at = p.tokens ? next[u] : k + r < p.rows ? k + r : -1;
+          at = p.tokens ? row[u] : k + r < p.rows ? k + r : -1;
           c = p.c0 + c * 8;
         } else {
           at = row[u];
           c = k + c * 8;
         }
-        n = at >= 0 ? p.cols - c : 0;
+        const int n = at >= 0 ? p.cols - c : 0;      // elements of the chunk that are there
         const uint8_t* from = p.base + (n > 0 ? at * p.pitch + static_cast<int64_t>(c) * kES : 0);
 #pragma unroll
         for (int i = 0; i < (DT == kBF16 ? 1 : 2); ++i) q[u][i] = u32x4_t{0, 0, 0, 0};
@@ -308,7 +311,7 @@ struct Side {
       }
     }
   }
-  // Writes what load() brought into registers to the stage.
+  // Writes what load() brought into registers to a stage in LDS.
   __device__ __forceinline__ void put(int wave, int lane, uint8_t* stage) {
     if constexpr (!DMA) {
 #pragma unroll
@@ -371,8 +374,26 @@ __device__ __forceinline__ void put16(T* o, const float* v, int n, bool accumula
   }
 }
 
-// TM x TN tiles by WM x WN waves, two stages of BK.
-template <int OP, int DT, bool DMA, class T, int TM, int TN, int WM, int WN, int BK>
+// Puts a step's LDS reads between the products of the step before, two to one of
+// them: left alone, the compiler puts them right before their use.
+template <int READS, int PRODUCTS>
+__device__ __forceinline__ void interleave() {
+  if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, READS < 2 ? 1 : 2, 0);
+  if constexpr (PRODUCTS > 0) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    interleave<(READS > 2 ? READS - 2 : 0), PRODUCTS - 1>();
+  } else if constexpr (READS > 2) {
+    interleave<READS - 2, 0>();
+  }
+}
+
+// TM x TN tiles by WM x WN waves, a ring of NST stages of BK.
+//
+// The operands of a step of 16 are read from LDS while the step before is
+// multiplied.  Before the last step of a stage the block meets: then its stage has
+// been read by all (its slot takes the stage NST further on), the next one is
+// there, and its first operands are read beside the last step's products.
+template <int OP, int DT, bool DMA, class T, int TM, int TN, int WM, int WN, int BK, int NST>
 __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
   constexpr int NW = WM * WN;
   using Rows = Side<TM, NW, BK, OP == kExpertDw, false, DT, DMA>;
@@ -417,58 +438,83 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
     for (int j = 0; j < FM; ++j) acc[i][j] = f32x16_t{};
 
   const int stages = (depth + BK - 1) / BK;
-  auto start = [&](int k, int slot) {
+  constexpr int PER = Rows::kPer + Cols::kPer, KK = BK / 16;
+  static_assert(KK % 2 == 0 && (DMA || NST == 2), "steps and stages");
+  auto load = [&](int k, int slot) {     // LDS-DMA: all the way; else into registers
+    if (k >= stages) return;
     rows.load(k * BK, wave, lane, lds + slot * kStage);
     cols.load(k * BK, wave, lane, lds + slot * kStage + Rows::kBytes);
-    if (k + 1 < stages) {
-      rows.look((k + 1) * BK, wave, lane);
-      cols.look((k + 1) * BK, wave, lane);
-    }
+    rows.look((k + 1) * BK, wave, lane);
+    cols.look((k + 1) * BK, wave, lane);
   };
-  auto land = [&](int slot) {
-    if constexpr (!DMA) {
-      rows.put(wave, lane, smem + slot * kStage);
-      cols.put(wave, lane, smem + slot * kStage + Rows::kBytes);
-    }
+  auto put = [&](int k, int slot) {
+    if (DMA || k >= stages) return;
+    rows.put(wave, lane, smem + slot * kStage);
+    cols.put(wave, lane, smem + slot * kStage + Rows::kBytes);
   };
-  if (stages) {
-    start(0, 0);
-    land(0);
-  }
-  for (int k = 0; k < stages; ++k) {
-    if constexpr (DMA) wait_vm<0>();
-    lds_barrier();
-    const bool more = k + 1 < stages;
-    if (more) start(k + 1, (k + 1) & 1);
-    const uint8_t* sr = smem + (k & 1) * kStage;
+  struct Frags { bf16x8_t c[PL][FN], r[PL][FM]; } f[2];
+  auto read = [&](Frags& g, int slot, int kk) {
+    const uint8_t* sr = smem + slot * kStage;
     const uint8_t* sc = sr + Rows::kBytes;
 #pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk) {
-      bf16x8_t fc[PL][FN], fr[PL][FM];
+    for (int p = 0; p < PL; ++p) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i) g.c[p][i] = Cols::frag(sc + p * Cols::kPlane, (wn * FN + i) * 32, kk, lane);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) g.r[p][j] = Rows::frag(sr + p * Rows::kPlane, (wm * FM + j) * 32, kk, lane);
+    }
+  };
+  auto multiply = [&](const Frags& g) {   // the terms' products, the smallest first
+#pragma unroll
+    for (int sum = PL == 1 ? 0 : 2; sum >= 0; --sum)
 #pragma unroll
       for (int p = 0; p < PL; ++p) {
+        const int o = sum - p;
+        if (o < 0 || o >= PL) continue;
 #pragma unroll
         for (int i = 0; i < FN; ++i)
-          fc[p][i] = Cols::frag(sc + p * Cols::kPlane, (wn * FN + i) * 32, kk, lane);
 #pragma unroll
-        for (int j = 0; j < FM; ++j)
-          fr[p][j] = Rows::frag(sr + p * Rows::kPlane, (wm * FM + j) * 32, kk, lane);
+          for (int j = 0; j < FM; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g.c[p][i], g.r[o][j], acc[i][j], 0, 0, 0);
       }
-      // the terms' products, the smallest first
+  };
+  if (stages) {
+    if constexpr (DMA) {
 #pragma unroll
-      for (int sum = PL == 1 ? 0 : 2; sum >= 0; --sum)
-#pragma unroll
-        for (int p = 0; p < PL; ++p) {
-          const int o = sum - p;
-          if (o < 0 || o >= PL) continue;
-#pragma unroll
-          for (int i = 0; i < FN; ++i)
-#pragma unroll
-            for (int j = 0; j < FM; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[p][i], fr[o][j], acc[i][j], 0, 0, 0);
-        }
+      for (int k = 0; k < NST; ++k) load(k, k);
+      wait_ahead<NST - 1, PER>(stages - 1);
+    } else {
+      load(0, 0);
+      put(0, 0);
+      load(1, 1);
+      put(1, 1);
+      load(2, 0);
     }
-    if (more) land((k + 1) & 1);
+    lds_barrier();
+    read(f[0], 0, 0);
+  }
+  constexpr int READS = PL * (FN * Cols::kReads + FM * Rows::kReads), PRODUCTS = (PL == 1 ? 1 : 6) * FN * FM;
+  int slot = 0;
+  for (int k = 0; k < stages; ++k) {
+#pragma unroll
+    for (int kk = 0; kk + 1 < KK; ++kk) {
+      read(f[(kk + 1) & 1], slot, kk + 1);
+      multiply(f[kk & 1]);
+      interleave<READS, PRODUCTS>();
+    }
+    // (behind the last stage this reads operands that are not used: a branch around
+    // the products would double the accumulators)
+    const int free = slot;
+    slot = slot + 1 == NST ? 0 : slot + 1;
+    if constexpr (DMA) wait_ahead<NST - 2, PER>(stages - 2 - k);
+    lds_barrier();
+    put(k + 2, free);
+    load(DMA ? k + NST : k + 3, free);
+    __builtin_amdgcn_sched_barrier(0);
+    read(f[0], slot, 0);
+    multiply(f[1]);
+    interleave<READS, PRODUCTS>();
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   const int most = OP == kExpertDw ? a.rows : tile.hi - tile.lo;
@@ -489,14 +535,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
   }
 }
 
-template <int OP, int DT, bool DMA, class T, int TM, int TN, int WM, int WN, int BK>
+template <int OP, int DT, bool DMA, class T, int TM, int TN, int WM, int WN, int BK, int NST>
 hipError_t launch_tiles(const ExpertArgs& a, hipStream_t s) {
   constexpr int NW = WM * WN;
   using Rows = Side<TM, NW, BK, OP == kExpertDw, false, DT, DMA>;
   using Cols = Side<TN, NW, BK, OP != kExpertFwd, true, DT, DMA>;
-  constexpr int lds = 2 * (Rows::kBytes + Cols::kBytes);
+  constexpr int lds = NST * (Rows::kBytes + Cols::kBytes);
   static_assert(lds <= 160 * 1024, "LDS");
-  auto* k = &k_experts<OP, DT, DMA, T, TM, TN, WM, WN, BK>;
+  auto* k = &k_experts<OP, DT, DMA, T, TM, TN, WM, WN, BK, NST>;
   // the LDS limit is raised once per device
   static std::atomic<uint64_t> raised{0};
   int dev = 0;
@@ -514,9 +560,9 @@ hipError_t launch_tiles(const ExpertArgs& a, hipStream_t s) {
 
 template <int OP, class T>
 hipError_t launch_op(const ExpertArgs& a, int dt, bool aligned, hipStream_t s) {
-  if (dt == kF32) return launch_tiles<OP, kF32, false, T, 128, 128, 2, 2, 32>(a, s);
-  if (!aligned) return launch_tiles<OP, kBF16, false, T, 128, 128, 2, 2, 64>(a, s);
-  return launch_tiles<OP, kBF16, true, T, 256, 256, 2, 4, 64>(a, s);
+  if (dt == kF32) return launch_tiles<OP, kF32, false, T, 128, 128, 2, 2, 32, 2>(a, s);
+  if (!aligned) return launch_tiles<OP, kBF16, false, T, 128, 128, 2, 2, 64, 2>(a, s);
+  return launch_tiles<OP, kBF16, true, T, 256, 256, 4, 2, 64, 2>(a, s);
 }
 
 }  // namespace
