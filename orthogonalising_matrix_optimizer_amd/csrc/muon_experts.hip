@@ -118,7 +118,9 @@ __device__ __forceinline__ Tile row_tile(const ExpertArgs& a, int lane) {
 }
 
 // dw: an eighth of each expert's tiles to an XCD, in turn from another one, so
-// that unequal experts load them alike.
+// that unequal experts load them alike.  (Whole experts on one XCD, the largest
+// first, read less but were slower: 49146 rows of 64 experts, 2048 x 1408, 530 against
+// 499 us.)
 template <int TM, int TN>
 __device__ __forceinline__ Tile matrix_tile(const ExpertArgs& a) {
   const int across = (a.cols + TN - 1) / TN, tiles = (a.rows + TM - 1) / TM * across;
@@ -150,11 +152,16 @@ template <int BK, bool COLS>
 __device__ __forceinline__ int along_off(int r, int c) {
   return r * (BK * 2) + ((c ^ swizzle<BK, COLS>(r)) << 4);
 }
-// Across: contraction row k, element p; the chunk index XOR-ed with 4 (k & 3),
-// so that four rows' 64 bytes fall into different quarters of the banks.
+// Across: contraction row k, element p; the chunk index XOR-ed so that the 64 bytes
+// of four rows that 32 lanes read together fall into different quarters of the
+// banks (with 64 elements a row, two rows share the 256 bytes).
+template <int R>
+__device__ __forceinline__ int turn(int k) {
+  return R == 64 ? 4 * (k >> 1 & 1) : 4 * (k & 3);
+}
 template <int R>
 __device__ __forceinline__ int across_off(int k, int p) {
-  return k * (R * 2) + (((p >> 3) ^ (4 * (k & 3))) << 4) + (p & 7) * 2;
+  return k * (R * 2) + (((p >> 3) ^ turn<R>(k)) << 4) + (p & 7) * 2;
 }
 
 // fp32 -> three bf16 terms of eight elements.
@@ -207,7 +214,7 @@ struct Side {
     const int slot = (wave + NW * u) * 64 + lane;
     r = slot / CPR;
     c = slot % CPR;
-    if constexpr (ACROSS) c ^= (4 * (r & 3)) & (CPR - 1);
+    if constexpr (ACROSS) c ^= turn<ROWS>(r);
     else c ^= swizzle<BK, COLS>(r);
   }
   __device__ __forceinline__ int source(int r) const {   // the matrix's row of a gathered row
@@ -350,27 +357,74 @@ struct Side {
   }
 };
 
-// ---- output: 16 consecutive columns of a row
-template <class T>
-__device__ __forceinline__ void put16(T* o, const float* v, int n, bool accumulate) {
-  if (n >= 16) {
+// ---- output
+//
+// A lane holds 16 consecutive columns of its row: four 16-byte pieces of fp32, two
+// of bf16 (of two neighbouring operands four).  Stored as they are, an instruction
+// would write 16 bytes here and there in 32 rows; so lanes 8 and 16 apart exchange
+// pieces first, after which an instruction writes whole lines of 128 bytes: slot
+// 2 u + v of a lane has a piece of row 8 u + 16 v + (lane & 7).  (dw of 64 experts'
+// 2048 x 1408 in fp32, 738 MB, from 49146 rows: 499 us without, 485 with; past the
+// caches 463.)
+__device__ __forceinline__ void exchange(u32x4_t (&q)[4], int lane) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float w[8];
+  for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = v[8 * h + i];
-      if (accumulate) {
-        float old[8];
-        load8(o + 8 * h, old);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] += old[i];
-      }
-      store8(o + 8 * h, w);
+    for (int u = 0; u < 4; u += 2) {
+      const auto r = __builtin_amdgcn_permlane16_swap(q[u][e], q[u + 1][e], false, false);
+      q[u][e] = r[0];
+      q[u + 1][e] = r[1];
     }
+  const bool up = lane & 8;
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t got = __builtin_amdgcn_update_dpp(0, up ? q[v][e] : q[v + 2][e], 0x128 /* row_ror:8 */, 0xf, 0xf, false);
+      q[v][e] = up ? got : q[v][e];
+      q[v + 2][e] = up ? q[v + 2][e] : got;
+    }
+}
+
+// The first n elements of a 16-byte piece, past the caches for outputs that would
+// only push the operands out of them.
+__device__ __forceinline__ void put_piece(float* o, u32x4_t q, int n, bool past) {
+  if (n >= 4) {
+    if (past) stream16b(o, q);
+    else store16b(o, q);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) store1(o + i, accumulate ? load1(o + i) + v[i] : v[i]);
+    for (int i = 0; i < 4; ++i)
+      if (i < n) glb(o)[i] = __uint_as_float(q[i]);
+  }
+}
+__device__ __forceinline__ void put_piece(uint16_t* o, u32x4_t q, int n, bool past) {
+  if (n >= 8) {
+    if (past) stream16b(o, q);
+    else store16b(o, q);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) glb(o)[i] = static_cast<uint16_t>(q[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+// 16 consecutive columns of a row, n of them there, added to what is.
+template <class T>
+__device__ __forceinline__ void add16(T* o, const float* v, int n) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (n >= 8 * h + 8) {
+      float w[8];
+      load8(o + 8 * h, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] += v[8 * h + i];
+      store8(o + 8 * h, w);
+    } else {
+#pragma unroll
+      for (int i = 8 * h; i < 8 * h + 8; ++i)
+        if (i < n) store1(o + i, load1(o + i) + v[i]);
+    }
   }
 }
 
@@ -519,18 +573,58 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
 
   const int most = OP == kExpertDw ? a.rows : tile.hi - tile.lo;
   T* out = static_cast<T*>(a.out) + (OP == kExpertDw ? tile.e * a.ostride : tile.lo * a.ldo);
-  if (OP == kExpertDw && a.accumulate && depth == 0) return;
+  if (OP == kExpertDw && a.accumulate) {
+    if (depth == 0) return;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int r = tile.r0 + (wm * FM + j) * 32 + (lane & 31);
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        const int c = tile.c0 + (wn * FN + i) * 32 + 16 * (lane >> 5);
+        float v[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] = acc[i][j][q];
+        if (r < most && c < a.cols) add16(out + r * a.ldo + c, v, a.cols - c);
+      }
+    }
+    return;
+  }
+  constexpr bool PAIR = sizeof(T) == 2 && FN % 2 == 0;   // two operands' pieces make a line
+  constexpr int EACH = 16 / sizeof(T);                   // elements of a piece
+  const int u = lane >> 3 & 1, v = lane >> 4 & 1, h = lane >> 5;
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
-    const int r = tile.r0 + (wm * FM + j) * 32 + (lane & 31);
-    if (r >= most) continue;
+    const int r0 = tile.r0 + (wm * FM + j) * 32;
 #pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      const int c = tile.c0 + (wn * FN + i) * 32 + 16 * (lane >> 5);
-      float v[16];
+    for (int i = 0; i < FN; i += PAIR ? 2 : 1) {
+      const int c0 = tile.c0 + (wn * FN + i) * 32;
+      if constexpr (sizeof(T) == 4 || PAIR) {
+        u32x4_t q[4];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) v[q] = acc[i][j][q];
-      if (c < a.cols) put16(out + r * a.ldo + c, v, a.cols - c, OP == kExpertDw && a.accumulate);
+        for (int n = 0; n < 4; ++n) {
+          float w[8];
+#pragma unroll
+          for (int e = 0; e < EACH; ++e) w[e] = PAIR ? acc[i + n / 2 * PAIR][j][8 * (n & 1) + e] : acc[i][j][(4 * n + e) & 15];
+          if constexpr (PAIR) q[n] = narrow8(w);
+          else q[n] = bits4(w);
+        }
+        exchange(q, lane);
+        const int c = c0 + (PAIR ? 32 * u + 16 * h + 8 * v : 16 * h + 8 * u + 4 * v);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int r = r0 + 8 * (n >> 1) + 16 * (n & 1) + (lane & 7);
+          if (r < most && c < a.cols) put_piece(out + r * a.ldo + c, q[n], a.cols - c, a.past);
+        }
+      } else {
+        const int r = r0 + (lane & 31), c = c0 + 16 * h;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = acc[i][j][8 * n + e];
+          if (r < most && c + 8 * n < a.cols) put_piece(out + r * a.ldo + c + 8 * n, narrow8(w), a.cols - c - 8 * n, a.past);
+        }
+      }
     }
   }
 }
@@ -559,20 +653,24 @@ hipError_t launch_tiles(const ExpertArgs& a, hipStream_t s) {
 }
 
 template <int OP, class T>
-hipError_t launch_op(const ExpertArgs& a, int dt, bool aligned, hipStream_t s) {
-  if (dt == kF32) return launch_tiles<OP, kF32, false, T, 128, 128, 2, 2, 32, 2>(a, s);
-  if (!aligned) return launch_tiles<OP, kBF16, false, T, 128, 128, 2, 2, 64, 2>(a, s);
-  return launch_tiles<OP, kBF16, true, T, 256, 256, 4, 2, 64, 2>(a, s);
+hipError_t launch_op(const ExpertArgs& a, int dt, bool aligned, int tile, hipStream_t s) {
+  if (dt == kF32) return launch_tiles<OP, kF32, false, T, 64, 64, 2, 2, 32, 2>(a, s);
+  if (!aligned)
+    return tile == 64 ? launch_tiles<OP, kBF16, false, T, 64, 64, 2, 2, 64, 2>(a, s)
+                      : launch_tiles<OP, kBF16, false, T, 128, 128, 2, 2, 64, 2>(a, s);
+  if (tile == 64) return launch_tiles<OP, kBF16, true, T, 64, 64, 2, 2, 64, 3>(a, s);
+  if (tile == 128) return launch_tiles<OP, kBF16, true, T, 128, 128, 2, 2, 64, 2>(a, s);
+  return launch_tiles<OP, kBF16, true, T, 256, 256, 2, 4, 64, 2>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_experts(const ExpertArgs& a, int op, int dt, int odt, bool aligned, hipStream_t s) {
+hipError_t launch_experts(const ExpertArgs& a, int op, int dt, int odt, bool aligned, int tile, hipStream_t s) {
   auto with = [&](auto z) {
     using T = decltype(z);
-    if (op == kExpertFwd) return launch_op<kExpertFwd, T>(a, dt, aligned, s);
-    if (op == kExpertDx) return launch_op<kExpertDx, T>(a, dt, aligned, s);
-    return launch_op<kExpertDw, T>(a, dt, aligned, s);
+    if (op == kExpertFwd) return launch_op<kExpertFwd, T>(a, dt, aligned, tile, s);
+    if (op == kExpertDx) return launch_op<kExpertDx, T>(a, dt, aligned, tile, s);
+    return launch_op<kExpertDw, T>(a, dt, aligned, tile, s);
   };
   return odt == kBF16 ? with(uint16_t{}) : with(float{});
 }

@@ -124,9 +124,10 @@ struct ExpertArgs {
   int32_t depth;            // contraction length (fwd, dx)
   int32_t src;              // rows of x when gathered
   int32_t accumulate;       // dw
+  int32_t past;             // write past the caches
 };
-// Blocks of a launch with tm x tn tiles.  The rows' tiles are known to the device
-// alone: a full tile for every tm slots and a part of one an expert at most.
+// Blocks of a launch with tm x tn tiles.  How the slots are split is known to the
+// device alone: a full tile for every tm slots and a part of one an expert at most.
 inline int64_t expert_blocks(const ExpertArgs& a, int op, int tm, int tn) {
   const int64_t across = (int64_t(a.cols) + tn - 1) / tn;
   if (op == kExpertDw) {
@@ -143,6 +144,7 @@ constexpr uint32_t kExpertSpan = 0xf0000000u;
 constexpr int64_t kExpertPitch = int64_t(1) << 22;
 // aligned: every row of the operands starts at 16 bytes (and holds whole ones along
 // the contraction), so that loads go straight to LDS
-hipError_t launch_experts(const ExpertArgs& a, int op, int dt, int odt, bool aligned, hipStream_t s);
+// tile: 64, with bf16 also 128 and, aligned, 256
+hipError_t launch_experts(const ExpertArgs& a, int op, int dt, int odt, bool aligned, int tile, hipStream_t s);
 
 }  // namespace muon

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <vector>
 
@@ -143,9 +144,49 @@ bool spans(const muon_mat& x) {
   return x.rows == 0 || ((x.rows - 1) * x.ld + x.cols) * esize(x.dtype) < int64_t(kExpertSpan);
 }
 
-int run_products(const ExpertArgs& a, int op, int dt, int odt, bool aligned, void* stream) {
-  if (expert_blocks(a, op, 128, 128) > kMaxBlocks) return MUON_E_SHAPE;
-  return launch_experts(a, op, dt, odt, aligned, static_cast<hipStream_t>(stream)) == hipSuccess ? MUON_OK : MUON_E_HIP;
+// Output tile of a product (64, 128 or 256 on a side) by an estimate of its time: the
+// rounds of tiles that the device's 256 CUs take, times the stages of 64 contraction
+// elements of a tile at what each costs, measured on MI355X with 1, 2 and 3 blocks a
+// CU, us: 256: 1.7, 128: 1.2 (0.8 alone), 64: 0.6; and a tile's own start and end.  A
+// launch's last round of 256-wide tiles counts whole.  fwd, us with tiles of 64 | 128 |
+// 256: 4096 slots, 8 experts, 1024 -> 2048: 39 | 38 | 34; 16384 slots, 1024 -> 1024: 62
+// | 52 | 61; 48 slots, 64 experts, 2048 -> 1408: 37 | 32 | 49, 12000: 170 | 128 | 131.
+int tile_of(const ExpertArgs& a, int op, int dt, bool aligned) {
+  if (dt == MUON_F32) return 64;   // 128-wide ones lost at every size: their LDS leaves one block a CU
+  if (const char* e = std::getenv("MUON_EXPERT_TILE")) {
+    const int t = std::atoi(e);
+    if (t == 64 || t == 128 || (t == 256 && aligned)) return t;
+  }
+  // of the experts, those that a few slots can reach
+  const double used = std::min<double>(a.experts, a.slots);
+  const double depth = op == kExpertDw ? 1.5 * a.slots / a.experts : a.depth;
+  const double stages = std::ceil(depth / 64);
+  auto time = [&](int t, double slots, double each, double alone, double own) {
+    const double across = double(ceil_div(a.cols, t));
+    // half a tile too many for an expert, on average
+    const double high = op == kExpertDw ? double(a.experts) * ceil_div(a.rows, t) : double(a.slots) / t + 0.5 * used;
+    const double rounds = high * across / slots;
+    const double whole = rounds <= 1 ? 1 : t == 256 ? std::ceil(rounds) : rounds + 0.3;
+    return whole * (stages * (rounds <= 0.5 ? alone : each) + own);
+  };
+  const double t64 = time(64, 768, 0.6, 0.5, 3), t128 = time(128, 512, 1.2, 0.8, 3);
+  if (!aligned) return t64 < t128 ? 64 : 128;
+  const double t256 = time(256, 256, 1.7, 1.7, 5);
+  return t256 < std::min(t64, t128) ? 256 : t64 < t128 ? 64 : 128;
+}
+
+// Outputs that are larger than half of the memory side's cache (256 MiB) go past
+// the caches.
+bool past_caches(const ExpertArgs& a, int op, int odt) {
+  const int64_t rows = op == kExpertDw ? int64_t(a.experts) * a.rows : a.slots;
+  return rows * a.cols * esize(odt) > int64_t(128) << 20;
+}
+
+int run_products(ExpertArgs a, int op, int dt, int odt, bool aligned, void* stream) {
+  a.past = past_caches(a, op, odt);
+  const int tile = tile_of(a, op, dt, aligned);
+  if (expert_blocks(a, op, tile, tile) > kMaxBlocks) return MUON_E_SHAPE;
+  return launch_experts(a, op, dt, odt, aligned, tile, static_cast<hipStream_t>(stream)) == hipSuccess ? MUON_OK : MUON_E_HIP;
 }
 
 int check_gates(const float* gates, const muon_slots& s, std::vector<Span>& v, bool write) {

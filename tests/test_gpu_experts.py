@@ -235,6 +235,40 @@ def test_products(tokens, k, experts, cols, outs, dtype, gather):
     check_layer(tokens, k, experts, cols, outs, dtype, gather)
 
 
+@pytest.mark.parametrize("tile", [64, 128, 256])
+@pytest.mark.parametrize("tokens,k,experts,cols,outs,dtype", [
+    (300, 2, 3, 200, 264, BF16), (520, 1, 1, 128, 520, BF16), (90, 3, 9, 77, 129, BF16), (300, 2, 3, 200, 264, F32),
+    (33, 2, 70, 48, 40, BF16), (1300, 1, 2, 712, 288, BF16)])
+def test_products_by_every_tile(tokens, k, experts, cols, outs, dtype, tile, monkeypatch):
+    monkeypatch.setenv("MUON_EXPERT_TILE", str(tile))
+    for gather in (False, True):
+        check_layer(tokens, k, experts, cols, outs, dtype, gather, drop=0.1)
+
+
+@pytest.mark.parametrize("tile", [64, 128, 256])
+def test_many_tiles_a_block(tile, monkeypatch):
+    """More tiles than blocks, so that a block goes from tile to tile: against the sums of fp32 products
+    in float64, on the GPU."""
+    monkeypatch.setenv("MUON_EXPERT_TILE", str(tile))
+    g = torch.Generator().manual_seed(tile)
+    experts, cols, outs, tokens = (5, 320, 1160, 13000) if tile == 256 else (5, 136, 456, 6000)
+    choice = pick(g, tokens, 2, experts)
+    plan = mo.expert_plan(choice.cuda(), experts)
+    x, w, dy = rand(g, tokens, cols), rand(g, experts, outs, cols), rand(g, 2 * tokens, outs)
+    y = mo.expert_linear(x, w, plan, gather=True)
+    dx, dw = mo.expert_linear_grad(dy, w, x, plan, gather=True)
+    at = plan.offsets.tolist()
+    xs = x[plan.tokens.long()].double()
+    for e in range(experts):
+        r = slice(at[e], at[e + 1])
+        for got, a, b in ((y[r], xs[r], w[e].double().t().contiguous()), (dx[r], dy[r].double(), w[e].double()),
+                          (dw[e], dy[r].double().t().contiguous(), xs[r])):
+            want, s = torch.mm(a, b), torch.mm(a.abs(), b.abs())
+            tol = a.shape[1] * 2 * U * s
+            tol = tol + half(got.dtype) * (want.abs() + tol)
+            assert ((got.double() - want).abs() <= tol).all(), (tile, e)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_products_with_dropped_slots(dtype):
     check_layer(200, 3, 6, 72, 104, dtype, True, drop=0.3)
