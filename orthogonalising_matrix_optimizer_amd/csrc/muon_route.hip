@@ -132,6 +132,7 @@ __device__ __forceinline__ void sort_pass(const SortArgs& a, int pass, SortShare
     const int me = blockIdx.x, blocks = gridDim.x;
     for (int bin = t % BINS; bin < BINS; bin += kSortThreads) {
       int32_t all = 0, early = 0;
+#pragma unroll 8
       for (int b = t / BINS; b < blocks; b += STRANDS) {
         const int32_t c = a.counts[int64_t(b) * BINS + bin];
         all += c;

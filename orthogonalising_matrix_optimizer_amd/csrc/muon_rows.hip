@@ -32,6 +32,12 @@ __device__ __forceinline__ void store_cols(T* row, int c, int cols, const float*
   }
 }
 
+// Lanes below this one in a mask.
+__device__ __forceinline__ int below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
+}
+
 __device__ __forceinline__ int64_t id_at(const void* ids, int bytes, int i) {
   return bytes == 8 ? glb(static_cast<const int64_t*>(ids))[i]
                     : static_cast<int64_t>(glb(static_cast<const int32_t*>(ids))[i]);
@@ -95,8 +101,8 @@ __device__ __forceinline__ void embed_sum(const EmbedGradArgs& a, int chunk, int
 #pragma unroll
     for (int u = 0; u < kGradBatch; ++u) {
       const int i = i0 + u < n ? i0 + u : n - 1;
-      const int64_t t = __builtin_amdgcn_readlane(from, i);
-      if (mine && i0 + u < n) load_cols(static_cast<const T*>(a.dy) + t * a.ldy, c, a.cols, v[u]);
+      const int64_t t = __builtin_amdgcn_readlane(from, i);   // (of padding there is no token)
+      if (mine && i0 + u < n && __builtin_amdgcn_readlane(keys, i) < a.rows) load_cols(static_cast<const T*>(a.dy) + t * a.ldy, c, a.cols, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < kGradBatch; ++u) {
@@ -112,7 +118,7 @@ __device__ __forceinline__ void embed_sum(const EmbedGradArgs& a, int chunk, int
       if (then == k && i + 1 < n) continue;
       if (mine) {
         if (came || then == k) {
-          store_cols(a.part + (static_cast<int64_t>(chunk) * 2 + (came ? 0 : 1)) * a.cols, c, a.cols, acc);
+          store8(a.part + (static_cast<int64_t>(chunk) * 2 + (came ? 0 : 1)) * a.ldp + c, acc);
         } else {
           D* o = static_cast<D*>(a.dw) + k * a.ldw;
           float w[8];
@@ -132,7 +138,7 @@ __device__ __forceinline__ void embed_sum(const EmbedGradArgs& a, int chunk, int
 }
 
 template <class D>
-__device__ __forceinline__ void embed_zero(const EmbedGradArgs& a, int block, int lane) {
+__device__ __forceinline__ void embed_zero(const EmbedGradArgs& a, int block, int lane, volatile uint8_t* list) {
   const int v = block * kEmbedZeroRows + lane;
   int lo = 0, hi = a.tokens;
   while (lo < hi) {   // the first position whose key is at least v
@@ -141,13 +147,16 @@ __device__ __forceinline__ void embed_zero(const EmbedGradArgs& a, int block, in
     else hi = mid;
   }
   const bool absent = v < a.rows && !(lo < a.tokens && a.key[lo] == v);
-  uint64_t todo = __ballot(absent);
+  // the pieces of all rows without tokens, one after the other
+  const uint64_t mask = __ballot(absent);
+  if (absent) list[below(mask)] = static_cast<uint8_t>(lane);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  const int wide = (a.cols + 7) / 8, items = __popcll(mask) * wide;
   const float zeros[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  while (todo) {
-    const int r = __builtin_ctzll(todo);
-    todo &= todo - 1;
-    D* o = static_cast<D*>(a.dw) + (static_cast<int64_t>(block) * kEmbedZeroRows + r) * a.ldw;
-    for (int c = lane * 8; c < a.cols; c += 512) store_cols(o, c, a.cols, zeros);
+  for (int i = lane; i < items; i += 64) {
+    const int n = i / wide;
+    D* o = static_cast<D*>(a.dw) + (static_cast<int64_t>(block) * kEmbedZeroRows + list[n]) * a.ldw;
+    store_cols(o, (i - n * wide) * 8, a.cols, zeros);
   }
 }
 
@@ -155,11 +164,12 @@ template <class T, class D>
 __global__ __launch_bounds__(kRowThreads) void k_embedding_grad(EmbedGradArgs a, int strips) {
   const int unit = blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, sums = a.chunks * strips;
+  __shared__ uint8_t list[kRowThreads / 64][64];
   if (unit < sums) {
     embed_sum<T, D>(a, unit / strips, unit % strips, lane);
   } else if (!a.accumulate) {
     const int z = unit - sums;
-    if (z < (a.rows + kEmbedZeroRows - 1) / kEmbedZeroRows) embed_zero<D>(a, z, lane);
+    if (z < (a.rows + kEmbedZeroRows - 1) / kEmbedZeroRows) embed_zero<D>(a, z, lane, list[threadIdx.x >> 6]);
   }
 }
 
@@ -191,15 +201,19 @@ __global__ __launch_bounds__(kRowThreads) void k_embedding_join(EmbedGradArgs a)
   const int share = (n + WAVES - 1) / WAVES;
   const int i0 = wave * share < n ? wave * share : n, i1 = i0 + share < n ? i0 + share : n;
   float v[4] = {0.f, 0.f, 0.f, 0.f};
-  auto add = [&](int64_t row) {
-    const float* p = a.part + row * a.cols;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c + e < a.cols) v[e] += p[c + e];
+  auto row = [&](int64_t r) {
+    return c < a.cols ? *reinterpret_cast<const float4*>(a.part + r * a.ldp + c) : make_float4(0.f, 0.f, 0.f, 0.f);
   };
-  if (wave == 0) add(static_cast<int64_t>(chunk) * 2 + 1);
-#pragma unroll 8
-  for (int i = i0; i < i1; ++i) add(static_cast<int64_t>(chunk + 1 + i) * 2);
+  auto add = [&](float4 q) { v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w; };
+  if (wave == 0) add(row(static_cast<int64_t>(chunk) * 2 + 1));
+  for (int i = i0; i < i1; i += kGradBatch) {
+    float4 q[kGradBatch];
+#pragma unroll
+    for (int u = 0; u < kGradBatch; ++u) q[u] = row(static_cast<int64_t>(chunk + 1 + (i + u < i1 ? i + u : i1 - 1)) * 2);
+#pragma unroll
+    for (int u = 0; u < kGradBatch; ++u)
+      if (i + u < i1) add(q[u]);
+  }
   sums[wave][lane] = make_float4(v[0], v[1], v[2], v[3]);
   __syncthreads();
   if (wave != 0) return;

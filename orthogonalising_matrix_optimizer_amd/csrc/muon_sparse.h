@@ -15,7 +15,7 @@ namespace muon {
 constexpr int kSortThreads = 1024;
 constexpr int kSortBits = 8, kSortWide = 10;
 // blocks up to which each counts all keys itself (one launch a pass)
-constexpr int kSortSelf = 32;
+constexpr int kSortSelf = 4;
 
 // Bits of the keys 0 .. limit, and how they are sorted.
 inline int key_bits(int64_t limit) {
@@ -92,20 +92,21 @@ struct EmbedArgs {
 };
 hipError_t launch_embedding(const EmbedArgs& a, int dt, hipStream_t s);
 
-// Sums of dy's rows over runs of equal sorted keys.  A block takes kEmbedRun
-// consecutive sorted positions; a run inside it is written at once, a run that
-// crosses its edges goes to `part` (two rows a block) and is joined by a second launch.
-constexpr int kEmbedZeroRows = 64;   // rows of dw that a block looks over for zeroing
+// Sums of dy's rows over runs of equal sorted keys.  A wave takes `chunk` consecutive
+// sorted positions; a run inside them is written at once, one that crosses their edges
+// goes to `part` (two rows a chunk) and is joined by a second launch.
+constexpr int kEmbedZeroRows = 64;   // rows of dw that a wave looks over for zeroing
 struct EmbedGradArgs {
   const void* dy;
   const int32_t* key;     // sorted ids (the last ones `rows`: no gradient)
   const int32_t* pos;     // their tokens
   void* dw;
-  float* part;            // chunks x 2 x cols
+  float* part;            // chunks x 2 rows
   int64_t ldy, ldw;
   float scale;
   int32_t tokens, rows, cols, accumulate;
-  int32_t chunk, chunks;  // sorted positions a block sums, blocks that sum
+  int32_t chunk, chunks;  // sorted positions a wave sums, and how many such chunks
+  int32_t ldp;            // floats from one row of part to the next, a multiple of 8
 };
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, int dt, int odt, hipStream_t s);
 

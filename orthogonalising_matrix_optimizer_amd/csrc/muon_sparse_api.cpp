@@ -199,17 +199,20 @@ int check_gates(const float* gates, const muon_slots& s, std::vector<Span>& v, b
 
 struct GradPlan {
   int64_t chunk, chunks;
-  size_t keys, counts, bytes;   // offsets: four arrays of n integers, counts, partial rows
+  size_t keys, counts, part, bytes;   // offsets: four arrays of n integers, counts, partial rows
 };
 
 GradPlan plan_grad(int64_t tokens, int64_t rows, int64_t cols) {
   GradPlan p;
-  p.chunk = 32;
+  // short chunks where there are few waves (two a SIMD are wanted), long ones where
+  // there are many: each writes up to two partial rows
+  p.chunk = 8;
+  while (p.chunk < 64 && tokens * ceil_div(cols, 512) >= 4096 * p.chunk) p.chunk *= 2;
   p.chunks = ceil_div(tokens, p.chunk);
   p.keys = round_up(size_t(tokens) * 4, 16);
   p.counts = 4 * p.keys;
-  const size_t part = round_up(p.counts + count_bytes(tokens, rows), 16);
-  p.bytes = tokens ? part + size_t(p.chunks) * 2 * size_t(cols) * 4 : 0;
+  p.part = round_up(p.counts + count_bytes(tokens, rows), 16);
+  p.bytes = tokens ? p.part + size_t(p.chunks) * 2 * round_up(size_t(cols), 8) * 4 : 0;
   return p;
 }
 
@@ -553,7 +556,7 @@ int muon_embedding_grad(const muon_mat* dy, const muon_ids* ids, float scale, in
     if (launch_sort(sort, s) != hipSuccess) return MUON_E_HIP;
     a.key = sort.key[(sort.passes - 1) & 1];
     a.pos = sort.pos[(sort.passes - 1) & 1];
-    a.part = reinterpret_cast<float*>(ws + p.bytes) - p.chunks * 2 * dw->cols;
+    a.part = reinterpret_cast<float*>(ws + p.part);
   }
   a.dy = dy->ptr;
   a.dw = dw->ptr;
@@ -566,6 +569,7 @@ int muon_embedding_grad(const muon_mat* dy, const muon_ids* ids, float scale, in
   a.accumulate = accumulate != 0;
   a.chunk = int32_t(p.chunk);
   a.chunks = int32_t(p.chunks);
+  a.ldp = int32_t(round_up(size_t(dw->cols), 8));
   return launch_embedding_grad(a, dy->dtype, dw->dtype, s) == hipSuccess ? MUON_OK : MUON_E_HIP;
 } catch (...) {   // an allocation of the host's failed
   return MUON_E_HIP;
