@@ -74,6 +74,7 @@ struct CombineArgs {
   const void* dout;       // tokens' rows (gradient)
   const float* gates;     // or null: ones
   const int32_t* place;
+  const int32_t* rows;    // gradient: the rows' tokens
   void* out;              // forward: tokens' rows; gradient: slots' rows, or null
   float* dgates;          // or null
   int64_t ldy, ldd, ldo;

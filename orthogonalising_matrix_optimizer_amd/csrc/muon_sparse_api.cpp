@@ -463,6 +463,7 @@ int muon_expert_combine_grad(const muon_mat* dout, const muon_mat* y, const floa
   a.y = dgates ? y->ptr : nullptr;
   a.gates = gates;
   a.place = slots->place;
+  a.rows = slots->tokens;
   a.out = dy && dout->cols ? dy->ptr : nullptr;
   a.dgates = dgates;
   a.ldd = dout->ld;
