@@ -228,6 +228,61 @@ __global__ __launch_bounds__(kRowThreads) void k_embedding_join(EmbedGradArgs a)
     if (c + e < a.cols) store1(o + c + e, (a.accumulate ? load1(o + c + e) : 0.f) + a.scale * v[e]);
 }
 
+// Up to kFewTokens tokens, in one launch and without a sort: a wave takes a row of
+// the table, finds the tokens that have it by ballots over all ids and adds their
+// rows in order.  (37 tokens, 333 rows of 77: 5 us where sort, sums and join take 15.)
+template <class T, class D>
+__global__ __launch_bounds__(kRowThreads) void k_embedding_few(EmbedGradArgs a, const void* ids, int id_bytes) {
+  constexpr int MASKS = kFewTokens / 64;
+  const int v = blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (v >= a.rows) return;
+  uint64_t mask[MASKS];
+  bool any = false;
+#pragma unroll
+  for (int m = 0; m < MASKS; ++m) {
+    const int t = m * 64 + lane;
+    mask[m] = m * 64 < a.tokens ? __ballot(t < a.tokens && id_at(ids, id_bytes, t < a.tokens ? t : 0) == v) : 0;
+    any = any || mask[m];
+  }
+  if (!any && a.accumulate) return;
+  D* o = static_cast<D*>(a.dw) + v * a.ldw;
+  for (int c = lane * 8; c < a.cols; c += 512) {
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int m = 0; m < MASKS; ++m) {
+      uint64_t left = mask[m];
+      while (left) {
+        float x[kGradBatch][8];
+        int n = 0;
+#pragma unroll
+        for (int u = 0; u < kGradBatch; ++u)
+          if (left) {
+            const int64_t t = m * 64 + __builtin_ctzll(left);
+            left &= left - 1;
+            ++n;
+            load_cols(static_cast<const T*>(a.dy) + t * a.ldy, c, a.cols, x[u]);
+          }
+#pragma unroll
+        for (int u = 0; u < kGradBatch; ++u)
+          if (u < n) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] += x[u][e];
+          }
+      }
+    }
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 0.f;
+    if (a.accumulate) load_cols(o, c, a.cols, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] += a.scale * acc[e];
+    store_cols(o, c, a.cols, w);
+  }
+}
+
 // ---- combine: a thread takes eight columns of a token, the rows of up to
 // kSlotBatch slots in flight
 constexpr int kSlotBatch = 8;
@@ -357,6 +412,16 @@ hipError_t launch_embedding_grad(const EmbedGradArgs& a, int dt, int odt, hipStr
       hipLaunchKernelGGL((k_embedding_join<D>), dim3(a.chunks - 1, blocks_of(a.cols, 256)), dim3(kRowThreads),
                          0, s, a);
     return hipGetLastError();
+  });
+}
+
+hipError_t launch_embedding_few(const EmbedGradArgs& a, const void* ids, int id_bytes, int dt, int odt, hipStream_t s) {
+  return with_type(dt, [&](auto z) {
+    return with_type(odt, [&](auto o) {
+      hipLaunchKernelGGL((k_embedding_few<decltype(z), decltype(o)>), dim3(blocks_of(a.rows, kRowThreads / 64)),
+                         dim3(kRowThreads), 0, s, a, ids, id_bytes);
+      return hipGetLastError();
+    });
   });
 }
 

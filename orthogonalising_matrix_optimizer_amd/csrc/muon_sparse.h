@@ -109,6 +109,9 @@ struct EmbedGradArgs {
   int32_t chunk, chunks;  // sorted positions a wave sums, and how many such chunks
   int32_t ldp;            // floats from one row of part to the next, a multiple of 8
 };
+// Without a sort, for few tokens (key, pos, part and the chunks are not used).
+constexpr int kFewTokens = 256;
+hipError_t launch_embedding_few(const EmbedGradArgs& a, const void* ids, int id_bytes, int dt, int odt, hipStream_t s);
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, int dt, int odt, hipStream_t s);
 
 // ---- experts' products (muon_experts.hip)

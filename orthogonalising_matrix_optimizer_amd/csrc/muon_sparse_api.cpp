@@ -198,6 +198,7 @@ int check_gates(const float* gates, const muon_slots& s, std::vector<Span>& v, b
 // ---- embedding's gradient
 
 struct GradPlan {
+  bool few;                     // without a sort and a workspace
   int64_t chunk, chunks;
   size_t keys, counts, part, bytes;   // offsets: four arrays of n integers, counts, partial rows
 };
@@ -206,13 +207,14 @@ GradPlan plan_grad(int64_t tokens, int64_t rows, int64_t cols) {
   GradPlan p;
   // short chunks where there are few waves (two a SIMD are wanted), long ones where
   // there are many: each writes up to two partial rows
+  p.few = tokens && tokens <= kFewTokens && ceil_div(rows, 4) <= kMaxBlocks;
   p.chunk = 8;
   while (p.chunk < 64 && tokens * ceil_div(cols, 512) >= 4096 * p.chunk) p.chunk *= 2;
   p.chunks = ceil_div(tokens, p.chunk);
   p.keys = round_up(size_t(tokens) * 4, 16);
   p.counts = 4 * p.keys;
   p.part = round_up(p.counts + count_bytes(tokens, rows), 16);
-  p.bytes = tokens ? p.part + size_t(p.chunks) * 2 * round_up(size_t(cols), 8) * 4 : 0;
+  p.bytes = tokens && !p.few ? p.part + size_t(p.chunks) * 2 * round_up(size_t(cols), 8) * 4 : 0;
   return p;
 }
 
@@ -541,7 +543,7 @@ int muon_embedding_grad(const muon_mat* dy, const muon_ids* ids, float scale, in
   char* ws = static_cast<char*>(workspace);
   EmbedGradArgs a;
   std::memset(&a, 0, sizeof(a));
-  if (ids->n) {
+  if (ids->n && !p.few) {
     SortArgs sort;
     std::memset(&sort, 0, sizeof(sort));
     sort.ids = ids->ptr;
@@ -571,7 +573,9 @@ int muon_embedding_grad(const muon_mat* dy, const muon_ids* ids, float scale, in
   a.chunk = int32_t(p.chunk);
   a.chunks = int32_t(p.chunks);
   a.ldp = int32_t(round_up(size_t(dw->cols), 8));
-  return launch_embedding_grad(a, dy->dtype, dw->dtype, s) == hipSuccess ? MUON_OK : MUON_E_HIP;
+  const hipError_t e = p.few ? launch_embedding_few(a, ids->ptr, ids->bytes, dy->dtype, dw->dtype, s)
+                           : launch_embedding_grad(a, dy->dtype, dw->dtype, s);
+  return e == hipSuccess ? MUON_OK : MUON_E_HIP;
 } catch (...) {   // an allocation of the host's failed
   return MUON_E_HIP;
 }

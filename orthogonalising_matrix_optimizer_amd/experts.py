@@ -20,7 +20,7 @@ from typing import NamedTuple, Optional, Tuple
 import torch
 
 from . import _lib
-from .mx import _DT, _MAT1, _call, _gpu, _mat, _new_one, _not_recorded, _rows_of, _written
+from .mx import _DT, _MAT1, _call, _empty, _gpu, _mat, _new_one, _not_recorded, _rows_of, _written
 
 _SLOTS, _STACK, _IDS = Struct("PPPqii"), Struct("Pqqqqqii"), Struct("Pqii")
 _I32 = torch.int32
@@ -34,17 +34,25 @@ class ExpertPlan:
     expert's rows) and place [tokens, k] (each slot's row, -1 if its expert was
     none of 0 .. experts - 1) are int32 tensors on the device."""
 
-    __slots__ = ("offsets", "tokens", "place", "n_tokens", "k", "experts", "device", "desc")
+    __slots__ = ("buffer", "n_tokens", "k", "experts", "device", "desc")
 
-    def __init__(self, n_tokens: int, k: int, experts: int, device: torch.device):
-        n = n_tokens * k
-        buf = torch.empty(2 * n + experts + 1, dtype=_I32, device=device)
-        self.place = buf.as_strided((n_tokens, k), (k, 1))
-        self.tokens = buf.as_strided((n,), (1,), n)
-        self.offsets = buf.as_strided((experts + 1,), (1,), 2 * n)
-        self.n_tokens, self.k, self.experts, self.device = n_tokens, k, experts, device
-        p = buf.data_ptr()
-        self.desc = _SLOTS.pack(p + 8 * n, p + 4 * n, p, n_tokens, k, experts)
+    def __init__(self, buffer: torch.Tensor, n_tokens: int, k: int, experts: int, device: torch.device):
+        # buffer: place, tokens and offsets, int32
+        self.buffer, self.n_tokens, self.k, self.experts, self.device = buffer, n_tokens, k, experts, device
+        p, n = buffer.data_ptr(), 4 * n_tokens * k
+        self.desc = _SLOTS.pack(p + 2 * n, p + n, p, n_tokens, k, experts)
+
+    @property
+    def offsets(self) -> torch.Tensor:
+        return self.buffer.as_strided((self.experts + 1,), (1,), 2 * self.slots)
+
+    @property
+    def tokens(self) -> torch.Tensor:
+        return self.buffer.as_strided((self.slots,), (1,), self.slots)
+
+    @property
+    def place(self) -> torch.Tensor:
+        return self.buffer.as_strided((self.n_tokens, self.k), (self.k, 1), 0)
 
     @property
     def slots(self) -> int:
@@ -67,7 +75,7 @@ def _workspace(n: int, dev: torch.device):
     """Scratch memory of n bytes (or none), its address and size."""
     if not n:
         return None, None, 0
-    t = torch.empty(n, dtype=torch.uint8, device=dev)
+    t = _empty((n,), (1,), dtype=torch.uint8, device=dev)
     return t, t.data_ptr(), n
 
 
@@ -157,7 +165,7 @@ def expert_plan(experts: torch.Tensor, n_experts: int) -> ExpertPlan:
     n, k = experts.shape
     _check_counts(n, k, n_experts)
     ids = _ids(experts)
-    plan = ExpertPlan(n, k, n_experts, dev)
+    plan = ExpertPlan(_empty((2 * n * k + n_experts + 1,), (1,), dtype=_I32, device=dev), n, k, n_experts, dev)
     keep, ws, size = _workspace(int(_lib.load().muon_expert_plan_workspace_bytes(n, k, n_experts)), dev)
     _lib.check(_call("muon_expert_plan", dev, ids, plan.desc, ws, size), "muon_expert_plan")
     return plan
@@ -177,12 +185,16 @@ def route(logits: torch.Tensor, k: int, normalize: bool = False) -> Routing:
     k = int(k)
     _check_counts(n, k, e)
     mat = _MAT1.pack(*_mat(logits, dev))
-    gates = torch.empty((n, k), dtype=torch.float32, device=dev)
-    chosen = torch.empty((n, k), dtype=_I32, device=dev)
-    plan = ExpertPlan(n, k, e, dev)
+    # one allocation: the plan, then the chosen experts and the gates
+    m = n * k
+    buf = _empty((4 * m + e + 1,), (1,), dtype=_I32, device=dev)
+    plan = ExpertPlan(buf, n, k, e, dev)
+    at = 2 * m + e + 1
+    chosen = buf.as_strided((n, k), (k, 1), at)
+    gates = buf.view(torch.float32).as_strided((n, k), (k, 1), at + m)
+    p = buf.data_ptr() + 4 * at
     keep, ws, size = _workspace(int(_lib.load().muon_expert_plan_workspace_bytes(n, k, e)), dev)
-    _lib.check(_call("muon_route", dev, mat, int(bool(normalize)), gates.data_ptr(), chosen.data_ptr(),
-                     plan.desc, ws, size), "muon_route")
+    _lib.check(_call("muon_route", dev, mat, int(bool(normalize)), p + 4 * m, p, plan.desc, ws, size), "muon_route")
     return Routing(gates, chosen, plan, bool(normalize))
 
 
@@ -325,7 +337,7 @@ def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan,
         raise ValueError(f"dout has {dout.shape[1]} features, y {y.shape[1]}")
     g = _f32(gates, (plan.n_tokens, plan.k), dev, "gates")
     dy, dym = _new_one(plan.slots, dout.shape[1], dout.dtype, dev)
-    dgates = torch.empty((plan.n_tokens, plan.k), dtype=torch.float32, device=dev)
+    dgates = _empty((plan.n_tokens, plan.k), (plan.k, 1), dtype=torch.float32, device=dev)
     _call("muon_expert_combine_grad", dev, dm, ym, g, plan.desc, dym, dgates.data_ptr())
     return dy, dgates
 

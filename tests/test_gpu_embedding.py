@@ -44,7 +44,7 @@ def ids_of(g, tokens, rows, kind):
 
 @pytest.mark.parametrize("kind", ["words", "same", "spread", "padded"])
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("tokens,rows,cols", [(1, 1, 1), (5, 3, 8), (33, 300, 77), (64, 70000, 24), (1000, 50, 33),
+@pytest.mark.parametrize("tokens,rows,cols", [(1, 1, 1), (5, 3, 8), (33, 300, 77), (64, 70000, 24), (1000, 50, 33), (256, 700, 1030), (257, 40, 8),
                                               (1025, 5000, 520), (2500, 70, 1030), (33000, 40, 9)])
 def test_lookup_and_gradient(tokens, rows, cols, dtype, kind):
     announce(f"embedding {tokens} of {rows} x {cols}, {dtype}, {kind}")
