@@ -654,7 +654,9 @@ hipError_t launch_tiles(const ExpertArgs& a, hipStream_t s) {
 
 template <int OP, class T>
 hipError_t launch_op(const ExpertArgs& a, int dt, bool aligned, int tile, hipStream_t s) {
-  if (dt == kF32) return launch_tiles<OP, kF32, false, T, 64, 64, 2, 2, 32, 2>(a, s);
+  if (dt == kF32)
+    return tile == 64 ? launch_tiles<OP, kF32, false, T, 64, 64, 2, 2, 32, 2>(a, s)
+                      : launch_tiles<OP, kF32, false, T, 128, 128, 2, 4, 32, 2>(a, s);
   if (!aligned)
     return tile == 64 ? launch_tiles<OP, kBF16, false, T, 64, 64, 2, 2, 64, 2>(a, s)
                       : launch_tiles<OP, kBF16, false, T, 128, 128, 2, 2, 64, 2>(a, s);

@@ -149,7 +149,7 @@ constexpr uint32_t kExpertSpan = 0xf0000000u;
 constexpr int64_t kExpertPitch = int64_t(1) << 22;
 // aligned: every row of the operands starts at 16 bytes (and holds whole ones along
 // the contraction), so that loads go straight to LDS
-// tile: 64, with bf16 also 128 and, aligned, 256
+// tile: 64, 128 or, aligned, 256
 hipError_t launch_experts(const ExpertArgs& a, int op, int dt, int odt, bool aligned, int tile, hipStream_t s);
 
 }  // namespace muon

@@ -147,12 +147,13 @@ bool spans(const muon_mat& x) {
 // Output tile of a product (64, 128 or 256 on a side) by an estimate of its time: the
 // rounds of tiles that the device's 256 CUs take, times the stages of 64 contraction
 // elements of a tile at what each costs, measured on MI355X with 1, 2 and 3 blocks a
-// CU, us: 256: 1.7, 128: 1.2 (0.8 alone), 64: 0.6; and a tile's own start and end.  A
-// launch's last round of 256-wide tiles counts whole.  fwd, us with tiles of 64 | 128 |
+// CU, us: 256: 1.7, 128: 1.2 (0.8 alone), 64: 0.6; fp32 (one block, three) 128: 3.1, 64:
+// 3.1 (2.4 alone); and a tile's own start and end.  A launch's last round of tiles with
+// a CU to themselves counts whole.  fwd, us with tiles of 64 | 128 |
 // 256: 4096 slots, 8 experts, 1024 -> 2048: 39 | 38 | 34; 16384 slots, 1024 -> 1024: 62
-// | 52 | 61; 48 slots, 64 experts, 2048 -> 1408: 37 | 32 | 49, 12000: 170 | 128 | 131.
+// | 52 | 61; 48 slots, 64 experts, 2048 -> 1408: 37 | 32 | 49, 12000: 170 | 128 | 131; fp32
+// 8192 slots, 32 experts, 1024 -> 1024: 150 | 142; 32768, 8, 2048 -> 1024: 1079 | 804.
 int tile_of(const ExpertArgs& a, int op, int dt, bool aligned) {
-  if (dt == MUON_F32) return 64;   // 128-wide ones lost at every size: their LDS leaves one block a CU
   if (const char* e = std::getenv("MUON_EXPERT_TILE")) {
     const int t = std::atoi(e);
     if (t == 64 || t == 128 || (t == 256 && aligned)) return t;
@@ -166,9 +167,10 @@ int tile_of(const ExpertArgs& a, int op, int dt, bool aligned) {
     // half a tile too many for an expert, on average
     const double high = op == kExpertDw ? double(a.experts) * ceil_div(a.rows, t) : double(a.slots) / t + 0.5 * used;
     const double rounds = high * across / slots;
-    const double whole = rounds <= 1 ? 1 : t == 256 ? std::ceil(rounds) : rounds + 0.3;
+    const double whole = rounds <= 1 ? 1 : slots == 256 ? std::ceil(rounds) : rounds + 0.3;
     return whole * (stages * (rounds <= 0.5 ? alone : each) + own);
   };
+  if (dt == MUON_F32) return time(64, 768, 3.1, 2.4, 3) <= time(128, 256, 3.1, 3.1, 4) ? 64 : 128;
   const double t64 = time(64, 768, 0.6, 0.5, 3), t128 = time(128, 512, 1.2, 0.8, 3);
   if (!aligned) return t64 < t128 ? 64 : 128;
   const double t256 = time(256, 256, 1.7, 1.7, 5);
