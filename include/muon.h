@@ -584,6 +584,7 @@ int muon_route_grad(const float* dgates, const muon_mat* logits, const float* ga
  * muon_expert_gather makes sorted rows).  fp32 operands are multiplied as sums of
  * three bf16 terms each (all of their 24 bits; products' terms below 2^-24 are
  * left out); one that is not finite makes the sums it enters NaN.
+ * Row pitches of operands are at most 2^22 elements (MUON_E_SHAPE).
  *   linear:    out[r] = x[r] w[e(r)]^T                 (slots x out)
  *   linear_dx: dx[r]  = dy[r] w[e(r)]                  (slots x in)
  *   linear_dw: dw[e]  = sum over e's rows dy[r]^T x[r] (out x in; zeros without

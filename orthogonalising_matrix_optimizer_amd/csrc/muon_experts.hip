@@ -203,10 +203,11 @@ struct Side {
   static_assert(kPer * NW * 1024 == kPlane && !(DMA && DT != kBF16), "load split");
   Panel p;
   // Along: the lane's rows of the tile (of the matrix when gathered), or -1; for
-  // LDS-DMA their offsets.  Across, gathered: the matrix's rows of the next stage.
+  // buffer loads their offsets.  Across, gathered: the matrix's rows of the next stage.
   int row[kPer];
   u32x4_t q[DMA ? 1 : kPer][DT == kBF16 ? 1 : 2];             // loaded, not yet in LDS
   u32x4_t desc;                                               // LDS-DMA, along and gathered: the buffer
+  static constexpr bool kBuffer = !DMA && DT == kF32;         // loads into registers by buffer instructions
 
   // Place of the lane's piece u: row of the stage and 16-byte chunk in it.
   static __device__ __forceinline__ void place(int u, int wave, int lane, int& r, int& c) {
@@ -223,9 +224,9 @@ struct Side {
   }
   __device__ __forceinline__ void plan(const Panel& panel, int wave, int lane) {
     p = panel;
-    if constexpr (DMA) {
+    if constexpr (DMA || kBuffer) {
       const int n = p.tokens ? p.src : p.rows < ROWS ? p.rows : ROWS;
-      const int64_t bytes = (n - 1) * p.pitch + int64_t(p.cols) * 2;
+      const int64_t bytes = (n - 1) * p.pitch + int64_t(p.cols) * kES;
       desc = make_desc(p.base, static_cast<uint32_t>(bytes));
     }
     if constexpr (!ACROSS) {
@@ -234,8 +235,8 @@ struct Side {
         int r, c;
         place(u, wave, lane, r, c);
         row[u] = p.tokens ? source(r) : r < p.rows ? r : -1;
-        if constexpr (DMA)
-          row[u] = static_cast<int>(row[u] < 0 ? kPast : static_cast<uint32_t>(row[u]) * static_cast<uint32_t>(p.pitch) + c * 16);
+        if constexpr (DMA || kBuffer)
+          row[u] = static_cast<int>(row[u] < 0 ? kPast : static_cast<uint32_t>(row[u]) * static_cast<uint32_t>(p.pitch) + c * 8 * kES);
       }
     }
     look(0, wave, lane);
@@ -278,6 +279,43 @@ struct Side {
         issue(make_desc(p.base + k * p.pitch + p.c0 * 2, static_cast<uint32_t>(n - 1) * pitch + static_cast<uint32_t>(p.cols - p.c0) * 2),
               0, [&](int, int r, int c) { return static_cast<uint32_t>(r) * pitch + c * 16; });
       }
+    } else if constexpr (kBuffer) {
+      // whole pieces by buffer loads, which cost no address arithmetic and read as zeros
+      // where a row is not there; columns past the matrix are its next row's, of results
+      // that are not stored
+      const uint32_t pitch = static_cast<uint32_t>(p.pitch);
+      auto fetch = [&](const u32x4_t& d, int u, uint32_t voff, uint32_t soff) {
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            reinterpret_cast<void*>(static_cast<uint64_t>(d[1]) << 32 | d[0]), 0, static_cast<int>(d[2]), static_cast<int>(d[3]));
+        q[u][0] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, voff, soff, 0);
+        q[u][1] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, voff + 16, soff, 0);
+      };
+      if constexpr (ACROSS) {
+        const int n = p.rows - k < BK ? p.rows - k : BK;
+        const u32x4_t d = p.tokens ? desc
+                                   : make_desc(p.base + k * p.pitch, static_cast<uint32_t>(n - 1) * pitch + static_cast<uint32_t>(p.cols) * 4);
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          int r, c;
+          place(u, wave, lane, r, c);
+          const uint32_t at = (p.c0 + c * 8) * 4;
+          fetch(d, u, p.tokens ? (row[u] < 0 ? kPast : static_cast<uint32_t>(row[u]) * pitch + at) : static_cast<uint32_t>(r) * pitch + at, 0);
+        }
+      } else if (k + BK <= p.cols) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) fetch(desc, u, static_cast<uint32_t>(row[u]), static_cast<uint32_t>(k) * 4);
+      } else {
+        const uint8_t* base = p.base + static_cast<int64_t>(k) * 4;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          int r, c;
+          place(u, wave, lane, r, c);
+          const uint32_t voff = static_cast<uint32_t>(row[u]);
+          const uint32_t* from = reinterpret_cast<const uint32_t*>(base + (voff == kPast ? 0 : voff));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[u][i / 4][i % 4] = voff != kPast && k + c * 8 + i < p.cols ? glb(from)[i] : 0;
+        }
+      }
     } else {
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
@@ -293,27 +331,14 @@ struct Side {
         }
         const int n = at >= 0 ? p.cols - c : 0;      // elements of the chunk that are there
         const uint8_t* from = p.base + (n > 0 ? at * p.pitch + static_cast<int64_t>(c) * kES : 0);
-#pragma unroll
-        for (int i = 0; i < (DT == kBF16 ? 1 : 2); ++i) q[u][i] = u32x4_t{0, 0, 0, 0};
-        if constexpr (DT == kBF16) {
-          const uint16_t* s = reinterpret_cast<const uint16_t*>(from);
-          if (n >= 8) {
-            q[u][0] = load16b(s);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < n) q[u][0][i / 2] |= static_cast<uint32_t>(glb(s)[i]) << (16 * (i & 1));
-          }
+        q[u][0] = u32x4_t{0, 0, 0, 0};
+        const uint16_t* s = reinterpret_cast<const uint16_t*>(from);
+        if (n >= 8) {
+          q[u][0] = load16b(s);
         } else {
-          const uint32_t* s = reinterpret_cast<const uint32_t*>(from);
-          if (n >= 8) {
-            q[u][0] = load16b(s);
-            q[u][1] = load16b(s + 4);
-          } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < n) q[u][i / 4][i % 4] = glb(s)[i];
-          }
+          for (int i = 0; i < 8; ++i)
+            if (i < n) q[u][0][i / 2] |= static_cast<uint32_t>(glb(s)[i]) << (16 * (i & 1));
         }
       }
     }

@@ -145,7 +145,7 @@ inline int64_t expert_blocks(const ExpertArgs& a, int op, int tm, int tn) {
 // Bytes that a buffer's descriptor spans at most: an offset from here on reads as
 // zeros and, with the offset along a row added, stays below 2^32.
 constexpr uint32_t kExpertSpan = 0xf0000000u;
-// Longest rows (elements) that are loaded straight to LDS: 256 of them are in a span.
+// Largest row pitch (elements): a tile's 256 rows of bf16, 128 of fp32, are in a span.
 constexpr int64_t kExpertPitch = int64_t(1) << 22;
 // aligned: every row of the operands starts at 16 bytes (and holds whole ones along
 // the contraction), so that loads go straight to LDS

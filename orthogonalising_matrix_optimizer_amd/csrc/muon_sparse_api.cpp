@@ -126,7 +126,7 @@ SortArgs slots_sort(const void* choice, int id_bytes, const muon_slots& s, void*
 
 // Rows of 16-byte pieces that start at 16 bytes.
 bool pieces(const void* p, int64_t ld, int64_t inner) {
-  return !misaligned(p, 16) && ld % 8 == 0 && inner % 8 == 0 && ld <= kExpertPitch;
+  return !misaligned(p, 16) && ld % 8 == 0 && inner % 8 == 0;
 }
 
 // Shared checks of the three products: rows operand, columns operand, slots.
@@ -185,6 +185,7 @@ bool past_caches(const ExpertArgs& a, int op, int odt) {
 }
 
 int run_products(ExpertArgs a, int op, int dt, int odt, bool aligned, void* stream) {
+  if (std::max(a.ldr, a.ldc) > kExpertPitch) return MUON_E_SHAPE;
   a.past = past_caches(a, op, odt);
   const int tile = tile_of(a, op, dt, aligned);
   if (expert_blocks(a, op, tile, tile) > kMaxBlocks) return MUON_E_SHAPE;
