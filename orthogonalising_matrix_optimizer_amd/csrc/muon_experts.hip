@@ -255,7 +255,10 @@ struct Side {
     }
   }
   // Starts the loads of the stage from contraction element k on; with LDS-DMA to
-  // `lds`, else into registers.
+  // `lds`, else into registers.  LAST: the stage may end within the contraction's last
+  // piece.  (The caller branches, for both operands at once: a join of the two ways
+  // between their loads makes the compiler wait there for the loads just issued.)
+  template <bool LAST>
   __device__ __forceinline__ void load(int k, int wave, int lane, uint32_t lds) {
     if constexpr (DMA) {
       const uint32_t pitch = static_cast<uint32_t>(p.pitch);
@@ -301,7 +304,7 @@ struct Side {
           const uint32_t at = (p.c0 + c * 8) * 4;
           fetch(d, u, p.tokens ? (row[u] < 0 ? kPast : static_cast<uint32_t>(row[u]) * pitch + at) : static_cast<uint32_t>(r) * pitch + at, 0);
         }
-      } else if (k + BK <= p.cols) {
+      } else if constexpr (!LAST) {
 #pragma unroll
         for (int u = 0; u < kPer; ++u) fetch(desc, u, static_cast<uint32_t>(row[u]), static_cast<uint32_t>(k) * 4);
       } else {
@@ -521,8 +524,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
   static_assert(KK % 2 == 0 && (DMA || NST == 2), "steps and stages");
   auto load = [&](int k, int slot) {     // LDS-DMA: all the way; else into registers
     if (k >= stages) return;
-    rows.load(k * BK, wave, lane, lds + slot * kStage);
-    cols.load(k * BK, wave, lane, lds + slot * kStage + Rows::kBytes);
+    if (OP == kExpertDw || DMA || (k + 1) * BK <= depth) {
+      rows.template load<false>(k * BK, wave, lane, lds + slot * kStage);
+      cols.template load<false>(k * BK, wave, lane, lds + slot * kStage + Rows::kBytes);
+    } else {
+      rows.template load<true>(k * BK, wave, lane, lds + slot * kStage);
+      cols.template load<true>(k * BK, wave, lane, lds + slot * kStage + Rows::kBytes);
+    }
     rows.look((k + 1) * BK, wave, lane);
     cols.look((k + 1) * BK, wave, lane);
   };
