@@ -254,11 +254,18 @@ struct Side {
       }
     }
   }
+  // Whether the stage from contraction element k on is all there, so that its pieces
+  // are loaded whole without a look at each.
+  __device__ __forceinline__ bool whole(int k) const {
+    if constexpr (DMA || (kBuffer && ACROSS)) return true;
+    else if constexpr (ACROSS) return k + BK <= p.rows && p.c0 + ROWS <= p.cols;
+    else return k + BK <= p.cols;
+  }
   // Starts the loads of the stage from contraction element k on; with LDS-DMA to
-  // `lds`, else into registers.  LAST: the stage may end within the contraction's last
-  // piece.  (The caller branches, for both operands at once: a join of the two ways
-  // between their loads makes the compiler wait there for the loads just issued.)
-  template <bool LAST>
+  // `lds`, else into registers.  (The caller branches on WHOLE, for both operands at
+  // once: a join of the two ways between their loads makes the compiler wait there
+  // for the loads just issued.)
+  template <bool WHOLE>
   __device__ __forceinline__ void load(int k, int wave, int lane, uint32_t lds) {
     if constexpr (DMA) {
       const uint32_t pitch = static_cast<uint32_t>(p.pitch);
@@ -304,7 +311,7 @@ struct Side {
           const uint32_t at = (p.c0 + c * 8) * 4;
           fetch(d, u, p.tokens ? (row[u] < 0 ? kPast : static_cast<uint32_t>(row[u]) * pitch + at) : static_cast<uint32_t>(r) * pitch + at, 0);
         }
-      } else if constexpr (!LAST) {
+      } else if constexpr (WHOLE) {
 #pragma unroll
         for (int u = 0; u < kPer; ++u) fetch(desc, u, static_cast<uint32_t>(row[u]), static_cast<uint32_t>(k) * 4);
       } else {
@@ -318,6 +325,22 @@ struct Side {
 #pragma unroll
           for (int i = 0; i < 8; ++i) q[u][i / 4][i % 4] = voff != kPast && k + c * 8 + i < p.cols ? glb(from)[i] : 0;
         }
+      }
+    } else if constexpr (WHOLE) {
+      // rows of the tile that are not there read as its first: their results are not
+      // stored; a gathered row without a token is masked
+      const uint8_t* base = ACROSS ? (p.tokens ? p.base : p.base + k * p.pitch) + p.c0 * 2 : p.base + k * 2;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        int r, c;
+        place(u, wave, lane, r, c);
+        const int at = ACROSS && !p.tokens ? r : row[u] < 0 ? 0 : row[u];
+        q[u][0] = load16b(reinterpret_cast<const uint16_t*>(base + static_cast<uint64_t>(static_cast<uint32_t>(at)) * static_cast<uint32_t>(p.pitch) + c * 16));
+      }
+      if (p.tokens) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u)
+          if (row[u] < 0) q[u][0] = u32x4_t{0, 0, 0, 0};
       }
     } else {
 #pragma unroll
@@ -524,12 +547,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
   static_assert(KK % 2 == 0 && (DMA || NST == 2), "steps and stages");
   auto load = [&](int k, int slot) {     // LDS-DMA: all the way; else into registers
     if (k >= stages) return;
-    if (OP == kExpertDw || DMA || (k + 1) * BK <= depth) {
-      rows.template load<false>(k * BK, wave, lane, lds + slot * kStage);
-      cols.template load<false>(k * BK, wave, lane, lds + slot * kStage + Rows::kBytes);
-    } else {
+    if (rows.whole(k * BK) && cols.whole(k * BK)) {
       rows.template load<true>(k * BK, wave, lane, lds + slot * kStage);
       cols.template load<true>(k * BK, wave, lane, lds + slot * kStage + Rows::kBytes);
+    } else {
+      rows.template load<false>(k * BK, wave, lane, lds + slot * kStage);
+      cols.template load<false>(k * BK, wave, lane, lds + slot * kStage + Rows::kBytes);
     }
     rows.look((k + 1) * BK, wave, lane);
     cols.look((k + 1) * BK, wave, lane);
