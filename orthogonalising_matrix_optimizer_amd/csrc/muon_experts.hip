@@ -178,6 +178,24 @@ __device__ __forceinline__ void split8(const float* v, u32x4_t& h, u32x4_t& m, u
   l = narrow8(r);
 }
 
+// A piece of eight bf16 elements moved down by n elements (0 .. 8), zeros behind.
+__device__ __forceinline__ u32x4_t moved(u32x4_t q, int n) {
+  const bool one = n & 1, two = n & 2, four = n & 4;
+  u32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t next = i < 3 ? q[i + 1] : 0;
+    r[i] = one ? q[i] >> 16 | next << 16 : q[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = two ? (i < 3 ? r[i + 1] : 0) : r[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = four ? (i < 2 ? r[i + 2] : 0) : r[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = n >= 8 ? 0 : r[i];
+  return r;
+}
+
 // What a block takes of one operand.
 struct Panel {
   const uint8_t* base;   // along: the tile's first row (gathered: the matrix); across: the expert's first row
@@ -206,6 +224,8 @@ struct Side {
   // buffer loads their offsets.  Across, gathered: the matrix's rows of the next stage.
   int row[kPer];
   u32x4_t q[DMA ? 1 : kPer][DT == kBF16 ? 1 : 2];             // loaded, not yet in LDS
+  int move[DMA || DT == kF32 ? 1 : kPer];                     // of bf16 in registers: see load()
+  bool moves;
   u32x4_t desc;                                               // LDS-DMA, along and gathered: the buffer
   static constexpr bool kBuffer = !DMA && DT == kF32;         // loads into registers by buffer instructions
 
@@ -326,47 +346,35 @@ struct Side {
           for (int i = 0; i < 8; ++i) q[u][i / 4][i % 4] = voff != kPast && k + c * 8 + i < p.cols ? glb(from)[i] : 0;
         }
       }
-    } else if constexpr (WHOLE) {
-      // rows of the tile that are not there read as its first: their results are not
-      // stored; a gathered row without a token is masked
-      const uint8_t* base = ACROSS ? (p.tokens ? p.base : p.base + k * p.pitch) + p.c0 * 2 : p.base + k * 2;
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        int r, c;
-        place(u, wave, lane, r, c);
-        const int at = ACROSS && !p.tokens ? r : row[u] < 0 ? 0 : row[u];
-        q[u][0] = load16b(reinterpret_cast<const uint16_t*>(base + static_cast<uint64_t>(static_cast<uint32_t>(at)) * static_cast<uint32_t>(p.pitch) + c * 16));
-      }
-      if (p.tokens) {
-#pragma unroll
-        for (int u = 0; u < kPer; ++u)
-          if (row[u] < 0) q[u][0] = u32x4_t{0, 0, 0, 0};
-      }
     } else {
+      // A row of the tile that is not there reads as its first, a piece that the row's
+      // end cuts as the row's last eight elements: put() moves them down, and zeroes what
+      // is no element.  (Results of columns past the matrix are not stored.)
+      bool any = false;
+      const uint8_t* base = ACROSS && !p.tokens ? p.base + k * p.pitch : p.base;
+      const int c0 = ACROSS ? p.c0 : k, last = p.cols - 8;
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
         int r, c;
         place(u, wave, lane, r, c);
-        int64_t at;
-        if constexpr (ACROSS) {
-          at = p.tokens ? row[u] : k + r < p.rows ? k + r : -1;
-          c = p.c0 + c * 8;
-        } else {
-          at = row[u];
-          c = k + c * 8;
-        }
-        const int n = at >= 0 ? p.cols - c : 0;      // elements of the chunk that are there
-        const uint8_t* from = p.base + (n > 0 ? at * p.pitch + static_cast<int64_t>(c) * kES : 0);
-        q[u][0] = u32x4_t{0, 0, 0, 0};
-        const uint16_t* s = reinterpret_cast<const uint16_t*>(from);
-        if (n >= 8) {
+        c = c0 + c * 8;
+        int at = ACROSS && !p.tokens ? (WHOLE || k + r < p.rows ? r : -1) : row[u];
+        const int from = WHOLE || c <= last ? c : last < 0 ? 0 : last;
+        move[u] = at < 0 ? 8 : WHOLE ? 0 : c - from < 8 ? c - from : 8;
+        any = any || at < 0;
+        at = at < 0 ? 0 : at;
+        const uint16_t* s = reinterpret_cast<const uint16_t*>(
+            base + static_cast<uint64_t>(static_cast<uint32_t>(at)) * static_cast<uint32_t>(p.pitch)) + from;
+        if (WHOLE || last >= 0) {
           q[u][0] = load16b(s);
-        } else {
+        } else {   // rows of less than eight elements
+          q[u][0] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i < n) q[u][0][i / 2] |= static_cast<uint32_t>(glb(s)[i]) << (16 * (i & 1));
+          for (int i = 0; i < 7; ++i)
+            if (i < p.cols) q[u][0][i / 2] |= static_cast<uint32_t>(glb(s)[i]) << (16 * (i & 1));
         }
       }
+      moves = !WHOLE || __ballot(any) != 0;
     }
   }
   // Writes what load() brought into registers to a stage in LDS.
@@ -376,7 +384,7 @@ struct Side {
       for (int u = 0; u < kPer; ++u) {
         uint8_t* to = stage + (wave + NW * u) * 1024 + lane * 16;
         if constexpr (DT == kBF16) {
-          *reinterpret_cast<u32x4_t*>(to) = q[u][0];
+          *reinterpret_cast<u32x4_t*>(to) = moves ? moved(q[u][0], move[u]) : q[u][0];
         } else {
           float v[8];
 #pragma unroll
