@@ -23,9 +23,9 @@
 // end.  All others are loaded into registers and checked there.  fp32 operands
 // are split there into three bf16 terms h + m + l, each the rounding of what the
 // terms before leave (24 bits in all), and six of the nine products of terms
-// are summed, the largest left out being m l with 2^-26 of h h: an fp32 product
-// in six bf16 matrix instructions, which together run at 2.7 times the rate of
-// the fp32 matrix instruction.
+// are summed, the largest left out being m l with at most 2^-24 of h h: an fp32
+// product in six bf16 matrix instructions, which together run at 2.7 times the rate
+// of the fp32 matrix instruction.
 //
 // The four results that the matrix instruction leaves in consecutive registers
 // are rows of its first operand, which is that of the output's columns.  Its 32
@@ -221,8 +221,9 @@ struct Side {
   static_assert(kPer * NW * 1024 == kPlane && !(DMA && DT != kBF16), "load split");
   Panel p;
   // Along: the lane's rows of the tile (of the matrix when gathered), or -1; for
-  // buffer loads their offsets.  Across, gathered: the matrix's rows of the next stage.
-  int row[kPer];
+  // buffer loads their offsets.
+  int row[ACROSS ? 1 : kPer];
+  int next;               // across, gathered: one of the wave's rows of the next stage, see look()
   u32x4_t q[DMA ? 1 : kPer][DT == kBF16 ? 1 : 2];             // loaded, not yet in LDS
   int move[DMA || DT == kF32 ? 1 : kPer];                     // of bf16 in registers: see load()
   bool moves;
@@ -261,18 +262,19 @@ struct Side {
     }
     look(0, wave, lane);
   }
-  // Across, gathered: finds the rows of the stage from contraction row k on.
+  // Across, gathered: finds the rows of the stage from contraction row k on, each by
+  // one lane (row i % kRows of the wave's piece i / kRows).
+  static constexpr int kRows = ACROSS ? 512 / ROWS : 1;       // rows of a piece
+  static_assert(kPer * kRows <= 64, "a lane for each row");
   __device__ __forceinline__ void look(int k, int wave, int lane) {
     if constexpr (ACROSS) {
-      if (p.tokens && k < p.rows) {
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-          int r, c;
-          place(u, wave, lane, r, c);
-          row[u] = source(k + r);
-        }
-      }
+      if (p.tokens && k < p.rows && lane < kPer * kRows) next = source(k + (wave + NW * (lane / kRows)) * kRows + lane % kRows);
     }
+  }
+  // The matrix's row of the lane's piece u, or -1.
+  __device__ __forceinline__ int found(int u, int lane) const {
+    if constexpr (ACROSS) return __shfl(next, u * kRows + lane / (64 / kRows), 64);
+    else return row[u];
   }
   // Whether the stage from contraction element k on is all there, so that its pieces
   // are loaded whole without a look at each.
@@ -302,7 +304,8 @@ struct Side {
         issue(desc, static_cast<uint32_t>(k) * 2, [&](int u, int, int c) { return c * 8 < left ? static_cast<uint32_t>(row[u]) : kPast; });
       } else if (p.tokens) {
         issue(desc, 0, [&](int u, int, int c) {
-          return row[u] >= 0 && p.c0 + c * 8 < p.cols ? static_cast<uint32_t>(row[u]) * pitch + (p.c0 + c * 8) * 2 : kPast;
+          const int at = found(u, lane);
+          return at >= 0 && p.c0 + c * 8 < p.cols ? static_cast<uint32_t>(at) * pitch + (p.c0 + c * 8) * 2 : kPast;
         });
       } else {
         const int n = p.rows - k < BK ? p.rows - k : BK;
@@ -329,7 +332,8 @@ struct Side {
           int r, c;
           place(u, wave, lane, r, c);
           const uint32_t at = (p.c0 + c * 8) * 4;
-          fetch(d, u, p.tokens ? (row[u] < 0 ? kPast : static_cast<uint32_t>(row[u]) * pitch + at) : static_cast<uint32_t>(r) * pitch + at, 0);
+          const int from = p.tokens ? found(u, lane) : r;
+          fetch(d, u, from < 0 ? kPast : static_cast<uint32_t>(from) * pitch + at, 0);
         }
       } else if constexpr (WHOLE) {
 #pragma unroll
@@ -358,7 +362,7 @@ struct Side {
         int r, c;
         place(u, wave, lane, r, c);
         c = c0 + c * 8;
-        int at = ACROSS && !p.tokens ? (WHOLE || k + r < p.rows ? r : -1) : row[u];
+        int at = ACROSS && !p.tokens ? (WHOLE || k + r < p.rows ? r : -1) : found(u, lane);
         const int from = WHOLE || c <= last ? c : last < 0 ? 0 : last;
         move[u] = at < 0 ? 8 : WHOLE ? 0 : c - from < 8 ? c - from : 8;
         any = any || at < 0;
