@@ -548,11 +548,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
       cols.plan({w, a.ldc * es, nullptr, 0, depth, a.cols, tile.c0}, wave, lane);
   }
 
-  f32x16_t acc[FN][FM];
+  // fp32: the products of the first terms have sums of their own, so that the five
+  // smaller ones of each step add nothing to their rounding
+  constexpr int SETS = PL == 1 ? 1 : 2;
+  f32x16_t acc[SETS][FN][FM];
 #pragma unroll
-  for (int i = 0; i < FN; ++i)
+  for (int n = 0; n < SETS; ++n)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = f32x16_t{};
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[n][i][j] = f32x16_t{};
 
   const int stages = (depth + BK - 1) / BK;
   constexpr int PER = Rows::kPer + Cols::kPer, KK = BK / 16;
@@ -597,7 +602,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
         for (int i = 0; i < FN; ++i)
 #pragma unroll
           for (int j = 0; j < FM; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g.c[p][i], g.r[o][j], acc[i][j], 0, 0, 0);
+            acc[sum ? 1 : 0][i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g.c[p][i], g.r[o][j], acc[sum ? 1 : 0][i][j], 0, 0, 0);
       }
   };
   if (stages) {
@@ -639,6 +644,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
     __builtin_amdgcn_sched_barrier(0);
   }
 
+  if constexpr (SETS > 1) {
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[0][i][j] += acc[SETS - 1][i][j];
+  }
   const int most = OP == kExpertDw ? a.rows : tile.hi - tile.lo;
   T* out = static_cast<T*>(a.out) + (OP == kExpertDw ? tile.e * a.ostride : tile.lo * a.ldo);
   if (OP == kExpertDw && a.accumulate) {
@@ -651,7 +662,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
         const int c = tile.c0 + (wn * FN + i) * 32 + 16 * (lane >> 5);
         float v[16];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) v[q] = acc[i][j][q];
+        for (int q = 0; q < 16; ++q) v[q] = acc[0][i][j][q];
         if (r < most && c < a.cols) add16(out + r * a.ldo + c, v, a.cols - c);
       }
     }
@@ -672,7 +683,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
         for (int n = 0; n < 4; ++n) {
           float w[8];
 #pragma unroll
-          for (int e = 0; e < EACH; ++e) w[e] = PAIR ? acc[i + n / 2 * PAIR][j][8 * (n & 1) + e] : acc[i][j][(4 * n + e) & 15];
+          for (int e = 0; e < EACH; ++e) w[e] = PAIR ? acc[0][i + n / 2 * PAIR][j][8 * (n & 1) + e] : acc[0][i][j][(4 * n + e) & 15];
           if constexpr (PAIR) q[n] = narrow8(w);
           else q[n] = bits4(w);
         }
@@ -689,7 +700,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
         for (int n = 0; n < 2; ++n) {
           float w[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = acc[i][j][8 * n + e];
+          for (int e = 0; e < 8; ++e) w[e] = acc[0][i][j][8 * n + e];
           if (r < most && c + 8 * n < a.cols) put_piece(out + r * a.ldo + c + 8 * n, narrow8(w), a.cols - c - 8 * n, a.past);
         }
       }
