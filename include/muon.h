@@ -590,7 +590,13 @@ int muon_route_grad(const float* dgates, const muon_mat* logits, const float* ga
  *   linear_dx: dx[r]  = dy[r] w[e(r)]                  (slots x in)
  *   linear_dw: dw[e]  = sum over e's rows dy[r]^T x[r] (out x in; zeros without
  *              rows), added to dw with `accumulate`.
- * Rows behind the last expert's are left as they were. */
+ * Rows behind the last expert's are left as they were.
+ * Where few tiles of dw meet many rows, parts of the rows are summed by tiles of their
+ * own and joined in order: linear_dw_workspace_bytes(slots, dw) of device memory, 16-byte
+ * aligned, used until the call's work is done (0 where nothing is split).  For
+ * experiments and tests MUON_EXPERT_TILE=64|128|256 (read at every call) forces the
+ * tile's width of calls that do not split (256 only for bf16 rows whose addresses and
+ * pitches are multiples of 16 bytes). */
 int muon_expert_linear(const muon_mat* x, const muon_stack* w, const muon_slots* slots,
                        int32_t gather, const muon_mat* out, void* stream);
 int muon_expert_linear_dx(const muon_mat* dy, const muon_stack* w, const muon_slots* slots,

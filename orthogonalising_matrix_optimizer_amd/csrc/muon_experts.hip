@@ -53,7 +53,8 @@ constexpr int kBatch = 64;                // experts looked at at once
 // ---- the tile of a block
 struct Tile {
   int e;        // expert
-  int lo, hi;   // its rows
+  int part;     // dw: where the results go: the expert, or the part of one
+  int lo, hi;   // its rows (of a part: the part's)
   int r0, c0;   // first row (fwd, dx: from lo; dw: of the matrix) and column
   bool any;
 };
@@ -77,43 +78,69 @@ __device__ __forceinline__ int sum_below(int v, int lane) {
   return v;
 }
 
-// fwd, dx: tiles of TM rows, expert by expert, all columns of a row tile after
-// each other; XCD x (blocks x, x + 8, ..) has the x-th eighth.
-template <int TM, int TN>
-__device__ __forceinline__ Tile row_tile(const ExpertArgs& a, int lane) {
-  const int across = (a.cols + TN - 1) / TN;
-  auto tiles_of = [&](int e) {
-    int lo = 0, hi = 0;
-    if (e < a.experts) rows_of(a, e, lo, hi);
-    return (hi - lo + TM - 1) / TM;
-  };
+// The experts' rows in pieces of `per`, expert by expert, `across` items a piece:
+// XCD x (blocks x, x + 8, ..) has the x-th eighth of the items.
+struct Found {
+  int e, piece, index, rest;   // expert, piece of it and of all, item of the piece
+  bool any;
+};
+__device__ __forceinline__ int pieces_of(const ExpertArgs& a, int e, int per) {
+  int lo = 0, hi = 0;
+  if (e < a.experts) rows_of(a, e, lo, hi);
+  return (hi - lo + per - 1) / per;
+}
+__device__ __forceinline__ Found find_piece(const ExpertArgs& a, int per, int across, int lane) {
   int all = 0;
-  for (int e0 = 0; e0 < a.experts; e0 += kBatch) all += __shfl(sum_below(tiles_of(e0 + lane), lane), 63, 64);
+  for (int e0 = 0; e0 < a.experts; e0 += kBatch) all += __shfl(sum_below(pieces_of(a, e0 + lane, per), lane), 63, 64);
   const int64_t items = static_cast<int64_t>(all) * across;
   const int x = blockIdx.x & 7;
   const int64_t item = items * x / 8 + (blockIdx.x >> 3);
-  Tile t{0, 0, 0, 0, 0, false};
-  if (item >= items * (x + 1) / 8) return t;
-  int want = static_cast<int>(item / across);
-  t.c0 = static_cast<int>(item % across) * TN;
+  Found f{0, 0, 0, 0, false};
+  if (item >= items * (x + 1) / 8) return f;
+  f.index = __builtin_amdgcn_readfirstlane(static_cast<int>(item / across));
+  f.rest = __builtin_amdgcn_readfirstlane(static_cast<int>(item % across));
+  int want = f.index;
   for (int e0 = 0; e0 < a.experts; e0 += kBatch) {
-    const int own = tiles_of(e0 + lane), upto = sum_below(own, lane);
+    const int own = pieces_of(a, e0 + lane, per), upto = sum_below(own, lane);
     const uint64_t past = __ballot(upto > want);
     if (past) {
       const int l = __builtin_ctzll(past);
-      t.e = e0 + l;
-      t.r0 = (want - __shfl(upto - own, l, 64)) * TM;
-      t.any = true;
+      f.e = __builtin_amdgcn_readfirstlane(e0 + l);
+      f.piece = __builtin_amdgcn_readfirstlane(want - __shfl(upto - own, l, 64));
+      f.any = true;
       break;
     }
     want -= __shfl(upto, 63, 64);
   }
-  t.e = __builtin_amdgcn_readfirstlane(t.e);
-  t.r0 = __builtin_amdgcn_readfirstlane(t.r0);
-  t.c0 = __builtin_amdgcn_readfirstlane(t.c0);
-  rows_of(a, t.e, t.lo, t.hi);
-  t.lo = __builtin_amdgcn_readfirstlane(t.lo);
-  t.hi = __builtin_amdgcn_readfirstlane(t.hi);
+  return f;
+}
+
+// fwd, dx: tiles of TM rows, all columns of a row tile after each other.
+template <int TM, int TN>
+__device__ __forceinline__ Tile row_tile(const ExpertArgs& a, int lane) {
+  const Found f = find_piece(a, TM, (a.cols + TN - 1) / TN, lane);
+  Tile t{f.e, 0, 0, 0, f.piece * TM, f.rest * TN, f.any};
+  if (t.any) {
+    rows_of(a, t.e, t.lo, t.hi);
+    t.lo = __builtin_amdgcn_readfirstlane(t.lo);
+    t.hi = __builtin_amdgcn_readfirstlane(t.hi);
+  }
+  return t;
+}
+
+// dw with split contractions: parts of a.chunk rows, all tiles of a part after each
+// other.
+template <int TM, int TN>
+__device__ __forceinline__ Tile part_tile(const ExpertArgs& a, int lane) {
+  const int across = (a.cols + TN - 1) / TN, tiles = (a.rows + TM - 1) / TM * across;
+  const Found f = find_piece(a, a.chunk, tiles, lane);
+  Tile t{f.e, f.index, 0, 0, f.rest / across * TM, f.rest % across * TN, f.any && f.index < a.parts};
+  if (t.any) {
+    rows_of(a, t.e, t.lo, t.hi);
+    t.lo = __builtin_amdgcn_readfirstlane(t.lo) + f.piece * a.chunk;
+    t.hi = __builtin_amdgcn_readfirstlane(t.hi);
+    t.hi = t.hi < t.lo + a.chunk ? t.hi : t.lo + a.chunk;
+  }
   return t;
 }
 
@@ -127,7 +154,7 @@ __device__ __forceinline__ Tile matrix_tile(const ExpertArgs& a) {
   const int share = (tiles + 7) / 8;
   const int i = blockIdx.x >> 3, e = i / share;
   const int at = ((blockIdx.x + e) & 7) * share + i % share;
-  Tile t{e, 0, 0, at / across * TM, at % across * TN, e < a.experts && at < tiles};
+  Tile t{e, e, 0, 0, at / across * TM, at % across * TN, e < a.experts && at < tiles};
   if (t.any) {
     rows_of(a, e, t.lo, t.hi);
     t.lo = __builtin_amdgcn_readfirstlane(t.lo);
@@ -524,7 +551,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
   const int wm = wave / WN, wn = wave % WN;
 
   Tile tile;
-  if constexpr (OP == kExpertDw) tile = matrix_tile<TM, TN>(a);
+  if constexpr (OP == kExpertDw) tile = a.chunk ? part_tile<TM, TN>(a, lane) : matrix_tile<TM, TN>(a);
   else tile = row_tile<TM, TN>(a, lane);
   if (!tile.any) return;
   const int depth = OP == kExpertDw ? tile.hi - tile.lo : a.depth;
@@ -651,8 +678,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
       for (int j = 0; j < FM; ++j) acc[0][i][j] += acc[SETS - 1][i][j];
   }
   const int most = OP == kExpertDw ? a.rows : tile.hi - tile.lo;
-  T* out = static_cast<T*>(a.out) + (OP == kExpertDw ? tile.e * a.ostride : tile.lo * a.ldo);
-  if (OP == kExpertDw && a.accumulate) {
+  T* out = static_cast<T*>(a.out) + (OP == kExpertDw ? tile.part * a.ostride : tile.lo * a.ldo);
+  if (OP == kExpertDw && a.accumulate && !a.chunk) {
     if (depth == 0) return;
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
@@ -744,7 +771,64 @@ hipError_t launch_op(const ExpertArgs& a, int dt, bool aligned, int tile, hipStr
   return launch_tiles<OP, kBF16, true, T, 256, 256, 2, 4, 64, 2>(a, s);
 }
 
+// Sums the parts of the experts' split contractions in order: a block takes 2048
+// elements of expert blockIdx.y's matrix, a thread eight of a row.
+template <class T>
+__global__ __launch_bounds__(256) void k_experts_join(ExpertArgs a, const float* in, T* out, int64_t ldo, int64_t ostride,
+                                                     bool whole) {
+  const int e = blockIdx.y, lane = threadIdx.x & 63;
+  int first = 0;
+  for (int e0 = 0; e0 < e; e0 += kBatch)
+    first += __shfl(sum_below(e0 + lane < e ? pieces_of(a, e0 + lane, a.chunk) : 0, lane), 63, 64);
+  int last = first + pieces_of(a, e, a.chunk);
+  last = last < a.parts ? last : a.parts;
+  if (a.accumulate && first >= last) return;
+  const int wide = (a.cols + 7) / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int r = static_cast<int>(i / wide), c = static_cast<int>(i - static_cast<int64_t>(r) * wide) * 8;
+  if (r >= a.rows) return;
+  float v[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = 0.f;
+  const float* from = in + r * a.ldo + c;
+#pragma unroll 4
+  for (int p = first; p < last; ++p) {
+    float w[8];
+    load8(from + p * a.ostride, w);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] += w[q];
+  }
+  T* o = out + e * ostride + r * ldo + c;
+  if (whole && c + 8 <= a.cols) {
+    if (a.accumulate) {
+      float w[8];
+      load8(o, w);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += w[q];
+    }
+    store8(o, v);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (c + q < a.cols) store1(o + q, a.accumulate ? load1(o + q) + v[q] : v[q]);
+  }
+}
+
 }  // namespace
+
+hipError_t launch_experts_join(const ExpertArgs& a, void* out, int64_t ldo, int64_t ostride, int odt, hipStream_t s) {
+  const unsigned blocks = static_cast<unsigned>((int64_t(a.rows) * ((a.cols + 7) / 8) + 255) / 256);
+  const float* in = static_cast<const float*>(a.out);
+  const int64_t size = odt == kBF16 ? 2 : 4;
+  const bool whole = ((reinterpret_cast<uintptr_t>(out) | ldo * size | ostride * size) & 15) == 0;
+  if (odt == kBF16)
+    hipLaunchKernelGGL((k_experts_join<uint16_t>), dim3(blocks, a.experts), dim3(256), 0, s, a, in,
+                       static_cast<uint16_t*>(out), ldo, ostride, whole);
+  else
+    hipLaunchKernelGGL((k_experts_join<float>), dim3(blocks, a.experts), dim3(256), 0, s, a, in,
+                       static_cast<float*>(out), ldo, ostride, whole);
+  return hipGetLastError();
+}
 
 hipError_t launch_experts(const ExpertArgs& a, int op, int dt, int odt, bool aligned, int tile, hipStream_t s) {
   auto with = [&](auto z) {

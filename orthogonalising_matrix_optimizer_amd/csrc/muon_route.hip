@@ -8,8 +8,9 @@
 // the order depends on nothing but the keys.  A position goes to
 //   (positions with smaller digits) + (equal digits in earlier blocks)
 //   + (in earlier waves of the block) + (earlier in the wave).
-// Up to 32 blocks, each counts the digits of all keys itself, which costs less
-// than a launch of its own for it; beyond, a launch writes the blocks' counts.
+// Up to kSortSelf blocks, each counts the digits of all keys itself, which costs
+// less than a launch of its own for it; beyond, a launch writes the blocks' counts
+// (us a pass with 16 blocks: 18.6 | 9.8).
 #include <type_traits>
 
 #include "muon_common.h"

@@ -130,6 +130,8 @@ struct ExpertArgs {
   int32_t src;              // rows of x when gathered
   int32_t accumulate;       // dw
   int32_t past;             // write past the caches
+  int32_t chunk, parts;     // dw: rows of a part of a split contraction (0: none are
+                            // split), parts that out has room for
 };
 // Blocks of a launch with tm x tn tiles.  How the slots are split is known to the
 // device alone: a full tile for every tm slots and a part of one an expert at most.
@@ -137,6 +139,7 @@ inline int64_t expert_blocks(const ExpertArgs& a, int op, int tm, int tn) {
   const int64_t across = (int64_t(a.cols) + tn - 1) / tn;
   if (op == kExpertDw) {
     const int64_t tiles = (int64_t(a.rows) + tm - 1) / tm * across;
+    if (a.chunk) return 8 * ((tiles * a.parts + 7) / 8);
     return 8 * a.experts * ((tiles + 7) / 8);
   }
   const int64_t tiles = a.slots / tm + (a.experts < a.slots ? a.experts : a.slots);
@@ -151,5 +154,8 @@ constexpr int64_t kExpertPitch = int64_t(1) << 22;
 // the contraction), so that loads go straight to LDS
 // tile: 64, 128 or, aligned, 256
 hipError_t launch_experts(const ExpertArgs& a, int op, int dt, int odt, bool aligned, int tile, hipStream_t s);
+
+// Sums a.parts parts that a launch with a.chunk wrote to a.out into the experts' matrices.
+hipError_t launch_experts_join(const ExpertArgs& a, void* out, int64_t ldo, int64_t ostride, int odt, hipStream_t s);
 
 }  // namespace muon

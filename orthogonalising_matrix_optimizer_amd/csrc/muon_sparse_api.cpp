@@ -154,6 +154,7 @@ bool spans(const muon_mat& x) {
 // | 52 | 61; 48 slots, 64 experts, 2048 -> 1408: 37 | 32 | 49, 12000: 170 | 128 | 131; fp32
 // 8192 slots, 32 experts, 1024 -> 1024: 150 | 142; 32768, 8, 2048 -> 1024: 1079 | 804.
 int tile_of(const ExpertArgs& a, int op, int dt, bool aligned) {
+  if (a.chunk) return 64;
   if (const char* e = std::getenv("MUON_EXPERT_TILE")) {
     const int t = std::atoi(e);
     if (t == 64 || t == 128 || (t == 256 && aligned)) return t;
@@ -190,6 +191,32 @@ int run_products(ExpertArgs a, int op, int dt, int odt, bool aligned, void* stre
   const int tile = tile_of(a, op, dt, aligned);
   if (expert_blocks(a, op, tile, tile) > kMaxBlocks) return MUON_E_SHAPE;
   return launch_experts(a, op, dt, odt, aligned, tile, static_cast<hipStream_t>(stream)) == hipSuccess ? MUON_OK : MUON_E_HIP;
+}
+
+// Contractions of dw that are split: where an expert has few tiles and many rows, the
+// chip would stand idle while each tile goes through all of its expert's rows.  Parts
+// of `chunk` rows have fp32 results of their own that a second launch sums in order.
+// A stage of 64 rows takes about 0.8 us, the second launch 6 us, a 64 x 64 tile of a
+// part 0.011 us to write and read again; of the two the sum is least where both are
+// alike.  us of a call, whole | split: 2 experts of 2048 rows, 256 x 128: 22 | 13 (fp32 57 |
+// 16); 1 of 16384, 128 x 128: 182 | 23; 8 of 2048, 512 x 256: 29 | 26, and, left whole
+// by the rule, 8 of 2048, 256 x 1024: 34 | 39, 16 of 512, 256 x 256: 9.5 | 18.
+struct Split {
+  int64_t chunk = 0, parts = 0, ld = 0;
+  size_t bytes = 0;
+};
+Split plan_split(int64_t slots, const muon_stack& dw) {
+  Split p;
+  const int64_t tiles = ceil_div(dw.rows, 64) * ceil_div(dw.cols, 64), each = slots / dw.count;
+  if (tiles == 0) return p;
+  const double sum = double(slots) * double(tiles);
+  const int64_t chunk = ceil_div(int64_t(std::max(std::sqrt(0.88 * sum), sum / 768)) + 1, 64) * 64;
+  if (0.8 * chunk / 64 + 6 + 0.011 * sum / chunk >= 0.8 * each / 64) return p;
+  p.chunk = chunk;
+  p.parts = slots / chunk + dw.count;
+  p.ld = int64_t(round_up(size_t(dw.cols), 8));
+  p.bytes = size_t(p.parts) * dw.rows * p.ld * 4;
+  return p;
 }
 
 int check_gates(const float* gates, const muon_slots& s, std::vector<Span>& v, bool write) {
@@ -368,7 +395,12 @@ int muon_expert_linear_dx(const muon_mat* dy, const muon_stack* w, const muon_sl
   return MUON_E_HIP;
 }
 
-size_t muon_expert_linear_dw_workspace_bytes(int64_t, const muon_stack*) { return 0; }
+size_t muon_expert_linear_dw_workspace_bytes(int64_t slots, const muon_stack* dw) {
+  if (!dw || slots < 0 || slots > MUON_MAX_SLOTS || dw->count < 1 || dw->count > MUON_MAX_EXPERTS || dw->rows < 0 ||
+      dw->rows > kMaxCols || dw->cols < 0 || dw->cols > kMaxCols)
+    return 0;
+  return plan_split(slots, *dw).bytes;
+}
 
 int muon_expert_linear_dw(const muon_mat* dy, const muon_mat* x, const muon_slots* slots,
                           int32_t gather, int32_t accumulate, const muon_stack* dw,
@@ -385,6 +417,8 @@ int muon_expert_linear_dw(const muon_mat* dy, const muon_mat* x, const muon_slot
     return MUON_E_SHAPE;
   add_span(v, *x, false);
   add_span(v, *dw, true);
+  const Split split = plan_split(n, *dw);
+  if ((rc = check_workspace(v, workspace, workspace_bytes, split.bytes)) != MUON_OK) return rc;
   if (conflict(v)) return MUON_E_ALIAS;
   if (dw->rows == 0 || dw->cols == 0) return MUON_OK;
   ExpertArgs a;
@@ -405,7 +439,15 @@ int muon_expert_linear_dw(const muon_mat* dy, const muon_mat* x, const muon_slot
   a.src = int32_t(x->rows);
   a.accumulate = accumulate != 0;
   const bool aligned = x->dtype == MUON_BF16 && pieces(dy->ptr, dy->ld, dy->cols) && pieces(x->ptr, x->ld, x->cols);
-  return run_products(a, kExpertDw, x->dtype, dw->dtype, aligned, stream);
+  if (!split.chunk) return run_products(a, kExpertDw, x->dtype, dw->dtype, aligned, stream);
+  a.out = workspace;
+  a.ldo = split.ld;
+  a.ostride = dw->rows * split.ld;
+  a.chunk = int32_t(split.chunk);
+  a.parts = int32_t(split.parts);
+  if ((rc = run_products(a, kExpertDw, x->dtype, MUON_F32, aligned, stream)) != MUON_OK) return rc;
+  return launch_experts_join(a, dw->ptr, dw->ld, dw->count > 1 ? dw->stride : 0, dw->dtype,
+                             static_cast<hipStream_t>(stream)) == hipSuccess ? MUON_OK : MUON_E_HIP;
 } catch (...) {   // an allocation of the host's failed
   return MUON_E_HIP;
 }

@@ -372,6 +372,51 @@ def test_accumulated_gradients(dtype, grad):
     assert torch.equal(plain, dw.to(grad))
 
 
+SPLIT = [(2100, 1, 2, 100, 60), (1600, 2, 2, 64, 64), (3001, 1, 1, 33, 77), (8000, 2, 4, 64, 136)]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tokens,k,experts,cols,outs", SPLIT)
+def test_split_contractions(tokens, k, experts, cols, outs, dtype, gather):
+    """Few tiles and many rows: parts of an expert's rows are summed apart, then in order."""
+    x, _, dy, plan, _, _, dw = check_layer(tokens, k, experts, cols, outs, dtype, gather, drop=0.1)
+    desc = mo.experts._stack(dw, dw.device)
+    assert mo._lib.load().muon_expert_linear_dw_workspace_bytes(tokens * k, desc) > 0
+    for _ in range(3):
+        assert torch.equal(mo.expert_linear_grad(dy, None, x, plan, gather=gather)[1], dw)
+
+
+@pytest.mark.parametrize("grad", [BF16, F32])
+@pytest.mark.parametrize("off,cols,outs", [(0, 64, 40), (3, 61, 40)])
+def test_split_contractions_accumulated(off, cols, outs, grad):
+    """Into strided matrices, with all rows at one expert, NaN behind the last and in a part of the memory used."""
+    g = torch.Generator().manual_seed(9)
+    choice = torch.full((4000, 1), 1, dtype=torch.int32)
+    choice[::7] = -1
+    choice[:5] = 2
+    plan = mo.expert_plan(choice.cuda(), 4)
+    x, dy = rand(g, 4000, cols), rand(g, 4000, outs)
+    n = int(plan.offsets[-1])
+    x[n:], dy[n:] = np.nan, np.nan
+    _, dw = mo.expert_linear_grad(dy, None, x, plan)
+    assert mo._lib.load().muon_expert_linear_dw_workspace_bytes(4000, mo.experts._stack(dw, dw.device)) > 0
+    assert (dw[[0, 3]] == 0).all() and torch.isfinite(dw).all() and (dw[1:3] != 0).any()
+    room = rand(g, 4, outs + 1, cols + off + 5, dtype=grad)
+    old = room.clone()
+    out = room[:, 1:, off:off + cols]
+    mo.expert_linear_grad(dy, None, x, plan, out=out, accumulate=True)
+    want = old.clone()
+    want[:, 1:, off:off + cols] = (old[:, 1:, off:off + cols].float() + dw).to(grad)
+    assert torch.equal(room, want)
+    mo.expert_linear_grad(dy, None, x, plan, out=out)
+    want[:, 1:, off:off + cols] = dw.to(grad)
+    assert torch.equal(room, want)
+    x[n - 1] = np.nan                                         # of expert 2
+    _, dw = mo.expert_linear_grad(dy, None, x, plan)
+    assert torch.isfinite(dw[[0, 1, 3]]).all() and torch.isnan(dw[2]).all()
+
+
 def test_gradients_against_differences():
     """d/dw and d/dx of sum(dy y) in fp32, whose error over a difference of 0.5 is that of the sums."""
     g = torch.Generator().manual_seed(10)

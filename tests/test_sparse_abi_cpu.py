@@ -252,6 +252,29 @@ def test_embedding_refusals(lib):
     assert back(d, i, ws=dw.ptr, size=need) == E["MUON_E_ALIAS"] and back(d, i, ws=BASE + 8, size=need) == E["MUON_E_ALIGN"]
 
 
+def test_memory_of_split_contractions(lib):
+    """Few tiles and many rows need memory, which is checked; the rest needs none."""
+    room = Room()
+
+    def need(slots, dw):
+        return lib.muon_expert_linear_dw_workspace_bytes(slots, ref(dw))
+    dw = room.stack(2, 100, 61, F32)
+    assert need(200, dw) == need(0, dw) == 0
+    n = need(8000, dw)
+    assert n > 0 and n % (100 * 64 * 4) == 0
+    assert need(8000, room.stack(64, 100, 61, F32)) == need(8000, room.stack(2, 2048, 2048, F32)) == 0
+    assert need(8000, room.stack(2, 0, 61, F32)) == need(-1, dw) == need(1 << 40, dw) == need(8000, None) == 0
+    assert 0 < need(_lib.MAX_SLOTS, room.stack(1, 64, 64, F32)) < 1 << 28
+    slots = room.slots(4000, 2, 2)
+    d, x = room.mat(8000, 100), room.mat(8000, 61)
+
+    def call(ws, size, o=dw):
+        return lib.muon_expert_linear_dw(ref(d), ref(x), ref(slots), 0, 0, ref(o), ws, size, None)
+    assert call(None, 0) == call(room.take(n), n - 1) == E["MUON_E_WORKSPACE"]
+    assert call(BASE + 8, n) == E["MUON_E_ALIGN"]
+    assert call(dw.ptr, n) == call(x.ptr, n) == E["MUON_E_ALIAS"]
+
+
 def test_package_exports():
     for n in ("route", "route_grad", "expert_plan", "expert_gather", "expert_linear", "expert_linear_grad", "expert_combine",
               "expert_combine_grad", "embedding", "embedding_grad", "ExpertPlan", "Routing"):
