@@ -53,7 +53,7 @@ constexpr int kBatch = 64;                // experts looked at at once
 // ---- the tile of a block
 struct Tile {
   int e;        // expert
-  int part;     // dw: where the results go: the expert, or the part of one
+  int part;     // part of a split contraction
   int lo, hi;   // its rows (of a part: the part's)
   int r0, c0;   // first row (fwd, dx: from lo; dw: of the matrix) and column
   bool any;
@@ -128,7 +128,7 @@ __device__ __forceinline__ Tile row_tile(const ExpertArgs& a, int lane) {
   return t;
 }
 
-// dw with split contractions: parts of a.chunk rows, all tiles of a part after each
+// Split contractions of dw: parts of a.chunk rows, all tiles of a part after each
 // other.
 template <int TM, int TN>
 __device__ __forceinline__ Tile part_tile(const ExpertArgs& a, int lane) {
@@ -154,7 +154,7 @@ __device__ __forceinline__ Tile matrix_tile(const ExpertArgs& a) {
   const int share = (tiles + 7) / 8;
   const int i = blockIdx.x >> 3, e = i / share;
   const int at = ((blockIdx.x + e) & 7) * share + i % share;
-  Tile t{e, e, 0, 0, at / across * TM, at % across * TN, e < a.experts && at < tiles};
+  Tile t{e, 0, 0, 0, at / across * TM, at % across * TN, e < a.experts && at < tiles};
   if (t.any) {
     rows_of(a, e, t.lo, t.hi);
     t.lo = __builtin_amdgcn_readfirstlane(t.lo);
@@ -540,7 +540,7 @@ __device__ __forceinline__ void interleave() {
 template <int OP, int DT, bool DMA, class T, int TM, int TN, int WM, int WN, int BK, int NST>
 __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
   constexpr int NW = WM * WN;
-  using Rows = Side<TM, NW, BK, OP == kExpertDw, false, DT, DMA>;
+  using Rows = Side<TM, NW, BK, OP >= kExpertDw, false, DT, DMA>;
   using Cols = Side<TN, NW, BK, OP != kExpertFwd, true, DT, DMA>;
   constexpr int kStage = Rows::kBytes + Cols::kBytes, PL = Rows::kPlanes;
   constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
@@ -551,16 +551,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
   const int wm = wave / WN, wn = wave % WN;
 
   Tile tile;
-  if constexpr (OP == kExpertDw) tile = a.chunk ? part_tile<TM, TN>(a, lane) : matrix_tile<TM, TN>(a);
+  if constexpr (OP == kExpertDw) tile = matrix_tile<TM, TN>(a);
+  else if constexpr (OP == kExpertPart) tile = part_tile<TM, TN>(a, lane);
   else tile = row_tile<TM, TN>(a, lane);
   if (!tile.any) return;
-  const int depth = OP == kExpertDw ? tile.hi - tile.lo : a.depth;
+  const int depth = OP >= kExpertDw ? tile.hi - tile.lo : a.depth;
   const int64_t es = DT == kBF16 ? 2 : 4;
   const uint8_t* rbase = static_cast<const uint8_t*>(a.r);
   const uint8_t* cbase = static_cast<const uint8_t*>(a.c);
   Rows rows;
   Cols cols;
-  if constexpr (OP == kExpertDw) {
+  if constexpr (OP >= kExpertDw) {
     rows.plan({rbase + tile.lo * a.ldr * es, a.ldr * es, nullptr, 0, depth, a.rows, tile.r0}, wave, lane);
     cols.plan({a.tokens ? cbase : cbase + tile.lo * a.ldc * es, a.ldc * es,
                a.tokens ? a.tokens + tile.lo : nullptr, a.src, depth, a.cols, tile.c0}, wave, lane);
@@ -677,9 +678,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
 #pragma unroll
       for (int j = 0; j < FM; ++j) acc[0][i][j] += acc[SETS - 1][i][j];
   }
-  const int most = OP == kExpertDw ? a.rows : tile.hi - tile.lo;
-  T* out = static_cast<T*>(a.out) + (OP == kExpertDw ? tile.part * a.ostride : tile.lo * a.ldo);
-  if (OP == kExpertDw && a.accumulate && !a.chunk) {
+  const int most = OP >= kExpertDw ? a.rows : tile.hi - tile.lo;
+  T* out = static_cast<T*>(a.out) + (OP == kExpertPart ? tile.part * a.ostride : OP == kExpertDw ? tile.e * a.ostride : tile.lo * a.ldo);
+  if (OP == kExpertDw && a.accumulate) {
     if (depth == 0) return;
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
@@ -738,7 +739,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
 template <int OP, int DT, bool DMA, class T, int TM, int TN, int WM, int WN, int BK, int NST>
 hipError_t launch_tiles(const ExpertArgs& a, hipStream_t s) {
   constexpr int NW = WM * WN;
-  using Rows = Side<TM, NW, BK, OP == kExpertDw, false, DT, DMA>;
+  using Rows = Side<TM, NW, BK, OP >= kExpertDw, false, DT, DMA>;
   using Cols = Side<TN, NW, BK, OP != kExpertFwd, true, DT, DMA>;
   constexpr int lds = NST * (Rows::kBytes + Cols::kBytes);
   static_assert(lds <= 160 * 1024, "LDS");
@@ -760,15 +761,18 @@ hipError_t launch_tiles(const ExpertArgs& a, hipStream_t s) {
 
 template <int OP, class T>
 hipError_t launch_op(const ExpertArgs& a, int dt, bool aligned, int tile, hipStream_t s) {
-  if (dt == kF32)
-    return tile == 64 ? launch_tiles<OP, kF32, false, T, 64, 64, 2, 2, 32, 2>(a, s)
-                      : launch_tiles<OP, kF32, false, T, 128, 128, 2, 4, 32, 2>(a, s);
-  if (!aligned)
-    return tile == 64 ? launch_tiles<OP, kBF16, false, T, 64, 64, 2, 2, 64, 2>(a, s)
-                      : launch_tiles<OP, kBF16, false, T, 128, 128, 2, 2, 64, 2>(a, s);
-  if (tile == 64) return launch_tiles<OP, kBF16, true, T, 64, 64, 2, 2, 64, 3>(a, s);
-  if (tile == 128) return launch_tiles<OP, kBF16, true, T, 128, 128, 2, 2, 64, 2>(a, s);
-  return launch_tiles<OP, kBF16, true, T, 256, 256, 2, 4, 64, 2>(a, s);
+  if (tile == 64) {
+    if (dt == kF32) return launch_tiles<OP, kF32, false, T, 64, 64, 2, 2, 32, 2>(a, s);
+    if (!aligned) return launch_tiles<OP, kBF16, false, T, 64, 64, 2, 2, 64, 2>(a, s);
+    return launch_tiles<OP, kBF16, true, T, 64, 64, 2, 2, 64, 3>(a, s);
+  }
+  if constexpr (OP != kExpertPart) {   // always 64
+    if (dt == kF32) return launch_tiles<OP, kF32, false, T, 128, 128, 2, 4, 32, 2>(a, s);
+    if (!aligned) return launch_tiles<OP, kBF16, false, T, 128, 128, 2, 2, 64, 2>(a, s);
+    if (tile == 128) return launch_tiles<OP, kBF16, true, T, 128, 128, 2, 2, 64, 2>(a, s);
+    return launch_tiles<OP, kBF16, true, T, 256, 256, 2, 4, 64, 2>(a, s);
+  }
+  return hipErrorInvalidValue;
 }
 
 // Sums the parts of the experts' split contractions in order: a block takes 2048
@@ -837,6 +841,7 @@ hipError_t launch_experts(const ExpertArgs& a, int op, int dt, int odt, bool ali
     if (op == kExpertDx) return launch_op<kExpertDx, T>(a, dt, aligned, tile, s);
     return launch_op<kExpertDw, T>(a, dt, aligned, tile, s);
   };
+  if (op == kExpertPart) return launch_op<kExpertPart, float>(a, dt, aligned, tile, s);
   return odt == kBF16 ? with(uint16_t{}) : with(float{});
 }
 

@@ -115,7 +115,8 @@ hipError_t launch_embedding_few(const EmbedGradArgs& a, const void* ids, int id_
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, int dt, int odt, hipStream_t s);
 
 // ---- experts' products (muon_experts.hip)
-enum ExpertOp : int32_t { kExpertFwd = 0, kExpertDx = 1, kExpertDw = 2 };
+// kExpertPart: dw with split contractions, which takes tiles of 64 alone.
+enum ExpertOp : int32_t { kExpertFwd = 0, kExpertDx = 1, kExpertDw = 2, kExpertPart = 3 };
 struct ExpertArgs {
   const void* r;            // operand of the output's rows: x, dy, dy
   const void* c;            // operand of the output's columns: w, w, x
@@ -130,16 +131,15 @@ struct ExpertArgs {
   int32_t src;              // rows of x when gathered
   int32_t accumulate;       // dw
   int32_t past;             // write past the caches
-  int32_t chunk, parts;     // dw: rows of a part of a split contraction (0: none are
-                            // split), parts that out has room for
+  int32_t chunk, parts;     // split dw: rows of a part, parts that out has room for
 };
 // Blocks of a launch with tm x tn tiles.  How the slots are split is known to the
 // device alone: a full tile for every tm slots and a part of one an expert at most.
 inline int64_t expert_blocks(const ExpertArgs& a, int op, int tm, int tn) {
   const int64_t across = (int64_t(a.cols) + tn - 1) / tn;
-  if (op == kExpertDw) {
+  if (op >= kExpertDw) {
     const int64_t tiles = (int64_t(a.rows) + tm - 1) / tm * across;
-    if (a.chunk) return 8 * ((tiles * a.parts + 7) / 8);
+    if (op == kExpertPart) return 8 * ((tiles * a.parts + 7) / 8);
     return 8 * a.experts * ((tiles + 7) / 8);
   }
   const int64_t tiles = a.slots / tm + (a.experts < a.slots ? a.experts : a.slots);
@@ -155,7 +155,8 @@ constexpr int64_t kExpertPitch = int64_t(1) << 22;
 // tile: 64, 128 or, aligned, 256
 hipError_t launch_experts(const ExpertArgs& a, int op, int dt, int odt, bool aligned, int tile, hipStream_t s);
 
-// Sums a.parts parts that a launch with a.chunk wrote to a.out into the experts' matrices.
+// Sums the parts that a launch of kExpertPart wrote to a.out (fp32) into the experts'
+// matrices.
 hipError_t launch_experts_join(const ExpertArgs& a, void* out, int64_t ldo, int64_t ostride, int odt, hipStream_t s);
 
 }  // namespace muon

@@ -154,7 +154,7 @@ bool spans(const muon_mat& x) {
 // | 52 | 61; 48 slots, 64 experts, 2048 -> 1408: 37 | 32 | 49, 12000: 170 | 128 | 131; fp32
 // 8192 slots, 32 experts, 1024 -> 1024: 150 | 142; 32768, 8, 2048 -> 1024: 1079 | 804.
 int tile_of(const ExpertArgs& a, int op, int dt, bool aligned) {
-  if (a.chunk) return 64;
+  if (op == kExpertPart) return 64;
   if (const char* e = std::getenv("MUON_EXPERT_TILE")) {
     const int t = std::atoi(e);
     if (t == 64 || t == 128 || (t == 256 && aligned)) return t;
@@ -187,7 +187,7 @@ bool past_caches(const ExpertArgs& a, int op, int odt) {
 
 int run_products(ExpertArgs a, int op, int dt, int odt, bool aligned, void* stream) {
   if (std::max(a.ldr, a.ldc) > kExpertPitch) return MUON_E_SHAPE;
-  a.past = past_caches(a, op, odt);
+  a.past = op != kExpertPart && past_caches(a, op, odt);   // parts are read again
   const int tile = tile_of(a, op, dt, aligned);
   if (expert_blocks(a, op, tile, tile) > kMaxBlocks) return MUON_E_SHAPE;
   return launch_experts(a, op, dt, odt, aligned, tile, static_cast<hipStream_t>(stream)) == hipSuccess ? MUON_OK : MUON_E_HIP;
@@ -445,7 +445,7 @@ int muon_expert_linear_dw(const muon_mat* dy, const muon_mat* x, const muon_slot
   a.ostride = dw->rows * split.ld;
   a.chunk = int32_t(split.chunk);
   a.parts = int32_t(split.parts);
-  if ((rc = run_products(a, kExpertDw, x->dtype, MUON_F32, aligned, stream)) != MUON_OK) return rc;
+  if ((rc = run_products(a, kExpertPart, x->dtype, MUON_F32, aligned, stream)) != MUON_OK) return rc;
   return launch_experts_join(a, dw->ptr, dw->ld, dw->count > 1 ? dw->stride : 0, dw->dtype,
                              static_cast<hipStream_t>(stream)) == hipSuccess ? MUON_OK : MUON_E_HIP;
 } catch (...) {   // an allocation of the host's failed
