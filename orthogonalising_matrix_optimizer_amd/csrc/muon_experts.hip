@@ -31,6 +31,11 @@
 // are rows of its first operand, which is that of the output's columns.  Its 32
 // rows are taken in an order that leaves a lane 16 consecutive columns of
 // one output row.
+//
+// Measured, 64 experts in bf16: 16384 x 6 slots, 2048 -> 1408 gathered 595 us (0.94 PF;
+// 495 on zeros, whose lower power leaves the clock at 2.35 GHz instead of 1.92; the matrix
+// instructions alone 407, the loads alone 390); 49146 slots, 1408 -> 2048: fwd 365, dx 355, dw
+// into fp32 485 (738 MB of stores).  48 slots: 29, the used matrices once.
 #include <atomic>
 #include <type_traits>
 
@@ -776,7 +781,8 @@ hipError_t launch_op(const ExpertArgs& a, int dt, bool aligned, int tile, hipStr
 }
 
 // Sums the parts of the experts' split contractions in order: a block takes 2048
-// elements of expert blockIdx.y's matrix, a thread eight of a row.
+// elements of expert blockIdx.y's matrix, a thread eight of a row.  An expert's first part
+// is found as the tiles find theirs.
 template <class T>
 __global__ __launch_bounds__(256) void k_experts_join(ExpertArgs a, const float* in, T* out, int64_t ldo, int64_t ostride,
                                                      bool whole) {

@@ -43,7 +43,8 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int bytes, int i) {
                     : static_cast<int64_t>(glb(static_cast<const int32_t*>(ids))[i]);
 }
 
-// ---- embedding: a thread takes eight columns of kEmbedEach tokens
+// ---- embedding: a thread takes eight columns of kEmbedEach tokens, so that as many
+// rows are on their way.  Bound by memory: 65537 tokens x 2560 in bf16, 672 MB, 124 us.
 constexpr int kEmbedEach = 4;
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void k_embedding(EmbedArgs a) {
@@ -79,7 +80,10 @@ __global__ __launch_bounds__(kRowThreads) void k_embedding(EmbedArgs a) {
 // run inside the chunk is written at once.  One that came in from the chunk
 // before goes to the chunk's first partial row, one that only leaves it to its
 // second; k_embedding_join adds a run's partial rows.  Waves behind those look
-// over 64 rows of the table each and zero the ones without tokens.
+// over 64 rows of the table each and zero the ones without tokens.  Fixed chunks,
+// not a wave for each row of the table: half of a text's tokens may share a few ids
+// (65536 of them: 43 us, 120 by owners).  65537 x 2560 bf16 into 50257 fp32 rows, 851 MB:
+// 245 us and 15 for the join, mostly stores; 16384 x 768 into 50257: 37 and 5.
 constexpr int kGradBatch = 8;   // rows in flight
 
 template <class T, class D>
@@ -230,7 +234,7 @@ __global__ __launch_bounds__(kRowThreads) void k_embedding_join(EmbedGradArgs a)
 
 // Up to kFewTokens tokens, in one launch and without a sort: a wave takes a row of
 // the table, finds the tokens that have it by ballots over all ids and adds their
-// rows in order.  (37 tokens, 333 rows of 77: 5 us where sort, sums and join take 15.)
+// rows in order.  (37 tokens, 333 rows of 77: 3.2 us where sort, sums and join take 15.)
 template <class T, class D>
 __global__ __launch_bounds__(kRowThreads) void k_embedding_few(EmbedGradArgs a, const void* ids, int id_bytes) {
   constexpr int MASKS = kFewTokens / 64;
@@ -284,7 +288,8 @@ __global__ __launch_bounds__(kRowThreads) void k_embedding_few(EmbedGradArgs a, 
 }
 
 // ---- combine: a thread takes eight columns of a token, the rows of up to
-// kSlotBatch slots in flight
+// kSlotBatch slots in flight.  Bound by the rows of y, read once here and there: 16384
+// tokens x 6 x 2048 in bf16, 470 MB, 112 us.
 constexpr int kSlotBatch = 8;
 template <class T, class D>
 __global__ __launch_bounds__(kRowThreads) void k_combine(CombineArgs a) {

@@ -417,6 +417,32 @@ def test_split_contractions_accumulated(off, cols, outs, grad):
     assert torch.isfinite(dw[[0, 1, 3]]).all() and torch.isnan(dw[2]).all()
 
 
+def test_split_contractions_in_a_graph():
+    """Captured, replayed with other rows and another choice, beside eager calls on another stream."""
+    g = torch.Generator().manual_seed(10)
+    choice = pick(g, 4000, 1, 3, drop=0.1).cuda()
+    x, dy = rand(g, 4000, 72), rand(g, 4000, 56)
+
+    def grads():
+        plan = mo.expert_plan(choice, 3)
+        return mo.expert_linear_grad(dy, None, x, plan, gather=True)[1]
+    assert mo._lib.load().muon_expert_linear_dw_workspace_bytes(4000, mo.experts._stack(grads(), x.device)) > 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dw = grads()
+    for i in range(4):
+        choice.copy_(pick(g, 4000, 1, 3, drop=0.2 * i))
+        x.copy_(rand(g, 4000, 72))
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):
+            want = grads()
+        torch.cuda.synchronize()
+        assert torch.equal(dw, want) and (dw != 0).any(), i
+
+
 def test_gradients_against_differences():
     """d/dw and d/dx of sum(dy y) in fp32, whose error over a difference of 0.5 is that of the sums."""
     g = torch.Generator().manual_seed(10)
