@@ -100,10 +100,11 @@ def _ids(t: torch.Tensor, dev: Optional[torch.device] = None) -> bytes:
     return _IDS.pack(t.data_ptr(), t.numel(), t.element_size(), 0)
 
 
-def _f32(t: torch.Tensor, plan_shape: Tuple[int, int], dev: torch.device, what: str) -> int:
-    """The address of a dense fp32 tensor with one number a slot."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != dev:
-        raise ValueError(f"{what} must be an fp32 tensor on the operands' device")
+def _per_slot(t: torch.Tensor, plan_shape: Tuple[int, int], dev: torch.device, what: str,
+         dtype: torch.dtype = torch.float32) -> int:
+    """The address of a dense tensor (fp32 or of `dtype`) with one number a slot."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{what} must be a tensor of {dtype} on the operands' device")
     if tuple(t.shape) != plan_shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous and {plan_shape[0]} x {plan_shape[1]}, not {tuple(t.shape)}")
     return t.data_ptr()
@@ -199,19 +200,25 @@ def route(logits: torch.Tensor, k: int, normalize: bool = False) -> Routing:
 
 
 def route_grad(dgates: torch.Tensor, logits: torch.Tensor, routing: Routing) -> torch.Tensor:
-    """Gradient of routing.gates with respect to the logits, in their type."""
+    """Gradient of routing.gates with respect to the logits, in their type.  A
+    Routing of a router of one's own has fp32 gates and int32 experts [tokens, k],
+    both contiguous, and expert_plan's plan of them."""
     _not_recorded(dgates)
+    if not isinstance(routing, Routing) or type(routing.plan) is not ExpertPlan:
+        raise ValueError("routing is a Routing with an ExpertPlan")
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits are a 2-D tensor [tokens, experts]")
     dev = _gpu(logits.device)
     n, e = logits.shape
-    shape = tuple(routing.gates.shape)
-    if shape[0] != n or routing.plan.experts != e:
-        raise ValueError(f"logits are {n} x {e}, the routing of {shape[0]} tokens and {routing.plan.experts} experts")
-    dg, g = _f32(dgates, shape, dev, "dgates"), _f32(routing.gates, shape, dev, "gates")
+    plan = routing.plan
+    shape = (plan.n_tokens, plan.k)
+    if shape[0] != n or plan.experts != e:
+        raise ValueError(f"logits are {n} x {e}, the routing of {shape[0]} tokens and {plan.experts} experts")
+    dg, g = _per_slot(dgates, shape, dev, "dgates"), _per_slot(routing.gates, shape, dev, "routing.gates")
+    chosen = _per_slot(routing.experts, shape, dev, "routing.experts", _I32)
     out, om = _new_one(n, e, logits.dtype, dev)
-    _call("muon_route_grad", dev, dg, _MAT1.pack(*_mat(logits, dev)), g, routing.experts.data_ptr(), shape[1],
-          int(routing.normalize), om)
+    _call("muon_route_grad", dev, dg, _MAT1.pack(*_mat(logits, dev)), g, chosen, plan.k, int(bool(routing.normalize)),
+          om)
     return out
 
 
@@ -315,7 +322,7 @@ def expert_combine(y: torch.Tensor, plan: ExpertPlan, gates: Optional[torch.Tens
     _not_recorded(y)
     dev = _plan_of(plan)
     ym = _rows_mat(y, plan.slots, dev, "y")
-    g = None if gates is None else _f32(gates, (plan.n_tokens, plan.k), dev, "gates")
+    g = None if gates is None else _per_slot(gates, (plan.n_tokens, plan.k), dev, "gates")
     _not_recorded(gates)
     res, om = _result(out, plan.n_tokens, y.shape[1], dtype or y.dtype, dev)
     _call("muon_expert_combine", dev, ym, g, plan.desc, om)
@@ -335,7 +342,7 @@ def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan,
     ym = _rows_mat(y, plan.slots, dev, "y")
     if y.shape[1] != dout.shape[1]:
         raise ValueError(f"dout has {dout.shape[1]} features, y {y.shape[1]}")
-    g = _f32(gates, (plan.n_tokens, plan.k), dev, "gates")
+    g = _per_slot(gates, (plan.n_tokens, plan.k), dev, "gates")
     dy, dym = _new_one(plan.slots, dout.shape[1], dout.dtype, dev)
     dgates = _empty((plan.n_tokens, plan.k), (plan.k, 1), dtype=torch.float32, device=dev)
     _call("muon_expert_combine_grad", dev, dm, ym, g, plan.desc, dym, dgates.data_ptr())
