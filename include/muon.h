@@ -613,7 +613,9 @@ int muon_expert_gather(const muon_mat* x, const muon_slots* slots, const muon_ma
 /* out[t] = sum_j gates[t,j] y[row of slot (t,j)] in fp32, in the order of j, and
  * its gradients: dy[row of (t,j)] = gates[t,j] dout[t], dgates[t,j] = the
  * product of dout[t] and that row of y (0 where dropped).  gates may be NULL
- * for ones (the gradient of a gathered x); dy or dgates may be NULL. */
+ * for ones (the gradient of a gathered x); dy or dgates may be NULL.  place and
+ * tokens go together: to the gradient a slot is also dropped where its place is
+ * no row, or a row of another token. */
 int muon_expert_combine(const muon_mat* y, const float* gates, const muon_slots* slots,
                         const muon_mat* out, void* stream);
 int muon_expert_combine_grad(const muon_mat* dout, const muon_mat* y, const float* gates,

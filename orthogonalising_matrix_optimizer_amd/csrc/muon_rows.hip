@@ -334,21 +334,32 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // tokens' rows of dout, read once for each slot, come from the caches.  (A wave for
 // each token, which reads dout once and k rows of y here and there: 16384 tokens x 6
 // x 2048 in bf16 309 us, 203 in this order.)  The row's slot is that of its
-// token's which lies there.
+// token's which lies there; rows that are only gathered need none.
 constexpr int kChunkBatch = 4;   // pieces of 512 columns in flight
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void k_combine_grad(CombineArgs a) {
   const int r = blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (r >= a.slots) return;
-  if (a.dgates && lane == 0 && a.place[r] < 0) a.dgates[r] = 0.f;   // slot r, dropped
   const int t = a.rows[r];
+  if (a.dgates) {
+    // slot r gets its number from the wave of its row, if that is one of its token's, else 0
+    const int at = a.place[r], of = at >= 0 && at < a.slots ? a.rows[at] : -1;
+    const int64_t own = static_cast<int64_t>(of) * a.k;
+    if (lane == 0 && !(of >= 0 && of < a.tokens && r >= own && r < own + a.k)) a.dgates[r] = 0.f;
+  }
   if (t < 0 || t >= a.tokens) return;
   const int64_t first = static_cast<int64_t>(t) * a.k;
-  const uint64_t here = __ballot(lane < a.k && a.place[first + (lane < a.k ? lane : 0)] == r);
-  if (!here) return;
-  const int64_t slot = first + __builtin_ctzll(here);
-  const float g = a.gates ? a.gates[slot] : 1.f;
+  uint64_t here = 0;   // the token's slots that lie here: one, in a plan of expert_plan's
+  float g = 1.f;
+  if (a.gates || a.dgates) {
+    here = __ballot(lane < a.k && a.place[first + (lane < a.k ? lane : 0)] == r);
+    if (!here) return;
+    if (a.gates) {
+      g = a.gates[first + __builtin_ctzll(here)];
+      for (uint64_t more = here & (here - 1); more; more &= more - 1) g += a.gates[first + __builtin_ctzll(more)];
+    }
+  }
   const T* d = static_cast<const T*>(a.dout) + t * a.ldd;
   const T* y = static_cast<const T*>(a.y) + r * a.ldy;
   T* out = static_cast<T*>(a.out) + r * a.ldo;
@@ -379,7 +390,7 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_grad(CombineArgs a) {
   }
   if (a.dgates) {
     dot = lanes_sum(dot);
-    if (lane == 0) a.dgates[slot] = dot;
+    if (here >> lane & 1) a.dgates[first + lane] = dot;
   }
 }
 
