@@ -35,8 +35,9 @@ int check_stack(const muon_stack& w) {
   if (w.count < 1 || w.count > MUON_MAX_EXPERTS || w.rows < 0 || w.cols < 0 || w.rows > kMaxCols || w.cols > kMaxCols)
     return MUON_E_SHAPE;
   if (w.rows == 0 || w.cols == 0) return MUON_OK;
-  if (w.ld < w.cols || w.ld > (int64_t(1) << 40)) return MUON_E_SHAPE;
-  if (w.count > 1 && (w.stride < (w.rows - 1) * w.ld + w.cols || w.stride > (int64_t(1) << 50))) return MUON_E_SHAPE;
+  if (w.ld < w.cols || w.ld > (int64_t(1) << 40) || !fits(w.rows, w.ld, w.cols)) return MUON_E_SHAPE;
+  const int64_t one = (w.rows - 1) * w.ld + w.cols;
+  if (w.count > 1 && (w.stride < one || !fits(w.count, w.stride, one))) return MUON_E_SHAPE;
   if (!w.ptr) return MUON_E_NULL;
   if (misaligned(w.ptr, esize(w.dtype))) return MUON_E_ALIGN;
   return MUON_OK;
@@ -59,7 +60,7 @@ void add_span(std::vector<Span>& v, const muon_stack& w, bool write) {
 
 int check_counts(int64_t n_tokens, int64_t k, int64_t experts) {
   if (n_tokens < 0 || k < 1 || k > MUON_MAX_K || experts < 1 || experts > MUON_MAX_EXPERTS) return MUON_E_SHAPE;
-  return n_tokens * k > MUON_MAX_SLOTS || n_tokens > MUON_MAX_SLOTS ? MUON_E_SHAPE : MUON_OK;
+  return n_tokens > MUON_MAX_SLOTS / k ? MUON_E_SHAPE : MUON_OK;
 }
 
 int64_t slots_of(const muon_slots& s) { return s.n_tokens * s.k; }
