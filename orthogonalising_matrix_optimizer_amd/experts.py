@@ -9,8 +9,8 @@ device: no call waits for the GPU, and all may be captured into a graph.
 
 Nothing here is recorded by autograd.  As for the 4-bit layers the gradients are
 calls of their own, made by hand or by the two halves of a
-torch.autograd.Function, and a tensor that requires a gradient is refused where
-autograd records.
+torch.autograd.Function, and a tensor (an output's too) that requires a gradient
+is refused where autograd records, one with a tangent of forward mode always.
 """
 from __future__ import annotations
 
@@ -145,6 +145,7 @@ def _result(out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtyp
     """`out` or a new tensor, and its packed muon_mat."""
     if out is None:
         return _new_one(rows, cols, dtype, dev)
+    _not_recorded(out)
     if tuple(out.shape) != (rows, cols):
         raise ValueError(f"out is {tuple(out.shape)}, not {(rows, cols)}")
     return out, _MAT1.pack(*_mat(out, dev))
@@ -203,9 +204,11 @@ def route_grad(dgates: torch.Tensor, logits: torch.Tensor, routing: Routing) -> 
     """Gradient of routing.gates with respect to the logits, in their type.  A
     Routing of a router of one's own has fp32 gates and int32 experts [tokens, k],
     both contiguous, and expert_plan's plan of them."""
-    _not_recorded(dgates)
     if not isinstance(routing, Routing) or type(routing.plan) is not ExpertPlan:
         raise ValueError("routing is a Routing with an ExpertPlan")
+    _not_recorded(dgates)
+    _not_recorded(logits)
+    _not_recorded(routing.gates)
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits are a 2-D tensor [tokens, experts]")
     dev = _gpu(logits.device)
@@ -275,7 +278,9 @@ def expert_linear_grad(dy: torch.Tensor, w: Optional[torch.Tensor], x: Optional[
     `accumulate`); list(dw) are gradients for Muon.step.  Without w there is no
     dx, without x no dw."""
     _not_recorded(dy)
+    _not_recorded(w)
     _not_recorded(x)
+    _not_recorded(out)
     dev = _plan_of(plan)
     dm = _rows_mat(dy, plan.slots, dev, "dy")
     dx = dw = None
@@ -320,10 +325,10 @@ def expert_combine(y: torch.Tensor, plan: ExpertPlan, gates: Optional[torch.Tens
     [tokens, k] (fp32; None: ones, the gradient of gathered rows): [tokens,
     cols] in y's type or `dtype`, zeros for a token without slots."""
     _not_recorded(y)
+    _not_recorded(gates)
     dev = _plan_of(plan)
     ym = _rows_mat(y, plan.slots, dev, "y")
     g = None if gates is None else _per_slot(gates, (plan.n_tokens, plan.k), dev, "gates")
-    _not_recorded(gates)
     res, om = _result(out, plan.n_tokens, y.shape[1], dtype or y.dtype, dev)
     _call("muon_expert_combine", dev, ym, g, plan.desc, om)
     if out is not None:
@@ -337,6 +342,8 @@ def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan,
     [tokens, k] in fp32, 0 for dropped slots).  Rows of dy that belong to no
     slot are uninitialised."""
     _not_recorded(dout)
+    _not_recorded(y)
+    _not_recorded(gates)
     dev = _plan_of(plan)
     dm = _rows_mat(dout, plan.n_tokens, dev, "dout")
     ym = _rows_mat(y, plan.slots, dev, "y")
@@ -365,6 +372,7 @@ def embedding(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0,
         if len(shape) != 2:
             res = res.view(shape)
     else:
+        _not_recorded(out)
         if tuple(out.shape) != shape:
             raise ValueError(f"out is {tuple(out.shape)}, not {shape}")
         res, om = out, _MAT1.pack(*_mat(_rows_of(out), dev))

@@ -27,6 +27,7 @@ from struct import Struct
 from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import _lib
 
@@ -171,10 +172,14 @@ def _rows_of(t: torch.Tensor) -> torch.Tensor:
 
 
 def _not_recorded(t: torch.Tensor) -> None:
-    """Refuses a tensor whose gradient autograd would look for in the result."""
-    if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
-        raise ValueError("the 4-bit operators and dropout record nothing for autograd: call them under "
-                         "torch.no_grad() or in an autograd.Function, or give t.detach()")
+    """Refuses a tensor whose gradient or tangent autograd would look for in the result."""
+    if isinstance(t, torch.Tensor):
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("this operator records nothing for autograd: call it under torch.no_grad() or in an "
+                             "autograd.Function, or give t.detach()")
+        if _forward_ad._current_level >= 0 and _forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("this operator records nothing for autograd's forward mode: call it in an "
+                             "autograd.Function with a jvp, or give unpack_dual(t).primal")
 
 
 def _written(ts) -> None:

@@ -56,3 +56,67 @@ def test_route_grad_checks_a_routings_gates_and_sizes(calls):
     with pytest.raises(ValueError):
         mo.route_grad(torch.zeros(5, 2), torch.zeros(5, 3), None)
     assert not calls
+
+
+def _gradient_calls(mark):
+    """Every tensor whose derivative a call would lose, marked by `mark`, one at a time."""
+    p, x, w, dy = _plan(), torch.zeros(10, 4), torch.zeros(3, 6, 4), torch.zeros(10, 6)
+    t, gates, ids = torch.zeros(5, 4), torch.zeros(5, 2), torch.zeros(3, dtype=torch.int64)
+    logits, rows = torch.zeros(5, 3), torch.zeros(3, 5)
+    r = mo.Routing(gates, torch.zeros(5, 2, dtype=torch.int32), p, False)
+    return [
+        lambda: mo.route(mark(logits), 1), lambda: mo.route_grad(mark(gates), logits, r),
+        lambda: mo.route_grad(gates, mark(logits), r), lambda: mo.route_grad(gates, logits, r._replace(gates=mark(gates))),
+        lambda: mo.expert_gather(mark(t), p), lambda: mo.expert_gather(t, p, out=mark(x)),
+        lambda: mo.expert_linear(mark(x), w, p), lambda: mo.expert_linear(x, mark(w), p),
+        lambda: mo.expert_linear(x, w, p, out=mark(dy)),
+        lambda: mo.expert_linear_grad(mark(dy), w, x, p), lambda: mo.expert_linear_grad(dy, mark(w), x, p),
+        lambda: mo.expert_linear_grad(dy, mark(w), None, p), lambda: mo.expert_linear_grad(dy, w, mark(x), p),
+        lambda: mo.expert_linear_grad(dy, w, x, p, out=mark(w)),
+        lambda: mo.expert_combine(mark(x), p), lambda: mo.expert_combine(x, p, mark(gates)),
+        lambda: mo.expert_combine(x, p, out=mark(t)),
+        lambda: mo.expert_combine_grad(mark(t), x, p, gates), lambda: mo.expert_combine_grad(t, mark(x), p, gates),
+        lambda: mo.expert_combine_grad(t, x, p, mark(gates)),
+        lambda: mo.embedding(ids, mark(t)), lambda: mo.embedding(ids, t, out=mark(torch.zeros(3, 4))),
+        lambda: mo.embedding_grad(mark(rows), ids, 4), lambda: mo.embedding_grad(rows, ids, 5, out=mark(torch.zeros(5, 5))),
+    ]
+
+
+def test_every_tensor_that_requires_a_gradient_is_refused(calls):
+    """Where autograd records; elsewhere each is taken."""
+    lost = _gradient_calls(lambda t: t.clone().requires_grad_(True))
+    for i, f in enumerate(lost):
+        with pytest.raises(ValueError, match="autograd") as e:
+            f()
+            pytest.fail(f"call {i} was taken")
+        assert "4-bit" not in str(e.value)
+    assert not calls
+    with torch.no_grad():
+        for f in lost:
+            f()
+    assert len(calls) >= len(lost)
+
+
+def test_every_tensor_with_a_tangent_is_refused(calls):
+    """Forward-mode derivatives would be lost too, also under no_grad; not within a Function's forward."""
+    with torch.autograd.forward_ad.dual_level():
+        lost = _gradient_calls(lambda t: torch.autograd.forward_ad.make_dual(t.clone(), torch.ones_like(t)))
+        for i, f in enumerate(lost):
+            for recorded in (True, False):
+                with torch.set_grad_enabled(recorded), pytest.raises(ValueError, match="autograd"):
+                    f()
+                    pytest.fail(f"call {i} was taken")
+        assert not calls
+        for f in _gradient_calls(lambda t: t):
+            f()
+
+        class Combine(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, y):
+                return mo.expert_combine(y, _plan())
+
+            @staticmethod
+            def jvp(ctx, dy):
+                return mo.expert_combine(dy, _plan())
+        y = torch.autograd.forward_ad.make_dual(torch.zeros(10, 4), torch.ones(10, 4))
+        assert torch.autograd.forward_ad.unpack_dual(Combine.apply(y)).tangent.shape == (5, 4)
