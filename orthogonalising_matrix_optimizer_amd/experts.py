@@ -88,7 +88,8 @@ def _check_counts(n_tokens: int, k: int, experts: int) -> None:
         raise ValueError(f"{n_tokens} tokens x {k} are more than {_lib.MAX_SLOTS} slots")
 
 
-def _ids(t: torch.Tensor, dev: Optional[torch.device] = None) -> bytes:
+def _ids(t: torch.Tensor, dev: Optional[torch.device] = None) -> Tuple[torch.Tensor, bytes]:
+    """Integers in one run (t, or a copy of rows that are apart) and their muon_ids."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"expected a tensor, got {type(t).__name__}")
     if t.dtype not in (torch.int32, torch.int64):
@@ -96,8 +97,10 @@ def _ids(t: torch.Tensor, dev: Optional[torch.device] = None) -> bytes:
     if dev is not None and t.device != dev:
         raise ValueError("operands must be on one device")
     if not t.is_contiguous():
-        raise ValueError("indexes must be contiguous")
-    return _IDS.pack(t.data_ptr(), t.numel(), t.element_size(), 0)
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError("rows of indexes must be contiguous (stride(-1) == 1)")
+        t = t.contiguous()
+    return t, _IDS.pack(t.data_ptr(), t.numel(), t.element_size(), 0)
 
 
 def _per_slot(t: torch.Tensor, plan_shape: Tuple[int, int], dev: torch.device, what: str,
@@ -158,15 +161,15 @@ def _plan_of(plan: ExpertPlan) -> torch.device:
 
 
 def expert_plan(experts: torch.Tensor, n_experts: int) -> ExpertPlan:
-    """Sorts the slots of a choice of experts [tokens, k] (int32 or int64;
-    a number outside 0 .. n_experts - 1 drops its slot), for routers other
+    """Sorts the slots of a choice of experts [tokens, k] (int32 or int64, rows
+    contiguous; a number outside 0 .. n_experts - 1 drops its slot), for routers other
     than route()."""
     if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
         raise ValueError("the choice of experts is a 2-D tensor [tokens, k]")
     dev = _gpu(experts.device)
     n, k = experts.shape
     _check_counts(n, k, n_experts)
-    ids = _ids(experts)
+    held, ids = _ids(experts)
     plan = ExpertPlan(_empty((2 * n * k + n_experts + 1,), (1,), dtype=_I32, device=dev), n, k, n_experts, dev)
     keep, ws, size = _workspace(int(_lib.load().muon_expert_plan_workspace_bytes(n, k, n_experts)), dev)
     _lib.check(_call("muon_expert_plan", dev, ids, plan.desc, ws, size), "muon_expert_plan")
@@ -359,13 +362,13 @@ def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan,
 def embedding(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0,
               out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """scale times the rows of the table w [rows, cols] that ids (int32 or int64,
-    any shape) name: [*ids.shape, cols] in w's type.  An id that is none of w's
+    any shape, rows contiguous: tokens[:, :-1], say) name: [*ids.shape, cols] in w's type.  An id that is none of w's
     rows (-1, say: padding) gives zeros."""
     _not_recorded(w)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("the table is a 2-D tensor [rows, cols]")
     dev = _gpu(w.device)
-    im, wm = _ids(ids, dev), _MAT1.pack(*_mat(w, dev))
+    (held, im), wm = _ids(ids, dev), _MAT1.pack(*_mat(w, dev))
     shape = (*ids.shape, w.shape[1])
     if out is None:
         res, om = _new_one(ids.numel(), w.shape[1], w.dtype, dev)
@@ -395,7 +398,7 @@ def embedding_grad(dy: torch.Tensor, ids: torch.Tensor, rows: int, scale: float 
         raise ValueError("accumulate needs out")
     d2 = _rows_of(dy)
     dev = _gpu(dy.device)
-    dm, im = _MAT1.pack(*_mat(d2, dev)), _ids(ids, dev)
+    dm, (held, im) = _MAT1.pack(*_mat(d2, dev)), _ids(ids, dev)
     rows, cols = int(rows), d2.shape[1]
     res, om = _result(out, rows, cols, grad_dtype, dev)
     keep, ws, size = _workspace(int(_lib.load().muon_embedding_grad_workspace_bytes(ids.numel(), rows, cols)), dev)

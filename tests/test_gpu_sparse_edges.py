@@ -92,3 +92,26 @@ def test_rows_gathered_by_a_plan_that_was_written_over(dtype, cols):
     want = torch.full((102, cols), 7.0, dtype=dtype, device="cuda")
     want[1:101][torch.from_numpy(ok).cuda()] = x[torch.from_numpy(tokens[ok]).long().cuda()]
     assert torch.equal(room, want)
+
+
+def test_ids_and_choices_of_any_row_pitch():
+    """A language model's inputs and targets, as slices of one batch; also captured."""
+    g = torch.Generator().manual_seed(7)
+    batch, w = torch.randint(0, 60, (9, 65), generator=g).cuda(), torch.randn(60, 40, generator=g).cuda()
+    for ids in (batch[:, :-1], batch[:, 1:], batch.int()[:, 3:], batch[::2], batch[0].expand(3, 65)):
+        dense = ids.contiguous()
+        dy = torch.randn(*ids.shape, 40, generator=g).cuda()
+        assert torch.equal(mo.embedding(ids, w), w[dense])
+        assert torch.equal(mo.embedding_grad(dy, ids, 60), mo.embedding_grad(dy, dense, 60))
+    choice = torch.randint(-1, 5, (700, 6), generator=g).cuda()
+    a, b = mo.expert_plan(choice[:, 1:4], 5), mo.expert_plan(choice[:, 1:4].contiguous(), 5)
+    assert torch.equal(a.buffer, b.buffer)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        y = mo.embedding(batch[:, :-1], w)
+    for _ in range(3):
+        batch.copy_(torch.randint(0, 60, (9, 65), generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, mo.embedding(batch[:, :-1].contiguous(), w))

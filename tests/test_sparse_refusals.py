@@ -120,3 +120,31 @@ def test_every_tensor_with_a_tangent_is_refused(calls):
                 return mo.expert_combine(dy, _plan())
         y = torch.autograd.forward_ad.make_dual(torch.zeros(10, 4), torch.ones(10, 4))
         assert torch.autograd.forward_ad.unpack_dual(Combine.apply(y)).tangent.shape == (5, 4)
+
+
+def test_ids_and_choices_of_any_row_pitch(calls):
+    """A column slice of a batch of tokens, as a language model's inputs are: dense copies of its rows are read."""
+    batch = torch.arange(12).reshape(3, 4)
+    read = []
+
+    def ids_of(packed):
+        p, n, size, _ = experts._IDS.unpack(packed)
+        import ctypes
+        kind = ctypes.c_int64 if size == 8 else ctypes.c_int32
+        read.append(list((kind * n).from_address(p)))
+    experts_call = experts._call
+    experts._call = lambda name, dev, *a: ids_of(a[1 if name == "muon_embedding_grad" else 0]) or 0
+    try:
+        for ids in (batch[:, :-1], batch[:, 1:], batch.int()[:, 1:3], batch[::2], batch.expand(2, 3, 4), batch[:, :1],
+                    batch[0].expand(5, 4)):
+            y = mo.embedding(ids, torch.zeros(20, 5))
+            assert y.shape == (*ids.shape, 5) and read.pop() == ids.reshape(-1).tolist()
+            mo.embedding_grad(torch.zeros(*ids.shape, 5), ids, 20)
+            assert read.pop() == ids.reshape(-1).tolist()
+        mo.expert_plan(batch[:, 1:3], 12)
+        assert read.pop() == batch[:, 1:3].reshape(-1).tolist()
+    finally:
+        experts._call = experts_call
+    for bad in (batch.t(), batch[:, ::2], batch[:, 1]):       # numbers that are apart, as in a matrix's rows
+        with pytest.raises(ValueError, match="contiguous"):
+            mo.embedding(bad, torch.zeros(20, 5))
