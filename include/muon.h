@@ -582,9 +582,11 @@ int muon_route_grad(const float* dgates, const muon_mat* logits, const float* ga
  * of what is written.  x has a row for each slot in the sorted order, or with
  * `gather` one for each token (of less than 0xf0000000 bytes in all: MUON_E_SHAPE, and
  * muon_expert_gather makes sorted rows).  fp32 operands are multiplied as sums of
- * three bf16 terms each (all of their 24 bits; products of terms that are at most
- * 2^-24 of the whole are left out); one that is not finite, or rounds to an
- * infinity in bf16, makes the sums it enters NaN.
+ * three bf16 terms each, which hold all of their 24 bits, subnormal ones' too; products
+ * of terms that are at most 2^-24 of the whole are left out.  An operand of 2^128 - 2^119
+ * (3.3895e38) or more counts as an infinity; infinities and NaN enter sums as in any fp32
+ * product.  Where the magnitudes of a sum's terms add up to 2^127 or more it may be an
+ * infinity or NaN though the sum itself is smaller.
  * Row pitches of operands are at most 2^22 elements (MUON_E_SHAPE).
  *   linear:    out[r] = x[r] w[e(r)]^T                 (slots x out)
  *   linear_dx: dx[r]  = dy[r] w[e(r)]                  (slots x in)

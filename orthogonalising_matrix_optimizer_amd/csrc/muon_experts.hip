@@ -21,11 +21,11 @@
 // bf16 operands whose rows start at 16 bytes and hold whole 16-byte pieces go
 // straight to LDS (LDS-DMA), which zeroes what a lane points past the buffer's
 // end.  All others are loaded into registers and checked there.  fp32 operands
-// are split there into three bf16 terms h + m + l, each the rounding of what the
-// terms before leave (24 bits in all), and six of the nine products of terms
-// are summed, the largest left out being m l with at most 2^-24 of h h: an fp32
+// are split there into three bf16 terms, each the rounding of what the terms before
+// leave (24 bits in all), and six of the nine products of terms are summed, the largest
+// left out being that of the second and third with at most 2^-24 of the first's: an fp32
 // product in six bf16 matrix instructions, which together run at 2.7 times the rate
-// of the fp32 matrix instruction.
+// of the fp32 matrix instruction (which keeps subnormal bf16 operands and fp32 sums).
 //
 // The four results that the matrix instruction leaves in consecutive registers
 // are rows of its first operand, which is that of the output's columns.  Its 32
@@ -196,17 +196,20 @@ __device__ __forceinline__ int across_off(int k, int p) {
   return k * (R * 2) + (((p >> 3) ^ turn<R>(k)) << 4) + (p & 7) * 2;
 }
 
-// fp32 -> three bf16 terms of eight elements.
+// fp32 -> three bf16 terms of eight elements, v = h + m 2^-8 + l 2^-16.  The scales keep
+// m and l among the numbers that bf16 has: unscaled, the last bits of what is below 2^-110
+// would be lost (a sixteenth of a number of 2^-130).  They cost two multiplications an element: 1001 x 2
+// slots, 333 -> 777 with gradients 59 us without, 63 with; 16384 x 2, 2048 -> 1024 2590 | 2680.
 __device__ __forceinline__ void split8(const float* v, u32x4_t& h, u32x4_t& m, u32x4_t& l) {
-  h = narrow8(v);
   float w[8], r[8];
+  h = narrow8(v);
   widen8(h, w);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] = v[e] - w[e];
+  for (int e = 0; e < 8; ++e) r[e] = (v[e] - w[e]) * 256.f;
   m = narrow8(r);
   widen8(m, w);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] -= w[e];
+  for (int e = 0; e < 8; ++e) r[e] = (r[e] - w[e]) * 256.f;
   l = narrow8(r);
 }
 
@@ -581,9 +584,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
       cols.plan({w, a.ldc * es, nullptr, 0, depth, a.cols, tile.c0}, wave, lane);
   }
 
-  // fp32: the products of the first terms have sums of their own, so that the five
-  // smaller ones of each step add nothing to their rounding
-  constexpr int SETS = PL == 1 ? 1 : 2;
+  // fp32: the products of each scale have sums of their own, so that the smaller ones add
+  // nothing to the rounding of the largest
+  constexpr int SETS = PL;
   f32x16_t acc[SETS][FN][FM];
 #pragma unroll
   for (int n = 0; n < SETS; ++n)
@@ -635,7 +638,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
         for (int i = 0; i < FN; ++i)
 #pragma unroll
           for (int j = 0; j < FM; ++j)
-            acc[sum ? 1 : 0][i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g.c[p][i], g.r[o][j], acc[sum ? 1 : 0][i][j], 0, 0, 0);
+            acc[sum][i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g.c[p][i], g.r[o][j], acc[sum][i][j], 0, 0, 0);
       }
   };
   if (stages) {
@@ -678,10 +681,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
   }
 
   if constexpr (SETS > 1) {
+    // where the first terms' sum is an infinity or NaN that is the result: an operand that
+    // is one has no further terms, and the others' sums say nothing more
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
-      for (int j = 0; j < FM; ++j) acc[0][i][j] += acc[SETS - 1][i][j];
+      for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const float big = acc[0][i][j][q], rest = (acc[SETS > 1 ? 1 : 0][i][j][q] + acc[SETS > 2 ? 2 : 0][i][j][q] * 0x1p-8f) * 0x1p-8f;
+          acc[0][i][j][q] = fabsf(big) < __builtin_inff() ? big + rest : big;
+        }
   }
   const int most = OP >= kExpertDw ? a.rows : tile.hi - tile.lo;
   T* out = static_cast<T*>(a.out) + (OP == kExpertPart ? tile.part * a.ostride : OP == kExpertDw ? tile.e * a.ostride : tile.lo * a.ldo);

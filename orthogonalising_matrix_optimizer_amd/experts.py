@@ -255,7 +255,8 @@ def expert_linear(x: torch.Tensor, w: torch.Tensor, plan: ExpertPlan, gather: bo
     """Each row of x times its expert's matrix: x[r] w[e]^T for w [experts, out,
     in], [slots, out] in x's type or `dtype`.  x [slots, in] is in the order of the
     plan's rows, or with `gather` [tokens, in], one row a token.  Rows that
-    belong to no slot are left as they were (uninitialised without `out`)."""
+    belong to no slot are left as they were (uninitialised without `out`).  fp32
+    operands keep their 24 bits; one of 3.3895e38 or more counts as an infinity."""
     _not_recorded(x)
     _not_recorded(w)
     dev = _plan_of(plan)

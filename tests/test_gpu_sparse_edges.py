@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import orthogonalising_matrix_optimizer_amd as mo
+from oracle import sparse_oracle as so
 from orthogonalising_matrix_optimizer_amd import experts as ex
 from tests.gpu_helpers import announce, host
 
@@ -115,3 +116,67 @@ def test_ids_and_choices_of_any_row_pitch():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, mo.embedding(batch[:, :-1].contiguous(), w))
+
+
+def products_in_float64(x, w, dy, offsets):
+    return so.linear(x, w, offsets), *so.linear_grad(dy, w, x, offsets)
+
+
+@pytest.mark.parametrize("power", [0, 60, 100, 105, 110, 112, 116, 118, 120, 124, 126, 130, 137, 149])
+@pytest.mark.parametrize("cols,outs,rows", [(1, 3, 5), (2, 40, 9), (77, 129, 150), (64, 64, 700)])
+def test_fp32_products_of_small_numbers(cols, outs, rows, power):
+    """Operands of 2^-power times operands of order 1, subnormal ones among them, in each place.
+
+    The bound of the products of fp32, (6 K + 2) 2u 1.02 S, and for sums among the subnormal numbers, of which
+    one step is 2^-149: a step for each of K first terms' products, 2^-8 of one for each of 2 K and 2^-16 for each
+    of 3 K others, and one each for the sums' addition and its two products: (2 K + 4) 2^-149 in all."""
+    announce(f"fp32 products of 2^-{power}: {rows} rows, {cols} -> {outs}")
+    g = torch.Generator().manual_seed(power + cols)
+    plan = mo.expert_plan((torch.arange(rows, dtype=torch.int32) % 3).reshape(-1, 1).cuda(), 3)
+    offsets = plan.offsets.cpu().numpy()
+
+    def rand(*size, small=False):
+        t = torch.randn(*size, generator=g).double() * (2.0 ** -power if small else 1.0)
+        return t.float().cuda()
+    for which in range(3):
+        x, w, dy = (rand(*s, small=i == which) for i, s in enumerate(((rows, cols), (3, outs, cols), (rows, outs))))
+        got = (mo.expert_linear(x, w, plan), *mo.expert_linear_grad(dy, w, x, plan))
+        xh, wh, dh = wide(x), wide(w).reshape(3, outs, cols), wide(dy)
+        want = products_in_float64(xh, wh, dh, offsets)
+        size = products_in_float64(np.abs(xh), np.abs(wh), np.abs(dh), offsets)
+        depth = (cols, outs, np.diff(offsets)[:, None, None])
+        for a, b, s, k in zip(got, want, size, depth):
+            tol = (6 * k + 2) * 2 * U * 1.02 * s + U * np.abs(b) + (2 * k + 4) * 2.0 ** -149
+            assert (np.abs(wide(a) - b) <= tol).all(), (which, np.max(np.abs(wide(a) - b) / tol))
+
+
+@pytest.mark.parametrize("cols,outs", [(8, 40), (77, 129)])
+def test_fp32_products_of_infinities_and_large_numbers(cols, outs):
+    """An infinity's products are infinities, NaN with zeros and with each other's opposites; no other result changes."""
+    g = torch.Generator().manual_seed(cols)
+    plan = mo.expert_plan(torch.zeros(90, 1, dtype=torch.int32).cuda(), 1)
+    x, w = torch.randn(90, cols, generator=g), torch.randn(1, outs, cols, generator=g)
+    x[3, 2], x[5, 0], x[7, 1], x[7, 3], x[9, 4] = np.inf, -np.inf, np.inf, -np.inf, np.nan
+    w[0, 6, 2] = 0.0
+    x[11], x[12, 5] = 1e38, 3.4e38                            # sums that overflow, and a number that counts as infinite
+    w[0, 8, 1] = np.inf
+    got = mo.expert_linear(x.cuda(), w.cuda(), plan).cpu()
+    x[12, 5] = np.inf
+    want = x.double() @ w[0].double().t()
+    plain = [r for r in range(90) if r not in (3, 5, 7, 9, 11, 12)]
+    for r in (3, 5, 7, 9, 12):
+        assert torch.equal(got[r].isnan(), want[r].isnan()) and torch.equal(got[r].isinf(), want[r].isinf()), r
+        ok = ~want[r].isnan()
+        assert torch.equal(got[r][ok].double(), want[r][ok]), r
+    assert got[3, 6].isnan() and got[7].isnan().sum() >= outs // 4
+    assert not got[11][want[11].abs() > 1e39].isfinite().any()
+    s = x.double().abs() @ w[0].double().abs().t()
+    cols_ok = [c for c in range(outs) if c != 8]
+    err = (got.double() - want).abs()[plain][:, cols_ok]
+    assert (err <= ((6 * cols + 2) * 2.04 * U * s + U * want.abs())[plain][:, cols_ok]).all()
+    assert torch.equal(got[plain][:, 8].double(), want[plain][:, 8])
+    big = (torch.rand(90, cols, generator=g) + 1) * 1e38     # 1e38 .. 2e38, sums below 2^127
+    small = torch.randn(1, outs, cols, generator=g) / (8 * cols)
+    got = mo.expert_linear(big.cuda(), small.cuda(), plan).cpu()
+    want, s = big.double() @ small[0].double().t(), big.double() @ small[0].double().abs().t()
+    assert ((got.double() - want).abs() <= (6 * cols + 2) * 2.04 * U * s + U * want.abs()).all()
