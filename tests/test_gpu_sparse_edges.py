@@ -180,3 +180,30 @@ def test_fp32_products_of_infinities_and_large_numbers(cols, outs):
     got = mo.expert_linear(big.cuda(), small.cuda(), plan).cpu()
     want, s = big.double() @ small[0].double().t(), big.double() @ small[0].double().abs().t()
     assert ((got.double() - want).abs() <= (6 * cols + 2) * 2.04 * U * s + U * want.abs()).all()
+
+
+@pytest.mark.parametrize("dtype,off", [(BF16, 8), (BF16, 3), (F32, 4), (F32, 1)])
+def test_tokens_rows_that_span_gigabytes(dtype, off):
+    """Gathered rows between 2 GiB and what a product addresses, and past it, where they are sorted first:
+    the same bits as from rows that lie together."""
+    pitch = (1 << 21) // dtype.itemsize                       # 2 MiB from row to row
+    most = mo._lib.GATHER_BYTES >> 21                         # rows of as much
+    g = torch.Generator().manual_seed(off)
+    room = torch.empty((most + 40) * pitch, dtype=dtype, device="cuda")
+    for rows in (most, most + 1, most + 40):
+        announce(f"{rows} rows 2 MiB apart, {dtype}, offset {off}")
+        x = room.as_strided((rows, 72), (pitch, 1), off)
+        near = torch.randn(rows, 72, generator=g).to(dtype).cuda()
+        x.copy_(near)
+        choice = torch.full((rows, 2), -1, dtype=torch.int32)
+        choice[rows // 2 + 100:] = torch.randint(0, 3, (rows - rows // 2 - 100, 2), generator=g, dtype=torch.int32)
+        plan = mo.expert_plan(choice.cuda(), 3)
+        n = int(plan.offsets[-1])
+        assert n > 1500 and int(plan.tokens[:n].min()) * pitch * dtype.itemsize > 1 << 31
+        w, dy = torch.randn(3, 56, 72, generator=g).to(dtype).cuda(), torch.randn(2 * rows, 56, generator=g).to(dtype).cuda()
+        assert torch.equal(mo.expert_linear(x, w, plan, gather=True)[:n], mo.expert_linear(near, w, plan, gather=True)[:n])
+        a, b = (mo.expert_linear_grad(dy, None, t, plan, gather=True)[1] for t in (x, near))
+        assert torch.equal(a, b) and (a != 0).all()
+        assert torch.equal(mo.expert_gather(x, plan)[:n], near[plan.tokens[:n].long()])
+        ids = torch.randint(rows // 2, rows, (300,), generator=g).cuda()
+        assert torch.equal(mo.embedding(ids, x), near[ids])
