@@ -1,5 +1,6 @@
-// Device helpers shared by the 4-bit operators: random numbers, block scales and
-// codes, and the lookup of a block's matrix in a grouped launch.
+// Device helpers shared by the 4-bit operators and those of experts and embedding: random
+// numbers, block scales and codes, the lookup of a block's matrix in a grouped launch,
+// and rows of any alignment.
 #pragma once
 #include "muon_mx.h"
 
@@ -17,6 +18,12 @@ template <class T>
 __device__ __forceinline__ const GAS T* glb(const T* p) { return (const GAS T*)(p); }
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Lanes below this one in a mask.
+__device__ __forceinline__ int below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
+}
 
 // Scale byte of a block from the bits of its largest magnitude (fp32), and the
 // power of two itself as fp32 bits (255: the block holds an infinity or NaN).

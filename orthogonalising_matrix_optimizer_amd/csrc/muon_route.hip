@@ -42,12 +42,6 @@ __device__ __forceinline__ uint64_t peers_of(int digit, bool in) {
   return same;
 }
 
-__device__ __forceinline__ int below(uint64_t mask) {
-  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
-                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
-}
-
-// One pass over the digit at `shift`; SELF: the blocks count for themselves.
 template <int BITS>
 struct SortShared {
   uint16_t count[kSortWaves][1 << BITS];   // a wave's, then the earlier waves'
@@ -84,6 +78,7 @@ __device__ __forceinline__ void scan_bins(SortShared<BITS>& sh, int t) {
   __syncthreads();
 }
 
+// One pass over the digit at `shift`; SELF: the blocks count for themselves.
 template <int BITS, int EACH, bool SELF>
 __device__ __forceinline__ void sort_pass(const SortArgs& a, int pass, SortShared<BITS>& sh) {
   constexpr int BINS = 1 << BITS, SPAN = kSortThreads * EACH;
@@ -413,16 +408,12 @@ hipError_t with_width(int experts, F&& f) {
   if (experts <= 256) return f(std::integral_constant<int, 4>{});
   return f(std::integral_constant<int, 8>{});
 }
-template <class F>
-hipError_t with_type(int dt, F&& f) {
-  return dt == kBF16 ? f(uint16_t{}) : f(float{});
-}
 
 }  // namespace
 
 hipError_t launch_sort(const SortArgs& a, hipStream_t s) {
   const bool wide = sort_bits(key_bits(a.limit)) == kSortWide;
-  if (sort_each(a.n) == 1)
+  if (sort_each(a.n, a.limit) == 1)
     return wide ? launch_sort_of<kSortWide, 1>(a, s) : launch_sort_of<kSortBits, 1>(a, s);
   return wide ? launch_sort_of<kSortWide, 4>(a, s) : launch_sort_of<kSortBits, 4>(a, s);
 }

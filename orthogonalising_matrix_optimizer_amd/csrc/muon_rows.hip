@@ -32,12 +32,6 @@ __device__ __forceinline__ void store_cols(T* row, int c, int cols, const float*
   }
 }
 
-// Lanes below this one in a mask.
-__device__ __forceinline__ int below(uint64_t mask) {
-  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
-                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
-}
-
 __device__ __forceinline__ int64_t id_at(const void* ids, int bytes, int i) {
   return bytes == 8 ? glb(static_cast<const int64_t*>(ids))[i]
                     : static_cast<int64_t>(glb(static_cast<const int32_t*>(ids))[i]);
@@ -392,11 +386,6 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_grad(CombineArgs a) {
     dot = lanes_sum(dot);
     if (here >> lane & 1) a.dgates[first + lane] = dot;
   }
-}
-
-template <class F>
-hipError_t with_type(int dt, F&& f) {
-  return dt == kBF16 ? f(uint16_t{}) : f(float{});
 }
 
 unsigned blocks_of(int64_t items, int64_t per) { return static_cast<unsigned>((items + per - 1) / per); }

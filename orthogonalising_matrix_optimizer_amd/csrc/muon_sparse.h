@@ -8,7 +8,13 @@
 
 namespace muon {
 
-// ---- stable counting sort (muon_sort.hip)
+// Calls f with an element of a type.
+template <class F>
+hipError_t with_type(int dt, F&& f) {
+  return dt == kBF16 ? f(uint16_t{}) : f(float{});
+}
+
+// ---- stable counting sort (muon_route.hip)
 //
 // Sorts positions 0 .. n-1 by an integer key, by position among equal keys, in
 // passes of kSortBits (or kSortWide) bits, the lowest first.
@@ -26,8 +32,14 @@ inline int key_bits(int64_t limit) {
 inline int sort_bits(int bits) {
   return bits <= kSortBits || (bits > kSortWide && bits <= 2 * kSortBits) ? kSortBits : kSortWide;
 }
-// positions a thread takes: more where the blocks' counts would be many
-inline int sort_each(int64_t n) { return n <= (int64_t(1) << 20) ? 1 : 4; }
+// Positions a thread takes: more where the blocks' counts, which every block of a pass reads,
+// would be many.  us with 1 | 4, of 64 experts' slots (8 bits): 131072 11 | 15, 262144 14 | 16,
+// 524288 25 | 18, 1048576 63 | 22; of 512 experts' (10 bits): 98304 21 | 19, 131072 25 | 19, 262144
+// 39 | 22, 1048576 260 | 38; a table's gradient of 50257 ids (two passes of 8): 262144 72 | 81,
+// 524288 123 | 114, 1048576 255 | 179.
+inline int sort_each(int64_t n, int64_t limit) {
+  return n <= (int64_t(1) << (sort_bits(key_bits(limit)) == kSortBits ? 18 : 17)) ? 1 : 4;
+}
 
 struct SortArgs {
   const void* ids;      // n integers of id_bytes (of the first pass)
@@ -96,7 +108,7 @@ hipError_t launch_embedding(const EmbedArgs& a, int dt, hipStream_t s);
 // Sums of dy's rows over runs of equal sorted keys.  A wave takes `chunk` consecutive
 // sorted positions; a run inside them is written at once, one that crosses their edges
 // goes to `part` (two rows a chunk) and is joined by a second launch.
-constexpr int kEmbedZeroRows = 64;   // rows of dw that a wave looks over for zeroing
+constexpr int kEmbedZeroRows = 64;   // rows of dw that a wave looks over for zeroing, one a lane
 struct EmbedGradArgs {
   const void* dy;
   const int32_t* key;     // sorted ids (the last ones `rows`: no gradient)
@@ -109,7 +121,9 @@ struct EmbedGradArgs {
   int32_t chunk, chunks;  // sorted positions a wave sums, and how many such chunks
   int32_t ldp;            // floats from one row of part to the next, a multiple of 8
 };
-// Without a sort, for few tokens (key, pos, part and the chunks are not used).
+// Without a sort, for few tokens (key, pos, part and the chunks are not used).  us without |
+// with a sort, of 256 tokens: 333 rows of 77 10 | 16, 4096 of 1024 11 | 38, 50257 of 768 30 | 40,
+// 50257 of 2560 121 | 109; of 512 (with masks for 1024): 18 | 16, 24 | 39, 77 | 40, 197 | 114.
 constexpr int kFewTokens = 256;
 hipError_t launch_embedding_few(const EmbedGradArgs& a, const void* ids, int id_bytes, int dt, int odt, hipStream_t s);
 hipError_t launch_embedding_grad(const EmbedGradArgs& a, int dt, int odt, hipStream_t s);

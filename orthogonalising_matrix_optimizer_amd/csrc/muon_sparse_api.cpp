@@ -98,12 +98,12 @@ int check_workspace(std::vector<Span>& v, void* ws, size_t have, size_t need) {
 
 // ---- sort
 
-int64_t sort_blocks(int64_t n) { return ceil_div(n, kSortThreads * sort_each(n)); }
+int64_t sort_blocks(int64_t n, int64_t limit) { return ceil_div(n, kSortThreads * sort_each(n, limit)); }
 int sort_passes(int64_t limit) { return int(ceil_div(key_bits(limit), sort_bits(key_bits(limit)))); }
 
 // Bytes of a sort's counts.
 size_t count_bytes(int64_t n, int64_t limit) {
-  const int64_t blocks = sort_blocks(n);
+  const int64_t blocks = sort_blocks(n, limit);
   return blocks <= kSortSelf ? 0 : size_t(blocks) * 4 << sort_bits(key_bits(limit));
 }
 
@@ -199,9 +199,9 @@ int run_products(ExpertArgs a, int op, int dt, int odt, bool aligned, void* stre
 // of `chunk` rows have fp32 results of their own that a second launch sums in order.
 // A stage of 64 rows takes about 0.8 us, the second launch 6 us, a 64 x 64 tile of a
 // part 0.011 us to write and read again; of the two the sum is least where both are
-// alike.  us of a call, whole | split: 2 experts of 2048 rows, 256 x 128: 22 | 13 (fp32 57 |
-// 16); 1 of 16384, 128 x 128: 182 | 23; 8 of 2048, 512 x 256: 29 | 26, and, left whole
-// by the rule, 8 of 2048, 256 x 1024: 34 | 39, 16 of 512, 256 x 256: 9.5 | 18.
+// alike.  us of a call that gathers, whole | split: 2 experts of 2048 rows, 256 x 128: 22 | 12
+// (fp32 62 | 16); 1 of 16384, 128 x 128: 181 | 17; 8 of 2048, 512 x 256: 29 | 25 to 34, and,
+// left whole by the rule, 8 of 2048, 256 x 1024: 34 | 39, 16 of 512, 256 x 256: 9.3 | 17.
 struct Split {
   int64_t chunk = 0, parts = 0, ld = 0;
   size_t bytes = 0;

@@ -207,3 +207,21 @@ def test_tokens_rows_that_span_gigabytes(dtype, off):
         assert torch.equal(mo.expert_gather(x, plan)[:n], near[plan.tokens[:n].long()])
         ids = torch.randint(rows // 2, rows, (300,), generator=g).cuda()
         assert torch.equal(mo.embedding(ids, x), near[ids])
+
+
+@pytest.mark.parametrize("experts,slots", [(64, 1 << 18), (64, (1 << 18) + 1), (512, 1 << 17), (512, (1 << 17) + 1),
+                                           (512, (1 << 18) + 4097)])
+def test_plans_around_the_sorts_borders(experts, slots):
+    """One position a thread and four, in keys of 8 and of 10 bits."""
+    announce(f"plan {slots} of {experts}")
+    g = torch.Generator().manual_seed(slots)
+    choice = torch.randint(-1, experts + 1, (slots, 1), generator=g, dtype=torch.int32)
+    plan = mo.expert_plan(choice.cuda(), experts)
+    flat = choice.reshape(-1).long()
+    key = torch.where((flat >= 0) & (flat < experts), flat, experts)
+    order, n = torch.argsort(key, stable=True), int((key < experts).sum())
+    assert torch.equal(plan.offsets.cpu().long(), torch.cumsum(torch.bincount(key + 1, minlength=experts + 2), 0)[:experts + 1])
+    assert torch.equal(plan.tokens.cpu()[:n].long(), order[:n]) and (plan.tokens[n:] == -1).all()
+    place = torch.full((slots,), -1, dtype=torch.int64)
+    place[order[:n]] = torch.arange(n)
+    assert torch.equal(plan.place.cpu().reshape(-1).long(), place)
