@@ -209,9 +209,7 @@ def route_grad(dgates: torch.Tensor, logits: torch.Tensor, routing: Routing) -> 
     both contiguous, and expert_plan's plan of them."""
     if not isinstance(routing, Routing) or type(routing.plan) is not ExpertPlan:
         raise ValueError("routing is a Routing with an ExpertPlan")
-    _not_recorded(dgates)
-    _not_recorded(logits)
-    _not_recorded(routing.gates)
+    _not_recorded(dgates, logits, routing.gates)
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits are a 2-D tensor [tokens, experts]")
     dev = _gpu(logits.device)
@@ -257,8 +255,7 @@ def expert_linear(x: torch.Tensor, w: torch.Tensor, plan: ExpertPlan, gather: bo
     plan's rows, or with `gather` [tokens, in], one row a token.  Rows that
     belong to no slot are left as they were (uninitialised without `out`).  fp32
     operands keep their 24 bits; one of 3.3895e38 or more counts as an infinity."""
-    _not_recorded(x)
-    _not_recorded(w)
+    _not_recorded(x, w)
     dev = _plan_of(plan)
     wm = _stack(w, dev)
     x, xm, gather = _sorted_rows(x, plan, gather, dev)
@@ -281,10 +278,7 @@ def expert_linear_grad(dy: torch.Tensor, w: Optional[torch.Tensor], x: Optional[
     out, in] goes to a new tensor of grad_dtype or to `out` (added to it with
     `accumulate`); list(dw) are gradients for Muon.step.  Without w there is no
     dx, without x no dw."""
-    _not_recorded(dy)
-    _not_recorded(w)
-    _not_recorded(x)
-    _not_recorded(out)
+    _not_recorded(dy, w, x, out)
     dev = _plan_of(plan)
     dm = _rows_mat(dy, plan.slots, dev, "dy")
     dx = dw = None
@@ -328,8 +322,7 @@ def expert_combine(y: torch.Tensor, plan: ExpertPlan, gates: Optional[torch.Tens
     """The rows y [slots, cols] of each token's slots summed, each times its gate
     [tokens, k] (fp32; None: ones, the gradient of gathered rows): [tokens,
     cols] in y's type or `dtype`, zeros for a token without slots."""
-    _not_recorded(y)
-    _not_recorded(gates)
+    _not_recorded(y, gates)
     dev = _plan_of(plan)
     ym = _rows_mat(y, plan.slots, dev, "y")
     g = None if gates is None else _per_slot(gates, (plan.n_tokens, plan.k), dev, "gates")
@@ -345,9 +338,7 @@ def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan,
     """Gradients of expert_combine: (dy [slots, cols] in dout's type, dgates
     [tokens, k] in fp32, 0 for dropped slots).  Rows of dy that belong to no
     slot are uninitialised."""
-    _not_recorded(dout)
-    _not_recorded(y)
-    _not_recorded(gates)
+    _not_recorded(dout, y, gates)
     dev = _plan_of(plan)
     dm = _rows_mat(dout, plan.n_tokens, dev, "dout")
     ym = _rows_mat(y, plan.slots, dev, "y")

@@ -171,15 +171,17 @@ def _rows_of(t: torch.Tensor) -> torch.Tensor:
         raise ValueError("the leading dimensions must be one run of evenly spaced rows") from None
 
 
-def _not_recorded(t: torch.Tensor) -> None:
-    """Refuses a tensor whose gradient or tangent autograd would look for in the result."""
-    if isinstance(t, torch.Tensor):
-        if t.requires_grad and torch.is_grad_enabled():
+def _not_recorded(*ts) -> None:
+    """Refuses tensors whose gradient or tangent autograd would look for in the result."""
+    for t in ts:
+        if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
             raise ValueError("this operator records nothing for autograd: call it under torch.no_grad() or in an "
                              "autograd.Function, or give t.detach()")
-        if _forward_ad._current_level >= 0 and _forward_ad.unpack_dual(t).tangent is not None:
-            raise ValueError("this operator records nothing for autograd's forward mode: call it in an "
-                             "autograd.Function with a jvp, or give unpack_dual(t).primal")
+    if _forward_ad._current_level >= 0:
+        for t in ts:
+            if isinstance(t, torch.Tensor) and _forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("this operator records nothing for autograd's forward mode: call it in an "
+                                 "autograd.Function with a jvp, or give unpack_dual(t).primal")
 
 
 def _written(ts) -> None:
