@@ -325,7 +325,8 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 // A wave takes a row of y and dy, in order: these are the bytes that count, and the
-// tokens' rows of dout, read once for each slot, come from the caches.  (A wave for
+// tokens' rows of dout, read once for each slot, come from the last cache (827 MB pass
+// L2, 470 of which are y and dout once).  (A wave for
 // each token, which reads dout once and k rows of y here and there: 16384 tokens x 6
 // x 2048 in bf16 309 us, 203 in this order.)  The row's slot is that of its
 // token's which lies there; rows that are only gathered need none.

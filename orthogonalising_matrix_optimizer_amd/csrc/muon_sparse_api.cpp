@@ -153,7 +153,7 @@ bool spans(const muon_mat& x) {
 // a CU to themselves counts whole.  fwd, us with tiles of 64 | 128 |
 // 256: 4096 slots, 8 experts, 1024 -> 2048: 39 | 38 | 34; 16384 slots, 1024 -> 1024: 62
 // | 52 | 61; 48 slots, 64 experts, 2048 -> 1408: 37 | 32 | 49, 12000: 170 | 128 | 131; fp32
-// 8192 slots, 32 experts, 1024 -> 1024: 150 | 142; 32768, 8, 2048 -> 1024: 1079 | 804.
+// 8192 slots, 32 experts, 1024 -> 1024: 150 | 140; 32768, 8, 2048 -> 1024: 965 | 813.
 int tile_of(const ExpertArgs& a, int op, int dt, bool aligned) {
   if (op == kExpertPart) return 64;
   if (const char* e = std::getenv("MUON_EXPERT_TILE")) {
