@@ -585,8 +585,9 @@ int muon_route_grad(const float* dgates, const muon_mat* logits, const float* ga
  * three bf16 terms each, which hold all of their 24 bits, subnormal ones' too; products
  * of terms that are at most 2^-24 of the whole are left out.  An operand of 2^128 - 2^119
  * (3.3895e38) or more counts as an infinity; infinities and NaN enter sums as in any fp32
- * product.  Where the magnitudes of a sum's terms add up to 2^127 or more it may be an
- * infinity or NaN though the sum itself is smaller.
+ * product (an infinity times a number of 2^-134 or less as times zero).  Where the
+ * magnitudes of a sum's terms add up to 2^127 or more it may be an infinity or NaN
+ * though the sum itself is smaller.
  * Row pitches of operands are at most 2^22 elements (MUON_E_SHAPE).
  *   linear:    out[r] = x[r] w[e(r)]^T                 (slots x out)
  *   linear_dx: dx[r]  = dy[r] w[e(r)]                  (slots x in)
