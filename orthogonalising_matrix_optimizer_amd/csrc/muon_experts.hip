@@ -198,8 +198,9 @@ __device__ __forceinline__ int across_off(int k, int p) {
 
 // fp32 -> three bf16 terms of eight elements, v = h + m 2^-8 + l 2^-16.  The scales keep
 // m and l among the numbers that bf16 has: unscaled, the last bits of what is below 2^-110
-// would be lost (a sixteenth of a number of 2^-130).  They cost two multiplications an element: 1001 x 2
-// slots, 333 -> 777 with gradients 59 us without, 63 with; 16384 x 2, 2048 -> 1024 2590 | 2680.
+// would be lost (a sixteenth of a number of 2^-130).  They cost two multiplications an
+// element: 1001 x 2 slots, 333 -> 777 with gradients 59 us without, 63 with; 16384 x 2,
+// 2048 -> 1024 2590 | 2680.
 __device__ __forceinline__ void split8(const float* v, u32x4_t& h, u32x4_t& m, u32x4_t& l) {
   float w[8], r[8];
   h = narrow8(v);
@@ -689,7 +690,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_experts(ExpertArgs a) {
       for (int j = 0; j < FM; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-          const float big = acc[0][i][j][q], rest = (acc[SETS > 1 ? 1 : 0][i][j][q] + acc[SETS > 2 ? 2 : 0][i][j][q] * 0x1p-8f) * 0x1p-8f;
+          const float big = acc[0][i][j][q];
+          const float rest = (acc[SETS > 1 ? 1 : 0][i][j][q] + acc[SETS > 2 ? 2 : 0][i][j][q] * 0x1p-8f) * 0x1p-8f;
           acc[0][i][j][q] = fabsf(big) < __builtin_inff() ? big + rest : big;
         }
   }

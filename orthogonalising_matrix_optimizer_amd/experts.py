@@ -104,7 +104,7 @@ def _ids(t: torch.Tensor, dev: Optional[torch.device] = None) -> Tuple[torch.Ten
 
 
 def _per_slot(t: torch.Tensor, plan_shape: Tuple[int, int], dev: torch.device, what: str,
-         dtype: torch.dtype = torch.float32) -> int:
+              dtype: torch.dtype = torch.float32) -> int:
     """The address of a dense tensor (fp32 or of `dtype`) with one number a slot."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev:
         raise ValueError(f"{what} must be a tensor of {dtype} on the operands' device")
@@ -354,8 +354,8 @@ def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan,
 def embedding(ids: torch.Tensor, w: torch.Tensor, scale: float = 1.0,
               out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """scale times the rows of the table w [rows, cols] that ids (int32 or int64,
-    any shape, rows contiguous: tokens[:, :-1], say) name: [*ids.shape, cols] in w's type.  An id that is none of w's
-    rows (-1, say: padding) gives zeros."""
+    any shape, rows contiguous: tokens[:, :-1], say) name: [*ids.shape, cols] in w's
+    type.  An id that is none of w's rows (-1, say: padding) gives zeros."""
     _not_recorded(w)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("the table is a 2-D tensor [rows, cols]")

@@ -15,8 +15,8 @@ the same elements.  Within a list each matrix has its own numbers.
 Nothing here is recorded by autograd.  The gradients are calls of their own
 (mx_linear_grad, dropout on the gradient), made by hand or by the two halves of
 a torch.autograd.Function; mx_linear, mx_linear_grad and dropout refuse a tensor
-that requires a gradient where autograd records.  mx_quantize takes weights
-that require one.
+that requires a gradient where autograd records, and one with a tangent of
+forward mode.  mx_quantize takes weights that require a gradient.
 """
 from __future__ import annotations
 

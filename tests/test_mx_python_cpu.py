@@ -155,3 +155,16 @@ def test_results_written_into_given_tensors_count_as_changes(monkeypatch):
         t = torch.zeros(8, 5)
         mo.mx_matmul(q, w, out=t)
     mo.mx_matmul([q, q], [w, w], out=[t, big[:8, :5]])
+
+
+def test_a_tangent_that_autograd_would_lose_is_refused():
+    """Forward mode's derivatives would be lost as those of backward mode are."""
+    fw = torch.autograd.forward_ad
+    with fw.dual_level():
+        x, dy = (fw.make_dual(torch.zeros(n, c), torch.ones(n, c)) for n, c in ((2, 40), (8, 4)))
+        w, saved = _held(4, 40), mx.MXSaved(_held(40, 8), 0.0, None)
+        for f in (lambda: mo.mx_linear(x, w), lambda: mo.dropout(x, 0.5, 1), lambda: mo.mx_linear_grad(dy, None, saved)):
+            with torch.no_grad(), pytest.raises(ValueError, match="autograd"):
+                f()
+        with pytest.raises(ValueError, match="GPU"):          # without a tangent the next refusal is that of host memory
+            mo.mx_linear(fw.unpack_dual(x).primal, w)
