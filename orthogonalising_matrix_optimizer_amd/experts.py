@@ -36,8 +36,16 @@ class ExpertPlan:
 
     __slots__ = ("buffer", "n_tokens", "k", "experts", "device", "desc")
 
-    def __init__(self, buffer: torch.Tensor, n_tokens: int, k: int, experts: int, device: torch.device):
-        # buffer: place, tokens and offsets, int32
+    def __init__(self, buffer: torch.Tensor, n_tokens: int, k: int, experts: int, device: torch.device,
+                 _own: bool = False):
+        # buffer: place, tokens and offsets, int32 (_own: allocated for them)
+        if not _own:
+            _check_counts(n_tokens, k, experts)
+            n = 2 * n_tokens * k + experts + 1
+            if not isinstance(buffer, torch.Tensor) or buffer.dtype != _I32 or buffer.device != device or \
+                    buffer.dim() != 1 or not buffer.is_contiguous() or buffer.storage_offset() or buffer.numel() < n:
+                raise ValueError(f"a plan of {n_tokens} tokens x {k} and {experts} experts is a tensor of {n} int32 "
+                                 f"on {device}, from its memory's start")
         self.buffer, self.n_tokens, self.k, self.experts, self.device = buffer, n_tokens, k, experts, device
         p, n = buffer.data_ptr(), 4 * n_tokens * k
         self.desc = _SLOTS.pack(p + 2 * n, p + n, p, n_tokens, k, experts)
@@ -84,8 +92,8 @@ def _check_counts(n_tokens: int, k: int, experts: int) -> None:
         raise ValueError(f"1 to {_lib.MAX_EXPERTS} experts, not {experts}")
     if not 1 <= k <= _lib.MAX_K:
         raise ValueError(f"1 to {_lib.MAX_K} experts a token, not {k}")
-    if n_tokens * k > _lib.MAX_SLOTS:
-        raise ValueError(f"{n_tokens} tokens x {k} are more than {_lib.MAX_SLOTS} slots")
+    if not 0 <= n_tokens * k <= _lib.MAX_SLOTS:
+        raise ValueError(f"{n_tokens} tokens x {k} are not 0 to {_lib.MAX_SLOTS} slots")
 
 
 def _ids(t: torch.Tensor, dev: Optional[torch.device] = None) -> Tuple[torch.Tensor, bytes]:
@@ -170,7 +178,7 @@ def expert_plan(experts: torch.Tensor, n_experts: int) -> ExpertPlan:
     n, k = experts.shape
     _check_counts(n, k, n_experts)
     held, ids = _ids(experts)
-    plan = ExpertPlan(_empty((2 * n * k + n_experts + 1,), (1,), dtype=_I32, device=dev), n, k, n_experts, dev)
+    plan = ExpertPlan(_empty((2 * n * k + n_experts + 1,), (1,), dtype=_I32, device=dev), n, k, n_experts, dev, True)
     keep, ws, size = _workspace(int(_lib.load().muon_expert_plan_workspace_bytes(n, k, n_experts)), dev)
     _lib.check(_call("muon_expert_plan", dev, ids, plan.desc, ws, size), "muon_expert_plan")
     return plan
@@ -193,7 +201,7 @@ def route(logits: torch.Tensor, k: int, normalize: bool = False) -> Routing:
     # one allocation: the plan, then the chosen experts and the gates
     m = n * k
     buf = _empty((4 * m + e + 1,), (1,), dtype=_I32, device=dev)
-    plan = ExpertPlan(buf, n, k, e, dev)
+    plan = ExpertPlan(buf, n, k, e, dev, True)
     at = 2 * m + e + 1
     chosen = buf.as_strided((n, k), (k, 1), at)
     gates = buf.view(torch.float32).as_strided((n, k), (k, 1), at + m)

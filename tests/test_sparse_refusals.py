@@ -148,3 +148,20 @@ def test_ids_and_choices_of_any_row_pitch(calls):
     for bad in (batch.t(), batch[:, ::2], batch[:, 1]):       # numbers that are apart, as in a matrix's rows
         with pytest.raises(ValueError, match="contiguous"):
             mo.embedding(bad, torch.zeros(20, 5))
+
+
+def test_a_plan_made_by_hand_has_room_for_its_arrays(calls):
+    """Its arrays' addresses go to the device as they are."""
+    good = torch.zeros(2 * 10 + 4, dtype=torch.int32)
+    for a in ((good[:-1], 5, 2, 3, CPU), (good.long(), 5, 2, 3, CPU), (good.float(), 5, 2, 3, CPU),
+              (torch.zeros(48, dtype=torch.int32)[::2], 5, 2, 3, CPU), (good.reshape(2, 12), 5, 2, 3, CPU), (None, 5, 2, 3, CPU),
+              (torch.zeros(30, dtype=torch.int32)[6:], 5, 2, 3, CPU),
+              (good, 5, 2, 3, torch.device("meta")), (good, 5, 2, 4, CPU), (good, 6, 2, 3, CPU), (good, 5, 0, 3, CPU),
+              (good, 5, 2, 0, CPU), (good, -5, 2, 3, CPU), (good, 5, 65, 3, CPU)):
+        with pytest.raises(ValueError):
+            experts.ExpertPlan(*a)
+    plan = experts.ExpertPlan(good, 5, 2, 3, CPU)
+    mo.expert_combine(torch.zeros(10, 4), plan)
+    made = mo.expert_plan(torch.zeros(5, 2, dtype=torch.int64), 3)
+    assert type(made) is experts.ExpertPlan and made.place.shape == (5, 2) and made.buffer.numel() == 24
+    assert [c[0] for c in calls] == ["muon_expert_combine", "muon_expert_plan"]
